@@ -23,6 +23,9 @@ __all__ = [
     "h2o_cache_view", "h2o_cache_scales", "h2o_sync_check", "h2o_test_wait_limit", "LIB_PATH",
     "KV_FORMATS", "h2o_reset", "h2o_attention_sync_check", "h2o_attention_test_wait_limit",
     "h2o_test_fail_allocations", "h2o_forget_device_state",
+    "H2OPool", "h2o_pool_create", "h2o_pool_destroy", "h2o_pool_view", "h2o_pool_write",
+    "h2o_pool_fork", "h2o_pool_copy", "h2o_pool_free", "h2o_pool_compact", "h2o_pool_attend",
+    "h2o_pool_sync_check",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libh2o.so"
@@ -73,6 +76,16 @@ def load_library() -> ctypes.CDLL:
         "h2o_attention_test_wait_limit": (I, [P]),
         "h2o_forget_device_state": (None, []),
         "h2o_test_fail_allocations": (I, [I]),
+        "h2o_pool_create": (I, [I] * 8 + [ctypes.POINTER(P)]),
+        "h2o_pool_destroy": (None, [P]),
+        "h2o_pool_view": (I, [P, I] + [ctypes.POINTER(P)] * 9),
+        "h2o_pool_write": (I, [P, I, I, P, P, P, I, P, P]),
+        "h2o_pool_fork": (I, [P, I, I, P, P]),
+        "h2o_pool_copy": (I, [P, I, I, P, P]),
+        "h2o_pool_free": (I, [P, I, I, P]),
+        "h2o_pool_compact": (I, [P, I, I, P, I, I]),
+        "h2o_pool_attend": (I, [P, I, I, P, I, P, I, P, P, I]),
+        "h2o_pool_sync_check": (I, [P]),
         "h2o_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -341,3 +354,150 @@ def h2o_test_fail_allocations(n: int) -> None:
 def h2o_forget_device_state() -> None:
     """Drops the library's cached per-device state (after a device reset)."""
     load_library().h2o_forget_device_state()
+
+
+# ---------------------------------------------------------------- paged cache
+class H2OPool:
+    """Owner of one h2o_pool handle: pages of tokens that sequences hold and share.
+
+    Sequences are numbered 0 .. sequences - 1 and empty at first. Sequence lists
+    are CUDA int32 tensors, read on the device; -1 entries are skipped."""
+
+    def __init__(self, handle: int, layers: int, pages: int, page_size: int, heads: int,
+                 head_dim: int, sequences: int, max_pages: int, kv: str):
+        self.handle = handle
+        self.layers, self.pages, self.page_size = layers, pages, page_size
+        self.heads, self.head_dim, self.kv = heads, head_dim, kv
+        self.sequences, self.max_pages, self.capacity = sequences, max_pages, max_pages * page_size
+        self.device = torch.cuda.current_device()
+
+    def close(self):
+        if self.handle:
+            load_library().h2o_pool_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def h2o_pool_create(layers: int, pages: int, page_size: int, heads: int, head_dim: int,
+                    sequences: int, max_pages: int, kv: str = "bf16") -> H2OPool:
+    """Pool of `layers` layers of `pages` pages each; `sequences` sequences of at most
+    `max_pages` pages. kv "bf16", or "fp8" (E4M3 codes with per-token scales)."""
+    _need_cuda()
+    if kv not in KV_FORMATS:
+        raise ValueError(f"kv must be one of {sorted(KV_FORMATS)}")
+    out = ctypes.c_void_p()
+    _check(load_library().h2o_pool_create(layers, pages, page_size, heads, head_dim, sequences,
+                                          max_pages, KV_FORMATS[kv], ctypes.byref(out)))
+    return H2OPool(out.value, layers, pages, page_size, heads, head_dim, sequences, max_pages, kv)
+
+
+def h2o_pool_destroy(pool: H2OPool) -> None:
+    pool.close()
+
+
+def _list_ptr(seqs, name: str = "seqs", n: int | None = None) -> int:
+    if isinstance(seqs, torch.Tensor) and seqs.dim() != 1:
+        raise ValueError(f"{name} must have one dimension, got {tuple(seqs.shape)}")
+    n = len(seqs) if n is None else n
+    return _dev_ptr(seqs, torch.int32, (n,), name)
+
+
+def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
+    """Zero-copy torch views of a pool's arrays (library-owned memory): of one layer, or of
+    all of them with a leading dimension of layers. K and V are bf16, or uint8 E4M3 codes
+    with "kscale" and "vscale" in an "fp8" pool."""
+    ptrs = [ctypes.c_void_p() for _ in range(9)]
+    _check(load_library().h2o_pool_view(pool.handle, layer or 0, *[ctypes.byref(p) for p in ptrs]))
+    lead = (pool.layers,) if layer is None else ()
+    N, H, P, S = pool.pages, pool.heads, pool.page_size, pool.sequences
+    dev = torch.device("cuda", pool.device)
+    mk = lambda p, shape, ts: torch.as_tensor(_DeviceArray(p.value, lead + shape, ts), device=dev)
+    fp8 = pool.kv == "fp8"
+    view = {}
+    for name, p in zip("KV", ptrs):
+        x = mk(p, (N, H, P, pool.head_dim), "|u1" if fp8 else "<i2")
+        view[name] = x if fp8 else x.view(torch.bfloat16)
+    if fp8:
+        view["kscale"], view["vscale"] = (mk(p, (N, H, P), "<f4") for p in ptrs[2:4])
+    view["pos"] = mk(ptrs[4], (N, H, P), "<i4")
+    view["score"] = mk(ptrs[5], (S, H, pool.capacity), "<f4")
+    view["table"] = mk(ptrs[6], (S, pool.max_pages), "<i4")
+    view["meta"] = mk(ptrs[7], (S, 2), "<i4")
+    view["ref"] = mk(ptrs[8], (N,), "<i4")
+    return view
+
+
+def h2o_pool_write(pool: H2OPool, layer: int, seqs, K, V, lens=None, score=None) -> None:
+    """Appends tokens to sequences: bf16 K, V [n, H, T, d], the first lens[i] (CUDA int32 [n];
+    default T) of entry i, with initial scores fp32 [n, H, T] (default 0)."""
+    ps = _list_ptr(seqs)
+    n, T = len(seqs), K.shape[2] if K.dim() == 4 else 0
+    shape = (n, pool.heads, T, pool.head_dim)
+    pk = _dev_ptr(K, torch.bfloat16, shape, "K")
+    pv = _dev_ptr(V, torch.bfloat16, shape, "V")
+    pl = None if lens is None else _dev_ptr(lens, torch.int32, (n,), "lens")
+    pc = None if score is None else _dev_ptr(score, torch.float32, shape[:3], "score")
+    _check(load_library().h2o_pool_write(pool.handle, layer, n, ps, pk, pv, T, pl, pc))
+
+
+def h2o_pool_fork(pool: H2OPool, layer: int, src, dst) -> None:
+    """Makes the empty sequences dst continuations of src that share their whole pages
+    (layer -1: in every layer)."""
+    a, b = _list_ptr(src, "src"), _list_ptr(dst, "dst", len(src))
+    _check(load_library().h2o_pool_fork(pool.handle, layer, len(src), a, b))
+
+
+def h2o_pool_copy(pool: H2OPool, layer: int, src, dst) -> None:
+    """h2o_pool_fork that copies every page instead of sharing the whole ones."""
+    a, b = _list_ptr(src, "src"), _list_ptr(dst, "dst", len(src))
+    _check(load_library().h2o_pool_copy(pool.handle, layer, len(src), a, b))
+
+
+def h2o_pool_free(pool: H2OPool, layer: int, seqs) -> None:
+    """Empties sequences (layer -1: in every layer); pages that nobody holds are free again."""
+    _check(load_library().h2o_pool_free(pool.handle, layer, len(seqs), _list_ptr(seqs)))
+
+
+def h2o_pool_compact(pool: H2OPool, layer: int, seqs, h: int, r: int) -> None:
+    """Keeps the r last tokens and the h others of largest score of every head of each
+    sequence longer than h + r (layer -1: in every layer)."""
+    _check(load_library().h2o_pool_compact(pool.handle, layer, len(seqs), _list_ptr(seqs), h, r))
+
+
+def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=None, lse=None,
+                    accumulate: bool = True):
+    """Attention of one token per sequence, q bf16 [n, q_heads, d], over the tokens of sequence
+    ``prefix`` (shared by the batch; -1: none) and each sequence's own. Returns (out bf16
+    [n, q_heads, d], lse fp32 [n, q_heads]); with ``accumulate`` the probabilities are added to
+    the accumulated scores. Rows of -1 entries are not written."""
+    ps = _list_ptr(seqs)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [n, q_heads, head_dim]")
+    shape = (len(seqs), q.shape[1], pool.head_dim)
+    pq = _dev_ptr(q, torch.bfloat16, shape, "q")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    _check(load_library().h2o_pool_attend(pool.handle, layer, shape[0], ps, prefix, pq, shape[1],
+                                          _dev_ptr(out, torch.bfloat16, shape, "out"),
+                                          _dev_ptr(lse, torch.float32, shape[:2], "lse"),
+                                          int(accumulate)))
+    return out, lse
+
+
+def h2o_pool_sync_check(pool: H2OPool) -> None:
+    """Synchronises the current stream and raises H2O_EDEVICE if a call on the pool reported
+    an error (then cleared)."""
+    _check(load_library().h2o_pool_sync_check(pool.handle))

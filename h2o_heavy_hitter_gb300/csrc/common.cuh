@@ -14,6 +14,8 @@ enum DeviceError : int {
   kErrWaitTimeout = 1,  // an mbarrier wait gave up
   kErrBadState = 2,     // a kernel found inconsistent row metadata
   kErrBadLength = 4,    // a ragged batch's prompt length was outside [0, T_max]
+  kErrNoPages = 8,      // a sequence of a pool was refused: no free page, or longer than its table
+  kErrBadList = 16,     // a pool call's list named a sequence outside the pool, twice, or in use
 };
 
 // Prompt length of `row` (= batch * heads + head) in a prefill launch over
@@ -166,16 +168,16 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // Quantises the values x[0..n) of this thread, part of a token vector spread
 // over the lanes in `mask` (`lanes` of them, a power of two, adjacent): scale =
 // amax / 448 and code = E4M3(x * (448 / amax)), fp32 with one rounding per
-// operation; a zero vector gets scale 0 and zero codes. Writes the codes
-// (n / 2 pairs) and returns the scale.
+// operation; a zero vector (largest magnitude at most `least`) gets scale 0 and
+// zero codes. Writes the codes (n / 2 pairs) and returns the scale.
 template <int N>
 __device__ __forceinline__ float quantize_e4m3(const float* x, unsigned mask, int lanes,
-                                               uint32_t* pairs) {
+                                               uint32_t* pairs, float least = 0.f) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(x[i]));
   for (int off = lanes / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, off));
-  if (amax == 0.f) {
+  if (amax <= least) {
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) pairs[j] = 0u;
     return 0.f;

@@ -20,11 +20,26 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 
 namespace {
 
 thread_local std::string g_error;
+
+int env_int(const char* name) {
+  const char* v = std::getenv(name);
+  return v ? std::atoi(v) : 0;
+}
+
+// Allocation-failure injection (h2o_test_fail_allocations): the next n device
+// allocations of the library throw as an exhausted allocator would.
+std::atomic<int> g_fail_allocs{0};
+
+}  // namespace
+
+namespace h2o {
+namespace host {
 
 int fail(int code, const std::string& msg) {
   g_error = msg;
@@ -37,35 +52,35 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 cudaStream_t current_stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
-int env_int(const char* name) {
-  const char* v = std::getenv(name);
-  return v ? std::atoi(v) : 0;
-}
-
-// Allocation-failure injection (h2o_test_fail_allocations): the next n device
-// allocations of the library throw as an exhausted allocator would.
-std::atomic<int> g_fail_allocs{0};
-
 void* device_alloc(size_t bytes, cudaStream_t s) {
   for (int n = g_fail_allocs.load(); n > 0; n = g_fail_allocs.load())
     if (g_fail_allocs.compare_exchange_weak(n, n - 1)) throw std::bad_alloc();
   return c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, s);
 }
 
-// One device allocation from PyTorch's caching allocator, freed on scope exit.
-struct Scratch {
-  void* p = nullptr;
-  explicit Scratch(size_t bytes, cudaStream_t s) {
-    if (bytes) p = device_alloc(bytes, s);
-  }
-  ~Scratch() {
-    if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
-  }
-  Scratch(const Scratch&) = delete;
-  Scratch& operator=(const Scratch&) = delete;
-};
+void device_free(void* p) { c10::cuda::CUDACachingAllocator::raw_delete(p); }
 
-}  // namespace
+int check_error_word(int32_t* word_dev, cudaStream_t s) {
+  int32_t word = 0;
+  cudaError_t e = cudaMemcpyAsync(&word, word_dev, sizeof(word), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e, "stream synchronise");
+  if (word != 0) {
+    cudaMemsetAsync(word_dev, 0, sizeof(int32_t), s);
+    char buf[160];
+    std::snprintf(buf, sizeof(buf),
+                  "device error word 0x%x (1 = wait timeout, 2 = bad state, 4 = length out of "
+                  "range, 8 = no page, 16 = bad sequence list)",
+                  word);
+    return fail(H2O_EDEVICE, buf);
+  }
+  return H2O_OK;
+}
+
+}  // namespace host
+}  // namespace h2o
+
+using namespace h2o::host;
 
 struct h2o_ctx {
   int layers, batch, heads, d, h, r, k, rows;
@@ -106,8 +121,6 @@ struct h2o_ctx {
 };
 
 namespace {
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Prompt tensors and prefill outputs are read and written by TMA, which needs
 // 16-byte aligned addresses.
@@ -367,22 +380,6 @@ int h2o_prefill_attention_noalloc(const void* Q, const void* K, const void* V, i
   if (e != cudaSuccess) return cuda_fail(e, "prefill forward launch");
   e = h2o::prefill_colsum(Q, K, lse, rows, T, nullptr, 1, head_dim, score, err, s);
   if (e != cudaSuccess) return cuda_fail(e, "prefill column-sum launch");
-  return H2O_OK;
-}
-
-// Reads, then clears, a device error word on `s` after the stream's work so
-// far; H2O_EDEVICE if it was set. Allocates nothing.
-static int check_error_word(int32_t* word_dev, cudaStream_t s) {
-  int32_t word = 0;
-  cudaError_t e = cudaMemcpyAsync(&word, word_dev, sizeof(word), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return cuda_fail(e, "stream synchronise");
-  if (word != 0) {
-    cudaMemsetAsync(word_dev, 0, sizeof(int32_t), s);
-    char buf[128];
-    std::snprintf(buf, sizeof(buf), "device error word 0x%x (1 = wait timeout, 2 = bad state, 4 = length out of range)", word);
-    return fail(H2O_EDEVICE, buf);
-  }
   return H2O_OK;
 }
 

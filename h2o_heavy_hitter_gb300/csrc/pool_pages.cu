@@ -1,0 +1,621 @@
+// Page management of the paged cache: writing tokens into sequences, forking,
+// copying, freeing and compacting them.
+//
+// A page is free when no sequence holds it (ref 0); fresh pages are always the
+// free ones of lowest index, given to the entries of a call's list in order, so
+// a call's result depends on nothing but the pool's state. Every operation
+// that needs pages runs a plan first: one block per layer, one thread per list
+// entry, which checks the entries, counts what each needs, ranks the needs with
+// a block scan, finds that many free pages in one pass over ref, and rewrites
+// the tables. A second kernel then moves the tokens with the whole GPU. The
+// passes over ref read four bytes a page and stop at the last page needed.
+#include <algorithm>
+
+#include "common.cuh"
+#include "pool.h"
+#include "scan.cuh"
+
+namespace h2o {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+static_assert(kPlanThreads >= kPoolMaxList, "one thread per list entry");
+
+__device__ __forceinline__ int pages_of(const PoolView& v, int tokens) {
+  return (tokens + v.page - 1) >> v.shift;
+}
+
+// The view of one layer.
+__device__ __forceinline__ PoolView at_layer(PoolView v, int layer) {
+  const size_t slots = static_cast<size_t>(v.pages) * v.heads * v.page * layer;
+  v.K += slots * v.row_bytes;
+  v.V += slots * v.row_bytes;
+  if (v.kscale) {
+    v.kscale += slots;
+    v.vscale += slots;
+  }
+  v.pos += slots;
+  v.score += static_cast<size_t>(v.seqs) * v.heads * v.cap * layer;
+  v.table += static_cast<size_t>(v.seqs) * v.width * layer;
+  v.meta += static_cast<size_t>(v.seqs) * 2 * layer;
+  v.ref += static_cast<size_t>(v.pages) * layer;
+  return v;
+}
+
+// First slot (of heads * page per page) of a page's head.
+__device__ __forceinline__ size_t slot_base(const PoolView& v, int page, int head) {
+  return (static_cast<size_t>(page) * v.heads + head) << v.shift;
+}
+
+// A list entry: its sequence, or -1 when there is nothing to do. An index
+// outside the pool, or one that an earlier entry names, is reported and skipped.
+// Blockwide: s_list holds the list.
+__device__ __forceinline__ int list_entry(const PoolView& v, const int32_t* list, int n,
+                                          int* s_list) {
+  const int i = threadIdx.x;
+  int seq = i < n ? list[i] : -1;
+  s_list[i] = seq;
+  __syncthreads();
+  if (seq == -1) return -1;
+  bool bad = seq < 0 || seq >= v.seqs;
+  for (int j = 0; j < i; ++j) bad |= s_list[j] == seq;
+  if (bad) {
+    atomicOr(v.err, kErrBadList);
+    seq = -1;
+  }
+  return seq;
+}
+
+// A sequence's length; a state that no call leaves is reported and reads as refused (-1).
+__device__ __forceinline__ int seq_length(const PoolView& v, int seq) {
+  const int len = v.meta[2 * seq];
+  if (len < 0 || len > v.cap) {
+    atomicOr(v.err, kErrBadState);
+    return -1;
+  }
+  return len;
+}
+
+// A page of a sequence, or -1 (reported) when the table holds none of the pool's.
+__device__ __forceinline__ int held_page(const PoolView& v, int seq, int j) {
+  const int p = v.table[static_cast<size_t>(seq) * v.width + j];
+  if (p < 0 || p >= v.pages) {
+    atomicOr(v.err, kErrBadState);
+    return -1;
+  }
+  return p;
+}
+
+__device__ __forceinline__ void drop_page(const PoolView& v, int p) {
+  if (atomicSub(&v.ref[p], 1) <= 0) {  // held by nobody: no call leaves that
+    atomicAdd(&v.ref[p], 1);
+    atomicOr(v.err, kErrBadState);
+  }
+}
+
+// Finds the `total` free pages of lowest index, in order, into fresh[]; returns how many there are.
+// Blockwide.
+__device__ int find_free(const PoolView& v, int total, int32_t* fresh, int* wsum) {
+  int found = 0;
+  for (int base = 0; base < v.pages && found < total; base += 4 * kPlanThreads) {
+    const int p = base + 4 * threadIdx.x;
+    int r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = p + e < v.pages ? v.ref[p + e] : 1;
+    const int mine = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
+    int sum;
+    int at = found + block_exclusive_scan(mine, wsum, &sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r[e] == 0 && at < total) fresh[at++] = p + e;
+    found += sum;
+  }
+  __syncthreads();  // fresh[] is visible to the block
+  return min(found, total);
+}
+
+// Gives every entry its run of fresh pages: returns the run's first index, or
+// -1 when the entry is refused because the free pages run out at it or before.
+// Blockwide; need = 0 for entries without work.
+__device__ int take_pages(const PoolView& v, int need, int32_t* fresh, int* wsum) {
+  int total;
+  const int first = block_exclusive_scan(need, wsum, &total);
+  const int found = total ? find_free(v, total, fresh, wsum) : 0;
+  return first + need <= found ? first : -1;
+}
+
+// ------------------------------------------------------------------ fork, copy
+// plan of an entry: {served, length, -, -}
+__global__ void __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
+                     const int32_t* __restrict__ dst, bool share, int32_t* fresh_all,
+                     int fresh_stride, int32_t* plan_all) {
+  __shared__ int s_list[kPlanThreads], s_src[kPlanThreads], s_len[kPlanThreads],
+      s_first[kPlanThreads];
+  __shared__ int wsum[33];
+  const PoolView v = at_layer(v0, blockIdx.x);
+  int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.x) * fresh_stride;
+  int32_t* plan = plan_all + static_cast<size_t>(blockIdx.x) * n * kPlanInts;
+  const int i = threadIdx.x;
+  int to = list_entry(v, dst, n, s_list);
+  const int from = i < n ? src[i] : -1;
+  int len = 0, next = 0;
+  if (from == -1) to = -1;
+  if (to >= 0) {
+    // a source that is also a destination of this call is empty: both are read before any write
+    if (from < 0 || from >= v.seqs || v.meta[2 * to] != 0) {
+      atomicOr(v.err, kErrBadList);
+      to = -1;
+    } else if ((len = seq_length(v, from)) < 0) {
+      to = -1;
+    } else {
+      next = v.meta[2 * from + 1];
+    }
+  }
+  const int rest = len & (v.page - 1);
+  const int need = to < 0 ? 0 : (share ? rest > 0 : pages_of(v, len));
+  int first = take_pages(v, need, fresh, wsum);
+  if (to >= 0 && first < 0) {
+    atomicOr(v.err, kErrNoPages);
+    to = -1;
+  }
+  s_list[i] = to;
+  s_src[i] = from;
+  s_len[i] = len;
+  s_first[i] = first;
+  __syncthreads();  // every length has been read
+  if (i < n) {
+    plan[i * kPlanInts] = to >= 0;
+    plan[i * kPlanInts + 1] = len;
+  }
+  if (to >= 0) {
+    v.meta[2 * to] = len;
+    v.meta[2 * to + 1] = next;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = warp; e < n; e += kPlanThreads / 32) {
+    const int b = s_list[e];
+    if (b < 0) continue;
+    const int whole = share ? s_len[e] >> v.shift : 0, np = pages_of(v, s_len[e]);
+    for (int j = lane; j < np; j += 32) {
+      int p;
+      if (j < whole) {
+        p = held_page(v, s_src[e], j);
+        if (p >= 0) atomicAdd(&v.ref[p], 1);
+      } else {
+        p = fresh[s_first[e] + j - whole];
+        v.ref[p] = 1;
+      }
+      v.table[static_cast<size_t>(b) * v.width + j] = p;
+    }
+  }
+}
+
+// Copies `n` 16-byte chunks with a warp, four loads in flight per lane.
+__device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src, int n, int lane) {
+  int c = lane;
+  for (; c + 96 < n; c += 128) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = reinterpret_cast<const uint4*>(src)[c + 32 * u];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(dst)[c + 32 * u] = x[u];
+  }
+  for (; c < n; c += 32) reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(src)[c];
+}
+
+// Copies the first `live` slots of a page's head.
+__device__ __forceinline__ void copy_slots(const PoolView& v, int to, int from, int head, int live,
+                                           int lane) {
+  const size_t a = slot_base(v, from, head), b = slot_base(v, to, head);
+  const int chunks = live * (v.row_bytes / 16);
+  warp_copy(v.K + b * v.row_bytes, v.K + a * v.row_bytes, chunks, lane);
+  warp_copy(v.V + b * v.row_bytes, v.V + a * v.row_bytes, chunks, lane);
+  for (int s = lane; s < live; s += 32) v.pos[b + s] = v.pos[a + s];
+  if (v.kscale)
+    for (int s = lane; s < live; s += 32) {
+      v.kscale[b + s] = v.kscale[a + s];
+      v.vscale[b + s] = v.vscale[a + s];
+    }
+}
+
+// One warp per (entry, head, slab of kSlab slots): the slab's scores, and the
+// tokens of its pages that were not shared. A head's slots of a page are
+// contiguous, so a partial page is one run of bytes per head.
+constexpr int kSlab = 256;
+
+__global__ void __launch_bounds__(256)
+    fork_copy_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
+                     const int32_t* __restrict__ dst, bool share,
+                     const int32_t* __restrict__ plan_all) {
+  const PoolView v = at_layer(v0, blockIdx.z);
+  const int32_t* plan = plan_all + static_cast<size_t>(blockIdx.z) * n * kPlanInts;
+  const int lane = threadIdx.x & 31;
+  const int task = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int e = task / v.heads, head = task % v.heads;
+  if (e >= n || !plan[e * kPlanInts]) return;
+  const int len = plan[e * kPlanInts + 1], lo = blockIdx.y * kSlab, hi = min(len, lo + kSlab);
+  if (lo >= hi) return;
+  const int from = src[e], to = dst[e];
+  const float* sa = v.score + (static_cast<size_t>(from) * v.heads + head) * v.cap;
+  float* sb = v.score + (static_cast<size_t>(to) * v.heads + head) * v.cap;
+  for (int s = lo + lane; s < hi; s += 32) sb[s] = sa[s];
+  const int first = share ? max(lo >> v.shift, len >> v.shift) : lo >> v.shift;
+  for (int j = first; j << v.shift < hi; ++j) {
+    const int a = held_page(v, from, j), b = held_page(v, to, j);
+    if (a >= 0 && b >= 0) copy_slots(v, b, a, head, min(v.page, len - (j << v.shift)), lane);
+  }
+}
+
+// ------------------------------------------------------------------ free
+__global__ void __launch_bounds__(kPlanThreads)
+    free_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs) {
+  __shared__ int s_list[kPlanThreads];
+  const PoolView v = at_layer(v0, blockIdx.x);
+  int seq = list_entry(v, seqs, n, s_list);
+  if (seq >= 0 && seq_length(v, seq) < 0) seq = -1;
+  __syncthreads();  // every thread has compared the list
+  s_list[threadIdx.x] = seq;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = warp; e < n; e += kPlanThreads / 32) {
+    const int s = s_list[e];
+    if (s < 0) continue;
+    const int np = pages_of(v, v.meta[2 * s]);
+    for (int j = lane; j < np; j += 32) {
+      const int p = held_page(v, s, j);
+      if (p >= 0) drop_page(v, p);
+      v.table[static_cast<size_t>(s) * v.width + j] = -1;
+    }
+    __syncwarp();
+    if (lane < 2) v.meta[2 * s + lane] = 0;
+  }
+}
+
+// ------------------------------------------------------------------ write
+// plan of an entry: {tokens to write (0: none), first slot, first position, -}
+__global__ void __launch_bounds__(kPlanThreads)
+    write_plan_kernel(PoolView v, int n, const int32_t* __restrict__ seqs, int T,
+                      const int32_t* __restrict__ lens, int32_t* fresh, int32_t* plan) {
+  __shared__ int s_list[kPlanThreads], s_len[kPlanThreads], s_new[kPlanThreads],
+      s_first[kPlanThreads];
+  __shared__ int wsum[33];
+  const int i = threadIdx.x;
+  int seq = list_entry(v, seqs, n, s_list);
+  __syncthreads();
+  int len = 0, next = 0, t = 0;
+  if (seq >= 0) {
+    t = lens ? lens[i] : T;
+    if (t < 0 || t > T) {
+      atomicOr(v.err, kErrBadLength);
+      t = t < 0 ? 0 : T;
+    }
+    len = seq_length(v, seq);
+    if (len < 0) {
+      seq = -1;
+    } else if (len + t > v.cap) {
+      atomicOr(v.err, kErrNoPages);
+      seq = -1;
+    } else {
+      next = v.meta[2 * seq + 1];
+      // a partial last page belongs to its sequence alone
+      if (t > 0 && (len & (v.page - 1))) {
+        const int p = held_page(v, seq, len >> v.shift);
+        if (p < 0 || v.ref[p] != 1) {
+          atomicOr(v.err, kErrBadState);
+          seq = -1;
+        }
+      }
+    }
+  }
+  const int have = pages_of(v, max(len, 0));
+  const int need = seq < 0 ? 0 : pages_of(v, len + t) - have;
+  const int first = take_pages(v, need, fresh, wsum);
+  if (seq >= 0 && first < 0) {
+    atomicOr(v.err, kErrNoPages);
+    seq = -1;
+  }
+  s_list[i] = seq;
+  s_len[i] = have;
+  s_new[i] = need;
+  s_first[i] = first;
+  if (i < n) {
+    plan[i * kPlanInts] = seq >= 0 ? t : 0;
+    plan[i * kPlanInts + 1] = len;
+    plan[i * kPlanInts + 2] = next;
+  }
+  if (seq >= 0) {
+    v.meta[2 * seq] = len + t;
+    v.meta[2 * seq + 1] = next + t;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = warp; e < n; e += kPlanThreads / 32) {
+    const int b = s_list[e];
+    if (b < 0) continue;
+    for (int j = lane; j < s_new[e]; j += 32) {
+      const int p = fresh[s_first[e] + j];
+      v.ref[p] = 1;
+      v.table[static_cast<size_t>(b) * v.width + s_len[e] + j] = p;
+    }
+  }
+}
+
+// One block per (entry, head, kWriteTokens tokens); eight lanes per token, each
+// D / 8 values of its key and of its value.
+constexpr int kWriteTokens = 32;
+// 448 / amax overflows below 448 / FLT_MAX (just above 2^-120): such vectors are stored as zero.
+constexpr float kTinyVector = 0x1p-119f;
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(256)
+    write_kernel(PoolView v, int n, const int32_t* __restrict__ seqs,
+                 const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V, int T,
+                 const float* __restrict__ score, const int32_t* __restrict__ plan) {
+  constexpr int LPT = 8, EPL = D / LPT, NV = EPL / 8;
+  const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
+  const int t = blockIdx.y * kWriteTokens + threadIdx.x / LPT, l = threadIdx.x % LPT;
+  if (t >= plan[e * kPlanInts]) return;  // whole groups of eight lanes leave together
+  const unsigned gmask = 0xffu << (threadIdx.x & 31 & ~(LPT - 1));
+  const int seq = seqs[e], slot = plan[e * kPlanInts + 1] + t;
+  const size_t src = (static_cast<size_t>(blockIdx.x) * T + t) * D + l * EPL;
+  uint4 raw[2][NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    raw[0][j] = *reinterpret_cast<const uint4*>(K + src + 8 * j);
+    raw[1][j] = *reinterpret_cast<const uint4*>(V + src + 8 * j);
+  }
+  const int p = held_page(v, seq, slot >> v.shift);
+  if (p < 0) return;
+  const size_t to = slot_base(v, p, head) + (slot & (v.page - 1));
+  if (l == 0) {
+    v.pos[to] = plan[e * kPlanInts + 2] + t;
+    v.score[(static_cast<size_t>(seq) * v.heads + head) * v.cap + slot] =
+        score ? score[static_cast<size_t>(blockIdx.x) * T + t] : 0.f;
+  }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    uint8_t* dst = (kv ? v.V : v.K) + to * v.row_bytes;
+    if constexpr (F8) {
+      float f[EPL];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) bf16x8_to_f32(raw[kv][j], f + 8 * j);
+      uint32_t pairs[EPL / 2];
+      const float sc = quantize_e4m3<EPL>(f, gmask, LPT, pairs, kTinyVector);
+      if constexpr (EPL == 16)
+        *reinterpret_cast<uint4*>(dst + l * EPL) =
+            make_uint4(pairs[0] | (pairs[1] << 16), pairs[2] | (pairs[3] << 16),
+                       pairs[4] | (pairs[5] << 16), pairs[6] | (pairs[7] << 16));
+      else
+        *reinterpret_cast<uint2*>(dst + l * EPL) =
+            make_uint2(pairs[0] | (pairs[1] << 16), pairs[2] | (pairs[3] << 16));
+      if (l == 0) (kv ? v.vscale : v.kscale)[to] = sc;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        *reinterpret_cast<uint4*>(dst + (l * EPL + 8 * j) * 2) = raw[kv][j];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ compact
+// Scores order as fp32 values do, NaN above all, the two zeros equal.
+__device__ __forceinline__ unsigned score_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const unsigned u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+constexpr int kSelectThreads = 1024;
+
+// Blocks (head, entry, layer) select; the block with head == heads of entry 0
+// plans its layer: plan of an entry = {first fresh page or -1, -, -, -}. The
+// selection reads lengths and scores only and the plan writes neither, so the
+// two run side by side. where[]: slot (page * page size + offset) of each kept
+// token, ascending; kept[]: its score.
+__global__ void __launch_bounds__(kSelectThreads)
+    compact_select_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs, int h, int r,
+                          int32_t* fresh_all, int fresh_stride, int32_t* plan_all,
+                          int32_t* __restrict__ where, float* __restrict__ kept) {
+  const PoolView v = at_layer(v0, blockIdx.z);
+  const int k = h + r, tid = threadIdx.x, nt = blockDim.x;
+  __shared__ int wsum[33];
+  if (blockIdx.x == static_cast<unsigned>(v.heads)) {
+    if (blockIdx.y) return;
+    __shared__ int s_list[kPlanThreads];
+    int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.z) * fresh_stride;
+    int32_t* plan = plan_all + static_cast<size_t>(blockIdx.z) * n * kPlanInts;
+    int seq = list_entry(v, seqs, n, s_list);
+    if (seq >= 0 && seq_length(v, seq) <= k) seq = -1;
+    const int need = seq < 0 ? 0 : pages_of(v, k);
+    const int first = take_pages(v, need, fresh, wsum);
+    if (seq >= 0 && first < 0) atomicOr(v.err, kErrNoPages);
+    if (tid < n) plan[tid * kPlanInts] = seq >= 0 ? first : -1;
+    return;
+  }
+  __shared__ unsigned hist[256];
+  __shared__ unsigned s_prefix;
+  __shared__ int s_rank;
+  const int head = blockIdx.x, e = blockIdx.y, seq = seqs[e];
+  if (seq < 0 || seq >= v.seqs) return;  // the planning block reports it
+  const int T = v.meta[2 * seq];
+  if (T <= k || T > v.cap) return;
+  const float* cs = v.score + (static_cast<size_t>(seq) * v.heads + head) * v.cap;
+  const int n_cand = T - r;
+  // Keep candidate p iff its key is above tau, or equals tau and p is not
+  // among the first `skip` candidates of that key: an MSB-first radix select.
+  unsigned tau = 0xffffffffu;
+  int skip = 0x7fffffff;
+  if (h > 0) {
+    unsigned prefix = 0, mask = 0;
+    int rank = n_cand - h;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < 256; i += nt) hist[i] = 0;
+      __syncthreads();
+      for (int p = tid; p < n_cand; p += nt) {
+        const unsigned u = score_key(cs[p]);
+        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      radix_pick(hist, rank, prefix, shift, &s_prefix, &s_rank);
+      __syncthreads();
+      prefix = s_prefix;
+      rank = s_rank;
+      mask |= 0xffu << shift;
+    }
+    tau = prefix;
+    skip = rank;
+  }
+  const int seg = (T + nt - 1) / nt;
+  const int p0 = min(T, tid * seg), p1 = min(T, p0 + seg);
+  int eq = 0;
+  if (h > 0)
+    for (int p = p0; p < min(p1, n_cand); ++p) eq += score_key(cs[p]) == tau;
+  int dummy;
+  const int eq_base = block_exclusive_scan(eq, wsum, &dummy);
+  auto keep = [&](int p, int& q) -> bool {
+    if (p >= n_cand) return true;
+    if (h == 0) return false;
+    const unsigned u = score_key(cs[p]);
+    return u > tau || (u == tau && q++ >= skip);
+  };
+  int mine = 0;
+  {
+    int q = eq_base;
+    for (int p = p0; p < p1; ++p) mine += keep(p, q);
+  }
+  int s = block_exclusive_scan(mine, wsum, &dummy);
+  const size_t out = ((static_cast<size_t>(blockIdx.z) * n + e) * v.heads + head) * k;
+  int q = eq_base;
+  for (int p = p0; p < p1; ++p)
+    if (keep(p, q)) {
+      const int page = held_page(v, seq, p >> v.shift);
+      where[out + s] = page < 0 ? -1 : (page << v.shift) + (p & (v.page - 1));
+      kept[out + s] = cs[p];
+      ++s;
+    }
+}
+
+// One warp per kGather kept slots of a head: all loads of a lane are in flight
+// before its stores. The first block of an entry also puts the new pages in the table
+// and drops the old ones, which the gather does not read again.
+constexpr int kGather = 4;
+
+template <int ROW>
+__global__ void __launch_bounds__(256)
+    compact_gather_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs, int k,
+                          const int32_t* __restrict__ fresh_all, int fresh_stride,
+                          const int32_t* __restrict__ plan_all, const int32_t* __restrict__ where,
+                          const float* __restrict__ kept) {
+  constexpr int CH = ROW / 16;                     // 16-byte chunks of a vector
+  constexpr int PER = 2 * CH;                      // chunks of a slot: key, then value
+  constexpr int NC = (PER * kGather + 31) / 32;    // chunks per lane
+  const PoolView v = at_layer(v0, blockIdx.z);
+  const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
+  const int first = plan_all[(static_cast<size_t>(blockIdx.z) * n + e) * kPlanInts];
+  if (first < 0) return;
+  const int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.z) * fresh_stride + first;
+  const int seq = seqs[e], lane = threadIdx.x & 31;
+  if (blockIdx.y == 0 && head == 0) {
+    const int old = pages_of(v, v.meta[2 * seq]), now = pages_of(v, k);
+    for (int j = threadIdx.x; j < old; j += blockDim.x) {
+      int32_t* t = v.table + static_cast<size_t>(seq) * v.width + j;
+      const int p = *t;
+      if (p >= 0 && p < v.pages) drop_page(v, p);
+      *t = j < now ? fresh[j] : -1;
+    }
+    for (int j = threadIdx.x; j < now; j += blockDim.x) v.ref[fresh[j]] = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) v.meta[2 * seq] = k;
+  }
+  const size_t in = ((static_cast<size_t>(blockIdx.z) * n + e) * v.heads + head) * k;
+  const int slot0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kGather;
+  uint4 x[NC];
+  uint8_t* dst[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = lane + 32 * i, slot = slot0 + c / PER;
+    dst[i] = nullptr;
+    if (c >= PER * kGather || slot >= k) continue;
+    const int w = where[in + slot];
+    if (w < 0) continue;
+    const int at = c % PER, kv = at >= CH, byte = (kv ? at - CH : at) * 16;
+    const size_t from = slot_base(v, w >> v.shift, head) + (w & (v.page - 1));
+    const size_t to = slot_base(v, fresh[slot >> v.shift], head) + (slot & (v.page - 1));
+    x[i] = *reinterpret_cast<const uint4*>((kv ? v.V : v.K) + from * ROW + byte);
+    dst[i] = (kv ? v.V : v.K) + to * ROW + byte;
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = x[i];
+  const int slot = slot0 + lane;
+  if (lane < kGather && slot < k) {
+    v.score[(static_cast<size_t>(seq) * v.heads + head) * v.cap + slot] = kept[in + slot];
+    const int w = where[in + slot];
+    if (w >= 0) {
+      const size_t from = slot_base(v, w >> v.shift, head) + (w & (v.page - 1));
+      const size_t to = slot_base(v, fresh[slot >> v.shift], head) + (slot & (v.page - 1));
+      v.pos[to] = v.pos[from];
+      if (v.kscale) {
+        v.kscale[to] = v.kscale[from];
+        v.vscale[to] = v.vscale[from];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, const int32_t* dst,
+                      bool share, int32_t* fresh, int32_t* plan, cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  fork_plan_kernel<<<layers, kPlanThreads, 0, stream>>>(v, n, src, dst, share, fresh,
+                                                        share ? n : n * v.width, plan);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid((n * v.heads + 7) / 8, (v.cap + kSlab - 1) / kSlab, layers);
+  fork_copy_kernel<<<grid, 256, 0, stream>>>(v, n, src, dst, share, plan);
+  return cudaGetLastError();
+}
+
+cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
+                      cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  free_kernel<<<layers, kPlanThreads, 0, stream>>>(v, n, seqs);
+  return cudaGetLastError();
+}
+
+cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void* K, const void* V,
+                       int T, const int32_t* lens, const float* score, int32_t* fresh,
+                       int32_t* plan, cudaStream_t stream) {
+  if (n == 0 || T == 0) return cudaSuccess;
+  write_plan_kernel<<<1, kPlanThreads, 0, stream>>>(v, n, seqs, T, lens, fresh, plan);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(n * v.heads, (T + kWriteTokens - 1) / kWriteTokens);
+  auto kk = static_cast<const __nv_bfloat16*>(K);
+  auto vv = static_cast<const __nv_bfloat16*>(V);
+  auto kern = v.d == 128 ? (v.kscale ? write_kernel<128, true> : write_kernel<128, false>)
+                         : (v.kscale ? write_kernel<64, true> : write_kernel<64, false>);
+  kern<<<grid, 256, 0, stream>>>(v, n, seqs, kk, vv, T, score, plan);
+  return cudaGetLastError();
+}
+
+cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* seqs, int h, int r,
+                         int32_t* fresh, int32_t* plan, int32_t* where, float* kept,
+                         cudaStream_t stream) {
+  const int k = h + r;
+  if (n == 0 || k >= v.cap) return cudaSuccess;  // no sequence can be longer than h + r
+  const int stride = n * ((k + v.page - 1) >> v.shift);
+  compact_select_kernel<<<dim3(v.heads + 1, n, layers), kSelectThreads, 0, stream>>>(
+      v, n, seqs, h, r, fresh, stride, plan, where, kept);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(n * v.heads, (k + 8 * kGather - 1) / (8 * kGather), layers);
+  auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>
+              : v.row_bytes == 128 ? compact_gather_kernel<128> : compact_gather_kernel<64>;
+  kern<<<grid, 256, 0, stream>>>(v, n, seqs, k, fresh, stride, plan, where, kept);
+  return cudaGetLastError();
+}
+
+}  // namespace h2o

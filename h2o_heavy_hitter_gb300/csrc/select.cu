@@ -13,41 +13,12 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "scan.cuh"
 
 namespace h2o {
 namespace {
 
 constexpr int kSelectThreads = 1024;
-
-// Block-wide exclusive scan of one int per thread; *total gets the sum.
-__device__ __forceinline__ int block_exclusive_scan(int x, int* wsum, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nw = blockDim.x >> 5;
-  int incl = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    const int v = lane < nw ? wsum[lane] : 0;
-    int vi = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, vi, off);
-      if (lane >= off) vi += y;
-    }
-    wsum[lane] = vi - v;
-    if (lane == 31) wsum[32] = vi;
-  }
-  __syncthreads();
-  const int r = wsum[warp] + incl - x;
-  *total = wsum[32];
-  __syncthreads();
-  return r;
-}
 
 // colsum rows are `stride` floats apart (the padded prompt length); the row's
 // own prompt length T is `stride`, or its batch entry's length in `lens`.
@@ -89,36 +60,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const float* __r
         if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
       }
       __syncthreads();
-      if (tid < 32) {
-        // Warp 0 finds the bin holding the rank-th key: each lane sums eight
-        // bins, a shuffle scan places the lanes, and the one lane whose range
-        // contains the rank walks its eight bins.
-        unsigned c[8];
-        int local = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          c[j] = hist[tid * 8 + j];
-          local += static_cast<int>(c[j]);
-        }
-        int incl = local;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, off);
-          if (tid >= off) incl += y;
-        }
-        int cum = incl - local;
-        if (cum <= rank && rank < incl) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (cum + static_cast<int>(c[j]) > rank) {
-              s_prefix = prefix | (static_cast<unsigned>(tid * 8 + j) << shift);
-              s_rank = rank - cum;
-              break;
-            }
-            cum += static_cast<int>(c[j]);
-          }
-        }
-      }
+      radix_pick(hist, rank, prefix, shift, &s_prefix, &s_rank);
       __syncthreads();
       prefix = s_prefix;
       rank = s_rank;

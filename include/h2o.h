@@ -394,6 +394,146 @@ int h2o_test_wait_limit(h2o_ctx* ctx);
  */
 int h2o_sync_check(h2o_ctx* ctx);
 
+/*
+ * ---- Paged cache -----------------------------------------------------------
+ *
+ * A pool holds sequences of different lengths in pages that sequences can
+ * share, next to the fixed slot cache of h2o_create: for batches whose members
+ * come and go, are forked (samples, beams) or begin with the same long prefix.
+ * The policy is applied by h2o_pool_compact, at the moments the caller picks.
+ *
+ * Per layer, with N pages of `page` tokens, S sequences of at most W pages
+ * (C = W * page tokens) and H key/value heads, a pool holds
+ *   K, V   bf16  [N][H][page][d]  stored keys / values (E4M3 codes, uint8, in
+ *                                 an H2O_KV_FP8 pool, quantised as h2o_create_ex
+ *                                 describes, with fp32 [N][H][page] scales each)
+ *   pos    int32 [N][H][page]     position of the token a slot holds
+ *   score  fp32  [S][H][C]        accumulated score of each slot of a sequence
+ *   table  int32 [S][W]           pages of a sequence in order, -1 behind the last
+ *   meta   int32 [S][2]           {tokens held, next position}
+ *   ref    int32 [N]              sequences that hold a page; 0 = free
+ * Token i of a sequence is in slot i mod page of page table[i / page]. Heads
+ * keep different tokens after a compaction, in ascending order of position.
+ * Scores belong to the sequence, keys, values and positions to the page. Whole
+ * pages may be shared and are never written again; the partial last page of a
+ * sequence is its own. Slots behind a sequence's last token hold no result.
+ *
+ * Lists. `seqs`, `src` and `dst` are device int32 [n], read on the device, n <=
+ * H2O_POOL_MAX_LIST; entries of -1 are skipped (a padded batch). An index
+ * outside the pool, or one named earlier in the list, sets bit 16 (bad list) of
+ * the pool's error word and its entry is skipped; only `src` may name a
+ * sequence twice. The operators that need pages take the free pages of lowest
+ * index, for the entries in order of the list; when they run out, that entry
+ * and all after it are refused, unchanged, with bit 8 (no page). A state
+ * that no call leaves (a length or a page out of range, installed through
+ * h2o_pool_view) sets bit 2 and is not followed. h2o_pool_sync_check reports
+ * the bits as H2O_EDEVICE.
+ *
+ * layer: >= 0, or -1 for all layers at once where that is said. Calls are
+ * enqueued on the current stream, never synchronise, and can be captured in a
+ * CUDA graph; scratch comes from PyTorch's caching allocator. Calls on one
+ * layer of a pool change its state, so they have to be ordered (one stream, or
+ * events); different layers and pools are independent but for the error word.
+ */
+typedef struct h2o_pool h2o_pool;
+
+#define H2O_POOL_MAX_LIST 1024  /* longest sequence list of one call */
+#define H2O_POOL_MAX_HEADS 1024 /* most key/value heads of a pool */
+#define H2O_POOL_MAX_GROUP 32   /* most query heads per key/value head (h2o_pool_attend) */
+
+/*
+ * h2o_pool_create - allocate a pool: every page free, every sequence empty.
+ * layers >= 1, pages >= 1, page_size in {16, 32, 64, 128}, head_dim in {64,
+ * 128}, 1 <= heads <= H2O_POOL_MAX_HEADS, 1 <= sequences <= 2^20, max_pages >=
+ * 1 pages per sequence with max_pages * page_size <= H2O_MAX_T, and pages *
+ * heads * page_size < 2^31. kv_format H2O_KV_BF16 or H2O_KV_FP8.
+ * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA; *out is then NULL.
+ */
+int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_dim, int sequences,
+                    int max_pages, int kv_format, h2o_pool** out);
+
+/* h2o_pool_destroy - wait for the device's work, then free the pool. NULL is
+ * accepted. Not during a stream capture. */
+void h2o_pool_destroy(h2o_pool* pool);
+
+/* h2o_pool_view - device addresses of one layer's arrays; the layers of an
+ * array lie one after the other. Same ownership and rules as h2o_cache_view; a
+ * bf16 pool has no scales (NULL). Any output pointer may be NULL.
+ * Errors: H2O_EINVAL. */
+int h2o_pool_view(h2o_pool* pool, int layer, void** K, void** V, float** k_scale, float** v_scale,
+                  int32_t** pos, float** score, int32_t** table, int32_t** meta, int32_t** ref);
+
+/*
+ * h2o_pool_write - append tokens to sequences of one layer: a prompt, or the
+ * next token(s) of a step. Entry i appends lens[i] tokens (T with lens NULL;
+ * a length outside [0, T] is clamped and sets bit 4) from K, V, device bf16
+ * [n][H][T][d], 16-byte aligned, with initial scores score, device fp32
+ * [n][H][T] (a prompt's column sums from h2o_prefill_attention; NULL: zeros).
+ * They take the sequence's next positions. An entry that would grow beyond
+ * max_pages is refused, unchanged, with bit 8.
+ * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
+ */
+int h2o_pool_write(h2o_pool* pool, int layer, int n, const int32_t* seqs, const void* K,
+                   const void* V, int T, const int32_t* lens, const float* score);
+
+/*
+ * h2o_pool_fork - make the empty sequence dst[i] a continuation of src[i]
+ * (layer -1: in every layer): it shares the whole pages, gets a copy of the
+ * partial last page (at most one fresh page), and its own copy of the scores.
+ * h2o_pool_copy - the same with every page copied: nothing is shared.
+ * A dst that is not empty sets bit 16 and is skipped. Sources are read as they
+ * were before the call. Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
+ */
+int h2o_pool_fork(h2o_pool* pool, int layer, int n, const int32_t* src, const int32_t* dst);
+int h2o_pool_copy(h2o_pool* pool, int layer, int n, const int32_t* src, const int32_t* dst);
+
+/*
+ * h2o_pool_free - empty sequences (layer -1: in every layer): each of their
+ * pages loses a holder, and is free when it had no other. Freeing an empty
+ * sequence does nothing. Errors: H2O_EINVAL, H2O_ECUDA.
+ */
+int h2o_pool_free(h2o_pool* pool, int layer, int n, const int32_t* seqs);
+
+/*
+ * h2o_pool_compact - apply the policy to sequences (layer -1: in every layer):
+ * each head of a sequence longer than h + r keeps the r last tokens and the h
+ * others with the largest (score, position) keys, in ascending order, as
+ * h2o_prefill selects from a prompt; shorter sequences are left as they are.
+ * Scores order as fp32 values, NaN above all. The kept tokens move to
+ * ceil((h + r) / page) fresh pages, so that other holders of the old pages keep
+ * theirs; the old pages then lose a holder. The next position is unchanged.
+ * h >= 0, r >= 0, 1 <= h + r <= H2O_MAX_K.
+ * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
+ */
+int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int h, int r);
+
+/*
+ * h2o_pool_attend - attention of one query token per sequence of a batch over
+ * the tokens of sequence `prefix` (-1: none), which all of them share and which
+ * is read once for the batch, and over each sequence's own tokens. Write a
+ * step's token first if it is to attend to itself.
+ *
+ * For row (i, query head hq), key head hq / (q_heads / H): p = softmax(q . k /
+ * sqrt(d)) over both token lists, out = sum_j p_j v_j (bf16, rounded once from
+ * fp32), lse = the natural log of the softmax's normaliser (fp32; may be NULL).
+ * With accumulate, every probability is added to its slot's accumulated score:
+ * to the sequence's for its own tokens (summed over the head's query group), to
+ * the prefix's, summed over group and batch, for the prefix: the statistic by
+ * which h2o_pool_compact can compact the prefix for all. Sums run in a fixed
+ * order: equal calls give equal bits. Without any token out is 0 and lse is
+ * -infinity. Rows of skipped entries keep what they held.
+ *
+ * q: device bf16 [n][q_heads][d]; out: device bf16 [n][q_heads][d]; lse: device
+ * fp32 [n][q_heads]; q and out 16-byte aligned. q_heads is a multiple of H, at
+ * most H2O_POOL_MAX_GROUP times. `prefix` in `seqs` is a bad entry.
+ * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
+ */
+int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int prefix,
+                    const void* q, int q_heads, void* out, float* lse, int accumulate);
+
+/* h2o_pool_sync_check - h2o_sync_check for a pool's error word. */
+int h2o_pool_sync_check(h2o_pool* pool);
+
 /* h2o_last_error - message of the calling thread's last failed call ("" if none). */
 const char* h2o_last_error(void);
 
