@@ -278,7 +278,8 @@ def h2o_last_evicted(ctx: H2OContext, layer: int) -> np.ndarray:
 class _DeviceArray:
     """Exposes a library-owned device buffer through __cuda_array_interface__."""
 
-    def __init__(self, ptr: int, shape: tuple, typestr: str):
+    def __init__(self, ptr: int, shape: tuple, typestr: str, owner=None):
+        self.owner = owner  # kept alive as long as the tensor made of this is
         self.__cuda_array_interface__ = {"data": (ptr, False), "shape": shape,
                                          "typestr": typestr, "version": 3, "strides": None}
 
@@ -414,15 +415,16 @@ def _list_ptr(seqs, name: str = "seqs", n: int | None = None) -> int:
 
 
 def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
-    """Zero-copy torch views of a pool's arrays (library-owned memory): of one layer, or of
-    all of them with a leading dimension of layers. K and V are bf16, or uint8 E4M3 codes
+    """Zero-copy torch views of a pool's arrays (library-owned memory, which they keep until
+    the pool is closed): of one layer, or of all with a leading dimension of layers. K and V are bf16, or uint8 E4M3 codes
     with "kscale" and "vscale" in an "fp8" pool."""
     ptrs = [ctypes.c_void_p() for _ in range(9)]
     _check(load_library().h2o_pool_view(pool.handle, layer or 0, *[ctypes.byref(p) for p in ptrs]))
     lead = (pool.layers,) if layer is None else ()
     N, H, P, S = pool.pages, pool.heads, pool.page_size, pool.sequences
     dev = torch.device("cuda", pool.device)
-    mk = lambda p, shape, ts: torch.as_tensor(_DeviceArray(p.value, lead + shape, ts), device=dev)
+    mk = lambda p, shape, ts: torch.as_tensor(_DeviceArray(p.value, lead + shape, ts, pool),
+                                              device=dev)
     fp8 = pool.kv == "fp8"
     view = {}
     for name, p in zip("KV", ptrs):

@@ -41,13 +41,6 @@ constexpr int kNewSlot = -2;  // argmin slot value meaning "the new token itself
 constexpr int kSoloSlots = 8192;  // longest row whose logits stay in shared memory
 constexpr int kSoloRegs = 4;      // slots per thread whose score/position is preloaded
 
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

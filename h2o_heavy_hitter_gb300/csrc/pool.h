@@ -29,6 +29,7 @@ struct PoolView {
 };
 
 constexpr int kPoolMaxList = 1024;  // longest list of sequences of one call: one thread each
+constexpr int kPoolMaxGroup = 32;   // query heads per key head: the own rows of a sequence fit one warp
 
 // Fresh pages are found and the sequences' tables changed by one block per
 // layer ("plan"); a second kernel then moves the tokens. `fresh` (scratch) has
@@ -68,5 +69,8 @@ struct AttendArgs {
 };
 size_t pool_attend_scratch(const AttendArgs& a);
 cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream);
+// The plain form, for E4M3 pools.
+size_t pool_attend_simple_scratch(const AttendArgs& a);
+cudaError_t pool_attend_simple(const AttendArgs& a, void* scratch, cudaStream_t stream);
 
 }  // namespace h2o

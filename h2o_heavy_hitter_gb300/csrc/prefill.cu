@@ -36,6 +36,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "device_state.h"
 #include "h2o.h"
 #include "kernels.h"
 #include "tc.cuh"
@@ -45,7 +46,6 @@ namespace {
 
 constexpr int BM = 128;  // query rows per tile
 constexpr int BN = 128;  // keys per tile
-constexpr int kBoxBytes = 128 * 128;  // one TMA box: 128 rows x 64 bf16
 
 // ---- bulk async stores (TMA engine, shared -> global) ---------------------------
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0,
@@ -67,11 +67,6 @@ __device__ __forceinline__ void bulk_wait_read_1() {
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
-// Orders this thread's generic-proxy shared-memory writes before later async-proxy reads.
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // ------------------------------------------------------------------ forward
 // An item of the forward kernel is a block of 256 query rows of one row:
 // query tiles A = 2 qb and B = 2 qb + 1. Every K/V tile loaded serves both
@@ -122,23 +117,12 @@ struct FwdParams {
   int32_t* err;
 };
 
-__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
 template <int D>
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int tile, int row,
                                           uint64_t* bar) {
 #pragma unroll
   for (int b = 0; b < D / 64; ++b)
     tma_load_3d(static_cast<uint8_t*>(dst) + b * kBoxBytes, map, b * 64, tile * 128, row, bar);
-}
-
-// Wait used by warps that go on to run warp-collective tcgen05.ld / st: the
-// result is made warp-uniform, so a wait that gives up in one lane never
-// leaves the warp to run them divergently.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
 
 // Item order shared by both kernels. Rows are taken in blocks of `rb` rows
@@ -155,12 +139,6 @@ __device__ __forceinline__ void item_coords(int it, int rows, int nqt, int rb, i
   const int w = it - b * per_block;
   rank = w / nb;
   row = r0 + w % nb;
-}
-
-// K-major operand (rows x D, D contiguous): k-step kk covers columns [16kk, 16kk + 16).
-template <int D>
-__device__ __forceinline__ uint64_t desc_kmajor(const uint8_t* tile, int kk) {
-  return smem_desc(tile + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024);
 }
 
 // Persistent: CTA b takes items b, b + grid, ... of a list ordered by
@@ -836,19 +814,6 @@ __global__ void __launch_bounds__(kColThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
-}
-
 // Rows per block of the item order: `tensors` bf16 [T, D] operands re-read by
 // every item of a row (K and V for the forward pass, Q for the column sums)
 // should total about 24 MB per block, well inside the 129 MB L2.
@@ -856,41 +821,6 @@ int rows_per_l2_block(int T, int D, int tensors) {
   const double per_row = static_cast<double>(tensors) * T * D * 2;
   const int rb = static_cast<int>(24.0e6 / per_row);
   return rb < 1 ? 1 : rb;
-}
-
-// Per-device state of this file (kernel attributes, looked-up symbol
-// addresses) is kept for devices 0 .. kMaxDevices - 1 under one mutex.
-// forget_device_state() starts a new epoch, which invalidates all of it.
-constexpr int kMaxDevices = 64;
-std::mutex g_device_state_mutex;
-int g_device_state_epoch = 1;
-
-// Lets `kernel` use `bytes` of dynamic shared memory on the current device.
-// The attribute is per device, so it is set once per device and epoch;
-// opted_in[dev] records the epoch in which it was set (guarded by the mutex,
-// so concurrent first calls are safe).
-template <typename Kernel>
-cudaError_t raise_smem_limit(Kernel kernel, size_t bytes, int (&opted_in)[kMaxDevices]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(g_device_state_mutex);
-  if (opted_in[dev] != g_device_state_epoch) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bytes));
-    if (e != cudaSuccess) return e;
-    opted_in[dev] = g_device_state_epoch;
-  }
-  return cudaSuccess;
-}
-
-// SM count of the current device (one persistent CTA per SM).
-int num_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
 }
 
 // [rows, T, D] bf16, boxes of 128 tokens x 64 channels, 128-byte swizzle,
@@ -937,7 +867,7 @@ cudaError_t forward_t(const void* Q, const void* K, const void* V, int rows, int
   if ((e = make_map(&mv, V, rows, T, D)) != cudaSuccess) return e;
   if ((e = make_store_map(&mo, O, rows, T, D)) != cudaSuccess) return e;
   static int opted_in[kMaxDevices] = {};
-  if ((e = raise_smem_limit(attn_fwd_kernel<D>, FwdCfg<D>::SMEM, opted_in)) != cudaSuccess) return e;
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(attn_fwd_kernel<D>), FwdCfg<D>::SMEM, opted_in)) != cudaSuccess) return e;
   const int nqt = (T + BM - 1) / BM, nqb = (nqt + 1) / 2;
   FwdParams p{lse2, lens, heads, rows, T, lse_stride(T), nqt, nqb, rows * nqb,
               rows_per_l2_block(T, D, 2), kLog2e / sqrtf(float(D)), err};
@@ -955,7 +885,7 @@ cudaError_t colsum_t(const void* Q, const void* K, const float* lse2, int rows, 
   if ((e = make_map(&mq, Q, rows, T, D)) != cudaSuccess) return e;
   if ((e = make_map(&mk, K, rows, T, D)) != cudaSuccess) return e;
   static int opted_in[kMaxDevices] = {};
-  if ((e = raise_smem_limit(attn_colsum_kernel<D>, ColCfg<D>::SMEM, opted_in)) != cudaSuccess)
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(attn_colsum_kernel<D>), ColCfg<D>::SMEM, opted_in)) != cudaSuccess)
     return e;
   const int nqt = (T + BM - 1) / BM;
   ColParams p{lse2, colsum, lens, heads, rows, T, lse_stride(T), nqt, rows * nqt,
@@ -981,6 +911,50 @@ cudaError_t prefill_colsum(const void* Q, const void* K, const float* lse2, int 
   if (static_cast<long>(rows) * T == 0) return cudaSuccess;
   return d == 128 ? colsum_t<128>(Q, K, lse2, rows, T, lens, heads, colsum, err, stream)
                   : colsum_t<64>(Q, K, lse2, rows, T, lens, heads, colsum, err, stream);
+}
+
+// ------------------------------------------------------------------ per-device state
+// Kernel attributes and looked-up symbol addresses are kept for devices
+// 0 .. kMaxDevices - 1 under one mutex. forget_device_state() starts a new
+// epoch, which invalidates all of it.
+namespace {
+std::mutex g_device_state_mutex;
+int g_device_state_epoch = 1;
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+cudaError_t raise_smem_limit(const void* kernel, size_t bytes, int (&opted_in)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_device_state_mutex);
+  if (opted_in[dev] != g_device_state_epoch) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    opted_in[dev] = g_device_state_epoch;
+  }
+  return cudaSuccess;
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 1;
 }
 
 // ------------------------------------------------------------------ allocation-free scratch

@@ -21,6 +21,15 @@ from . import kv_fp8
 BAD_STATE, BAD_LENGTH, NO_PAGE, BAD_LIST = 2, 4, 8, 16
 
 
+def quantise(x):
+    """kv_fp8.quantize_vector of every vector [..., d], those of magnitude up to 2^-119 as zero."""
+    amax = np.max(np.abs(x), -1).astype(np.float32)
+    zero = amax <= 2.0 ** -119
+    inv = np.float32(kv_fp8.E4M3_MAX) / np.where(zero, np.float32(1), amax)
+    y = np.where(zero[..., None], np.float32(0), x.astype(np.float32) * inv[..., None])
+    return kv_fp8.e4m3_encode(y), np.where(zero, np.float32(0), amax / np.float32(kv_fp8.E4M3_MAX))
+
+
 class Pool:
     """One layer. K, V hold the stored values (dequantised for fp8) in float64; with fp8 also
     the codes and scales."""
@@ -102,20 +111,17 @@ class Pool:
             have, first = (int(x) for x in self.meta[s])
             self.table[s, self._need(have):self._need(have) + need] = self._take(need)
             self.meta[s] += t
-            for j in range(t):
-                p, o = self.table[s, (have + j) // self.page], (have + j) % self.page
-                for name, store, new in (("K", self.K, K), ("V", self.V, V)):
-                    for h in range(self.heads):
-                        x = new[i, h, j]
-                        if self.fp8:
-                            if np.max(np.abs(x)) <= 2.0 ** -119:
-                                x = np.zeros_like(x)
-                            c, sc = kv_fp8.quantize_vector(x)
-                            self.codes[name][p, h, o], self.scale[name][p, h, o] = c, sc
-                            x = kv_fp8.dequantize_vector(c, sc)
-                        store[p, h, o] = x
-                self.pos[p, :, o] = first + j
-                self.score[s, :, have + j] = 0 if score is None else score[i, :, j]
+            j = np.arange(t)
+            p, o = self.table[s][(have + j) // self.page], (have + j) % self.page
+            for name, store, new in (("K", self.K, K), ("V", self.V, V)):
+                x = new[i, :, :t].swapaxes(0, 1)  # [t, heads, d]
+                if self.fp8:
+                    c, sc = quantise(x)
+                    self.codes[name][p, :, o], self.scale[name][p, :, o] = c, sc
+                    x = kv_fp8.dequantize_vector(c, sc[..., None])
+                store[p, :, o] = x
+            self.pos[p, :, o] = (first + j)[:, None]
+            self.score[s, :, have:have + t] = 0 if score is None else score[i, :, :t]
 
     def fork(self, src, dst, share=True):
         dst = self._list(dst)

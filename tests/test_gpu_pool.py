@@ -166,6 +166,28 @@ def test_attend_many_rows_on_a_prefix(batch, heads, group, prefix, kv):
     b.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads,group,d,page,batch,longest,prefix", [
+    (24, 1, 64, 16, 6, 1500, 2200),   # many tiles per SM, units that begin and end inside a share
+    (24, 2, 128, 64, 9, 700, 3000),
+    (16, 5, 64, 32, 60, 130, 1700),   # three row tiles a head: a block of two and one of one
+    (20, 8, 128, 128, 17, 260, 2500), # two row tiles, the second nearly empty
+])
+def test_attend_many_tiles(heads, group, d, page, batch, longest, prefix, kv):
+    lens = [longest - (i * 331) % longest for i in range(batch)] + [prefix]
+    pages = sum(-(-n // page) for n in lens) + 1
+    b = Both(pages, page, heads, d, batch + 1, -(-max(lens) // page), kv, seed=batch)
+    for i, n in enumerate(lens):
+        b.write([i], n)
+    b.check()
+    b.attend(range(batch), heads * group, prefix=batch)
+    b.check()
+    b.attend(range(batch), heads * group, prefix=batch)
+    b.attend([batch] + list(range(0, batch, 2)), heads * group)  # the prefix as a sequence
+    b.check()
+    b.close()
+
+
 def test_attend_ignores_what_lies_behind_a_sequence():
     """NaN and infinities in the slots behind the last token, of the prefix too."""
     b = Both(pages=12, page=32, heads=2, d=64, sequences=3, max_pages=4)
@@ -206,7 +228,7 @@ def test_attend_repeats_bit_for_bit():
     b.write(range(17), 900, [int(x) for x in b.rng.integers(0, 90, 16)] + [900])
     _, q = bf16(b.queries(16, 8))
     before, runs = b.view["score"].clone(), []
-    for _ in range(4):
+    for _ in range(10):
         b.view["score"].copy_(before)
         out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints(range(16)), q, prefix=16)
         runs.append((out.clone(), lse.clone(), b.view["score"].clone()))
@@ -322,6 +344,18 @@ def test_calls_on_another_stream_and_in_a_graph():
         assert np.abs(lse.double().cpu().numpy() - want_lse).max() <= 1e-4
     b.check()
     b.close()
+
+
+def test_views_keep_their_pool():
+    import gc
+    import h2o_heavy_hitter_gb300 as h2o
+    pool = h2o.h2o_pool_create(1, 8, 16, 2, 64, 3, 4)
+    view = h2o.h2o_pool_view(pool)
+    k = view["K"][0, 3]
+    del view, pool
+    gc.collect()
+    others = [torch.full((8, 2, 16, 64), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+    assert not k.any() and len(others) == 64
 
 
 def test_large_pool_offsets_pass_32_bits():

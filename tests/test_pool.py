@@ -107,3 +107,15 @@ def test_oracle_compaction_selects_as_the_prompt_selection_does():
         kept, _ = oracle.prefill_select(scores[head], 12, 5)
         pages, offs = p._slots(0)
         assert np.array_equal(p.pos[pages, head, offs], np.sort(kept))
+
+
+def test_oracle_quantises_every_vector_as_the_fp8_oracle_does():
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((5, 3, 16)).astype(np.float32).astype(np.float64)
+    x[0, 0] = 0
+    x[1] *= 1e30
+    x[2] *= 1e-30
+    c, s = kv_pool.quantise(x)
+    for i in np.ndindex(5, 3):
+        want = oracle.kv_fp8.quantize_vector(x[i])
+        assert np.array_equal(c[i], want[0]) and s[i] == want[1]
