@@ -23,7 +23,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "libh2o.so"
 
 CU_SOURCES = ["decode.cu", "decode_multi.cu", "decode_ring.cu", "prefill.cu", "select.cu",
-              "pool_attend.cu", "pool_attend_simple.cu", "pool_pages.cu"]
+              "pool_attend.cu", "pool_pages.cu", "pool_prefix.cu"]
 CPP_SOURCES = ["h2o_api.cpp", "pool_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

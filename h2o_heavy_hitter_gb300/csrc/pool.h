@@ -69,8 +69,4 @@ struct AttendArgs {
 };
 size_t pool_attend_scratch(const AttendArgs& a);
 cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream);
-// The plain form, for E4M3 pools.
-size_t pool_attend_simple_scratch(const AttendArgs& a);
-cudaError_t pool_attend_simple(const AttendArgs& a, void* scratch, cudaStream_t stream);
-
 }  // namespace h2o

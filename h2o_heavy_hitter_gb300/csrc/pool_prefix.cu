@@ -1,0 +1,695 @@
+// Attention over a prefix that many query rows share: the queries of all
+// sequences of a batch are the rows of one matrix per key head. (The few-rows
+// case, the own tokens and the joining of pieces are in pool_attend.cu.)
+//
+// pool_prefix_kernel: S = Q K^T and O += P V (tcgen05, accumulators in TMEM), a
+//   thread per query row. Units are blocks of two tiles of 128 rows; a persistent
+//   CTA per SM takes an equal contiguous share of the units' key tiles. With one
+//   row tile the four warps of half t take keys 64 t .. 64 t + 63 of every tile and
+//   an accumulator of their own, so that two short softmax chains run side by side
+//   and no maximum is exchanged; with two, the halves take a row tile each and
+//   share the key and value tiles. S is double-buffered: the product of the next
+//   tile runs under the softmax of this one. Bound by HBM up to some 128 rows,
+//   beyond by the exponentials and the products of 256 rows a tile.
+// pool_prefix_score_kernel: the prefix's scores once every row's lse is known: S^T
+//   = K Q^T again, a thread per key, p = 2^(s - lse) summed over all rows in
+//   order. It reads K once more (2 d bytes a key and head); keeping the logits of
+//   more than 32 rows would move 8 bytes a key and row.
+#include "device_state.h"
+#include "pool_tiles.cuh"
+
+namespace h2o {
+namespace {
+
+// ------------------------------------------------------------------ attention
+// Warps: 0 tiles by TMA (bf16 pool), 1 MMA and TMEM, 2 queries, 3..6 half or row
+// tile 0, 7..10: 1 (one per TMEM lane quadrant), 11..14 tiles from E4M3 codes.
+constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpSoftmax = 3, kWarpCodes = 11;
+constexpr int kCodeThreads = 128;
+
+template <int D, bool F8>
+struct Cfg {
+  static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
+  static constexpr int TILE = TILE_KEYS * D * 2;
+  static constexpr int R = (F8 ? 4 : 5) * (D == 128 ? 1 : 2);
+  static constexpr uint32_t O_COL = 256;  // S buffers at columns 0 and 128, O of half t at 256 + 128 t
+  static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + SCALES + 1024 + 1024;
+};
+
+template <int R>
+struct Bars {
+  RingBars<R> ring;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
+  uint64_t o_last[2], o_free[2];               // one phase per unit
+  uint32_t tmem;
+};
+
+// A walk along one CTA's share of the units.
+struct Walk {
+  const AttendParams& p;
+  int len, tiles, cta;
+  int64_t at, end;
+  bool two;
+  int h, b, kt0, kt1, piece;
+
+  __device__ Walk(const AttendParams& p, int len, int cta) : p(p), len(len), cta(cta) {
+    tiles = key_tiles(len);
+    const int64_t total = static_cast<int64_t>(p.s.heads) * p.s.blocks * tiles;
+    at = share_begin(total, p.s.grid, cta);
+    end = share_begin(total, p.s.grid, cta + 1);
+  }
+  __device__ int rows(int t) const {  // valid rows of the unit's row tile t
+    return min(p.s.per_tile, p.s.n - (2 * b + (two ? t : 0)) * p.s.per_tile) * p.s.group;
+  }
+  __device__ bool next() {
+    if (at >= end) return false;
+    const int u = static_cast<int>(at / tiles);
+    kt0 = static_cast<int>(at - static_cast<int64_t>(u) * tiles);
+    kt1 = static_cast<int>(min(static_cast<int64_t>(tiles), kt0 + (end - at)));
+    h = u / p.s.blocks;
+    b = u - h * p.s.blocks;
+    two = 2 * b + 1 < p.s.nq;
+    piece = u + cta;
+    at += kt1 - kt0;
+    return true;
+  }
+};
+
+struct TileCursor {
+  Walk w;
+  int kt, kt1, seq, len, h;
+  __device__ explicit TileCursor(const Walk& walk)
+      : w(walk), kt(-1), kt1(0), seq(walk.p.a.prefix), len(walk.len) {}
+  __device__ bool step() {
+    if (++kt < kt1) return true;
+    if (!w.next()) return false;
+    kt = w.kt0;
+    kt1 = w.kt1;
+    h = w.h;
+    return true;
+  }
+};
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
+    pool_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv,
+                       const __grid_constant__ AttendParams p) {
+  using C = Cfg<D, F8>;
+  constexpr int R = C::R;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* ring = smem + 2 * C::TILE;
+  float* scales = reinterpret_cast<float*>(ring + R * C::TILE);
+  auto* bars = reinterpret_cast<Bars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(Bars<R>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
+  const PoolView& v = p.a.v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_ready[i], 8);
+      mbar_init(&bars->pv_done[i], 1);
+      mbar_init(&bars->o_last[i], 1);
+      mbar_init(&bars->o_free[i], 4);
+    }
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->ring.empty[i], 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == kWarpMMA) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == kWarpQ && lane == 0) tma_prefetch_map(&tq);
+  if (!F8 && warp == 0 && lane == 0) {
+    tma_prefetch_map(&tk);
+    tma_prefetch_map(&tv);
+  }
+  const int plen = max(0, checked_length(v, p.a.prefix, cta + threadIdx.x == 0));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  Walk w(p, plen, cta);
+  grid_launch_dependents();  // the few-rows kernel, as SMs become free
+
+  if (!F8 && warp == 0) {
+    produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
+  } else if (F8 && warp >= kWarpCodes) {
+    produce_e4m3<D, R, true, kCodeThreads>(v, ring, bars->ring, scales, TileCursor(w),
+                                           threadIdx.x - 32 * kWarpCodes);
+  } else if (warp == kWarpQ) {
+    if (lane == 0) {
+      uint32_t qn = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        for (int t = 0; t < (w.two ? 2 : 1); ++t, ++qn) {
+          const uint32_t qb = qn & 1;
+          if (qn >= 2 && !mbar_wait(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, v.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bars->q_full[qb], p.s.per_tile * p.s.group * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sQ + qb * C::TILE + c * kBoxBytes, &tq, c * 64, 0, w.h,
+                        (2 * w.b + t) * p.s.per_tile, &bars->q_full[qb]);
+        }
+      }
+    }
+  } else if (warp == kWarpMMA) {
+    // ---------------------------------------------------------------- MMA issuer
+    // S j is followed by the P V of S j - 1, so the softmax of one S overlaps the
+    // product of the next; the S buffer of j is that of j - 2, whose P V is issued.
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16(TILE_ROWS, TILE_KEYS, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16(TILE_ROWS, D, 0, 1);
+      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(ring, 0);
+      const uint64_t dv0 = smem_desc(ring, kBoxBytes, 1024);
+      uint32_t g = 0, qn = 0, j = 0;
+      int e = 0;
+      bool ok = true;
+      struct {
+        bool live = false, two, first, last, frees;
+        int t, e;
+        uint32_t j, g;
+      } pv;
+      auto issue_pv = [&]() -> bool {
+        const uint32_t st = (2 * pv.g + 1) % R, buf = pv.j & 1;
+        if (!mbar_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
+            !mbar_wait(&bars->ring.full[st], ((2 * pv.g + 1) / R) & 1, v.err))
+          return false;
+        if (pv.first && pv.e > 0) {
+          for (int t = 0; t < 2; ++t)
+            if ((!pv.two || t == pv.t) && !mbar_wait(&bars->o_free[t], (pv.e - 1) & 1, v.err))
+              return false;
+        }
+        tc_fence_after();
+        const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+        const uint32_t s_tm = tmem + buf * 128;
+        // B = V tile, MN-major: 16 keys = two 8-row swizzle atoms (2048 bytes)
+#pragma unroll
+        for (int kk = 0; kk < TILE_KEYS / 16; ++kk) {
+          const int half = kk >> 2;
+          const uint32_t o = tmem + C::O_COL + (pv.two ? pv.t : half) * 128;
+          const uint32_t a = s_tm + (pv.two ? kk * 8 : half * 64 + (kk & 3) * 8);
+          const bool fresh = pv.first && (pv.two ? kk == 0 : (kk & 3) == 0);
+          umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
+        }
+        umma_commit(&bars->pv_done[buf]);
+        if (pv.frees) umma_commit(&bars->ring.empty[st]);
+        if (pv.last)
+          for (int t = 0; t < 2; ++t)
+            if (!pv.two || t == pv.t) umma_commit(&bars->o_last[t]);
+        return true;
+      };
+      while (ok && w.next()) {
+        const int nt = w.two ? 2 : 1;
+        for (int kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
+          const uint32_t st = (2 * g) % R;
+          for (int t = 0; ok && t < nt; ++t, ++j) {
+            const uint32_t qb = (qn + t) & 1;
+            if ((kt == w.kt0 && !mbar_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
+                (t == 0 && !mbar_wait(&bars->ring.full[st], ((2 * g) / R) & 1, v.err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+            const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
+            const uint32_t d_tm = tmem + (j & 1) * 128;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+              umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
+            }
+            umma_commit(&bars->s_full[j & 1]);
+            if (t == nt - 1) umma_commit(&bars->ring.empty[st]);
+            if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
+            if (pv.live && !issue_pv()) {
+              ok = false;
+              break;
+            }
+            pv.live = true;
+            pv.two = w.two;
+            pv.first = kt == w.kt0;
+            pv.last = kt == w.kt1 - 1;
+            pv.frees = t == nt - 1;
+            pv.t = t;
+            pv.e = e;
+            pv.j = j;
+            pv.g = g;
+          }
+        }
+        qn += nt;
+        ++e;
+      }
+      if (ok && pv.live) issue_pv();
+    }
+  } else if (warp >= kWarpSoftmax && warp < kWarpCodes) {
+    // ---------------------------------------------------------------- softmax
+    const int t = (warp - kWarpSoftmax) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane, tid = ((warp - kWarpSoftmax) & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t o_tm = tmem + lane_off + C::O_COL + t * 128;
+    uint32_t j0 = 0, g = 0;
+    int e = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int rows = w.rows(t), step = w.two ? 2 : 1;
+      const bool active = quad * 32 < rows;  // warp-uniform
+      const int chunks = w.two ? 2 : 1, col0 = w.two ? 0 : 64 * t;
+      float m = -INFINITY, l = 0.f;
+      for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
+        const uint32_t jj = j0 + (kt - w.kt0) * step, j = w.two ? jj + t : jj;
+        const uint32_t s_tm = tmem + lane_off + (j & 1) * 128, st = (2 * g + 1) % R;
+        if (!warp_wait(&bars->s_full[j & 1], (j >> 1) & 1, v.err)) {
+          ok = false;
+          break;
+        }
+        const int valid = w.len - kt * TILE_KEYS;  // may exceed 128
+        if (F8 || valid < TILE_KEYS) {
+          // the value tile stays in its slot until these probabilities are used
+          if (!warp_wait(&bars->ring.full[st], ((2 * g + 1) / R) & 1, v.err)) {
+            ok = false;
+            break;
+          }
+        }
+        tc_fence_after();
+        const float4* ks = reinterpret_cast<const float4*>(scales + (g % kScaleTiles<true>) * 2 * TILE_KEYS);
+        const float4* vs = ks + TILE_KEYS / 4;
+        // 64 logits from column `first`, unscaled by 1 / sqrt(d); those behind the end -inf
+        auto load = [&](uint32_t (&s)[64], int first) {
+          tmem_ld32(s_tm + first, s);
+          tmem_ld32(s_tm + first + 32, s + 32);
+          tmem_wait_ld();
+          if (F8) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float4 k4 = ks[first / 4 + x];
+              s[4 * x] = __float_as_uint(__uint_as_float(s[4 * x]) * k4.x);
+              s[4 * x + 1] = __float_as_uint(__uint_as_float(s[4 * x + 1]) * k4.y);
+              s[4 * x + 2] = __float_as_uint(__uint_as_float(s[4 * x + 2]) * k4.z);
+              s[4 * x + 3] = __float_as_uint(__uint_as_float(s[4 * x + 3]) * k4.w);
+            }
+          }
+          if (first + 64 > valid) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x)
+              if (first + x >= valid) s[x] = __float_as_uint(-INFINITY);
+          }
+        };
+        if (active) {
+          uint32_t s[64];
+          float mx = -INFINITY;
+          for (int c = 0; c < chunks; ++c) {
+            const int first = col0 + 64 * c;
+            load(s, first);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 64; x += 8)
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                m4[y] = fmax3(m4[y], __uint_as_float(s[x + y]), __uint_as_float(s[x + 4 + y]));
+            mx = fmax3(fmax3(mx, m4[0], m4[1]), m4[2], m4[3]);
+          }
+          mx *= p.qscale;
+          float alpha = 1.f;
+          bool rescale = false;
+          if (mx > m + 8.f) {
+            rescale = kt > w.kt0 && l > 0.f;
+            if (rescale) alpha = ex2(m - mx);
+            m = mx;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = f2_pack(p.qscale, p.qscale), nm2 = f2_pack(-ref, -ref);
+          uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+          for (int c = 0; c < chunks; ++c) {
+            const int first = col0 + 64 * c;
+            if (chunks > 1) load(s, first);
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[cc * 16 + 2 * x]),
+                                         __uint_as_float(s[cc * 16 + 2 * x + 1])),
+                                 sc2, nm2),
+                          a, b);
+                const float p0 = ex2(a), p1 = ex2(b);
+                rs2[x & 1] = f2_add(rs2[x & 1], f2_pack(p0, p1));
+                if (F8) {
+                  const float2 v2 = reinterpret_cast<const float2*>(vs)[first / 2 + cc * 8 + x];
+                  pk[x] = pack_bf16x2(p0 * v2.x, p1 * v2.y);
+                } else {
+                  pk[x] = pack_bf16x2(p0, p1);
+                }
+              }
+              // P over S columns already read: this half's, or (two chunks) the first 64
+              tmem_st8(s_tm + (w.two ? 32 * c : col0) + cc * 8, pk);
+            }
+          }
+          float r0, r1, r2, r3;
+          f2_unpack(rs2[0], r0, r1);
+          f2_unpack(rs2[1], r2, r3);
+          l = fmaf(l, alpha, (r0 + r1) + (r2 + r3));
+          // the whole warp rescales its O rows when any of its rows raised the max;
+          // the P V before this S must have completed (with two row tiles it has:
+          // it was issued before this S)
+          if (__any_sync(0xffffffffu, rescale)) {
+            // (on its own barrier, whose phase before belongs to the P V of j - 3: a
+            // parity wait may be one phase behind or level, never two)
+            if (!w.two && !warp_wait(&bars->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, v.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_tm + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tmem_st32(o_tm + c * 32, o);
+            }
+          }
+        }
+        if (!F8 && valid < TILE_KEYS) {  // values behind the end count as zero, whatever they are
+          const int lo = w.two ? 0 : 64 * t, hi = w.two ? TILE_KEYS : lo + 64;
+          const int from = max(lo, valid);
+          for (int x = tid; x < (hi - from) * (D / 8); x += 128) {
+            const int row = from + x / (D / 8), c = x % (D / 8);
+            *reinterpret_cast<uint4*>(ring + st * C::TILE + (c >> 3) * kBoxBytes + row * 128 +
+                                      (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&bars->p_ready[j & 1], w.two ? 2 : 1);
+      }
+      if (!ok) break;
+      // ---- the piece: O out of TMEM, which the next unit may then use
+      if (!warp_wait(&bars->o_last[t], e & 1, v.err)) break;
+      tc_fence_after();
+      if (active) {
+        const size_t rec = (static_cast<size_t>(w.piece) * 2 + t) * TILE_ROWS + r;
+        float* po = p.w.po + rec * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_tm + c * 32, o);
+          tmem_wait_ld();
+          if (r < rows) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              reinterpret_cast<uint4*>(po + c * 32)[x] =
+                  make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+        if (r < rows) p.w.pml[rec] = make_float2(m, l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_free[t]);
+      j0 += (w.kt1 - w.kt0) * step;
+      ++e;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ scores of the prefix
+// Warps: 0 tiles by TMA, 1 MMA and TMEM, 2 queries, 3..6 even key tiles, 7..10 odd
+// ones, 11..14 tiles from E4M3 codes.
+template <int D, bool F8>
+struct ScoreCfg {
+  static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
+  static constexpr int TILE = TILE_KEYS * D * 2;
+  static constexpr int R = 4 * (D == 128 ? 1 : 2);
+  static constexpr int SCALES = F8 ? kScaleTiles<false> * 2 * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + SCALES + 1024 + 1024;
+};
+
+template <int R>
+struct ScoreBars {
+  RingBars<R> ring;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
+  uint32_t tmem;
+};
+
+// One CTA's share of the (head, key tile) list.
+struct KeyCursor {
+  int64_t it, end;
+  int tiles, seq, len, h, kt;
+  __device__ KeyCursor(const AttendParams& p, int len, int cta) : seq(p.a.prefix), len(len) {
+    tiles = key_tiles(len);
+    const int64_t total = static_cast<int64_t>(p.s.heads) * tiles;
+    it = share_begin(total, p.s.grid, cta) - 1;
+    end = share_begin(total, p.s.grid, cta + 1);
+  }
+  __device__ bool step() {
+    if (++it >= end) return false;
+    h = static_cast<int>(it / tiles);
+    kt = static_cast<int>(it - static_cast<int64_t>(h) * tiles);
+    return true;
+  }
+  // after step(): this is the head's last tile of the share
+  __device__ bool last_of_head() const { return it + 1 >= end || kt + 1 == tiles; }
+};
+
+// The row tiles of a head stay in shared memory when there are at most two; more
+// are fetched again for every key tile. A fill is one load of a row tile: fill f
+// lies in buffer f & 1.
+template <int D, bool F8>
+__global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
+    pool_prefix_score_kernel(const __grid_constant__ CUtensorMap tq,
+                             const __grid_constant__ CUtensorMap tk,
+                             const __grid_constant__ AttendParams p) {
+  using C = ScoreCfg<D, F8>;
+  constexpr int R = C::R;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* ring = smem + 2 * C::TILE;
+  float* scales = reinterpret_cast<float*>(ring + R * C::TILE);
+  auto* bars = reinterpret_cast<ScoreBars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(ScoreBars<R>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
+  const PoolView& v = p.a.v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->ring.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      // E4M3: the issuing thread arrives too, having seen the tile's scales written
+      mbar_init(&bars->s_full[i], F8 ? 2 : 1);
+      mbar_init(&bars->s_free[i], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == kWarpMMA) {
+    tmem_alloc(&bars->tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tq);
+    if (!F8) tma_prefetch_map(&tk);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const int len = max(0, checked_length(v, p.a.prefix, false));
+  const int nq = p.s.nq, group = p.s.group;
+  const bool stay = nq <= 2;
+  KeyCursor k(p, len, blockIdx.x);
+
+  if (!F8 && warp == 0) {
+    produce_tma<D, R, false>(v, &tk, nullptr, ring, bars->ring, k);
+  } else if (F8 && warp >= kWarpCodes) {
+    produce_e4m3<D, R, false, kCodeThreads>(v, ring, bars->ring, scales, k,
+                                            threadIdx.x - 32 * kWarpCodes);
+  } else if (warp == kWarpQ) {
+    if (lane == 0) {
+      uint32_t f = 0;
+      int last = -1;
+      bool ok = true;
+      while (ok && k.step()) {
+        if (stay && k.h == last) continue;
+        last = k.h;
+        for (int qt = 0; qt < nq; ++qt, ++f) {
+          const uint32_t qb = f & 1;
+          if (f >= 2 && !mbar_wait(&bars->q_empty[qb], ((f >> 1) - 1) & 1, v.err)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bars->q_full[qb], p.s.per_tile * group * D * 2);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sQ + qb * C::TILE + c * kBoxBytes, &tq, c * 64, 0, k.h, qt * p.s.per_tile,
+                        &bars->q_full[qb]);
+        }
+      }
+    }
+  } else if (warp == kWarpMMA) {
+    if (lane == 0) {
+      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(ring, 0);
+      uint32_t f0 = 0, cnt[2] = {0, 0};  // f0: fill of the head's (or tile's) row tile 0
+      bool ok = true;
+      int last = -1;
+      for (uint32_t g = 0; ok && k.step(); ++g) {
+        const bool fresh = !stay || k.h != last;  // row tiles newly filled
+        if (fresh && last >= 0) f0 += nq;
+        last = k.h;
+        const bool done = !stay || k.last_of_head();  // the row tiles' last use
+        const uint32_t st = g % R;
+        const int t = g & 1;
+        if (!mbar_wait(&bars->ring.full[st], (g / R) & 1, v.err)) break;
+        for (int qt = 0; qt < nq; ++qt) {
+          const uint32_t f = f0 + qt, qb = f & 1, buf = 2 * t + (cnt[t] & 1);
+          if ((fresh && !mbar_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
+              (cnt[t] >= 2 && !mbar_wait(&bars->s_free[buf], ((cnt[t] >> 1) - 1) & 1, v.err))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
+          const uint32_t idesc = idesc_bf16(TILE_KEYS, (rows + 15) / 16 * 16, 0, 0);
+          const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+          const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + buf * 128, kb + off, qd + off, idesc, kk > 0);
+          }
+          umma_commit(&bars->s_full[buf]);
+          if (F8) mbar_arrive(&bars->s_full[buf]);
+          if (done) umma_commit(&bars->q_empty[qb]);
+          if (qt == nq - 1) umma_commit(&bars->ring.empty[st]);
+          ++cnt[t];
+        }
+      }
+    }
+  } else if (warp >= kWarpSoftmax && warp < kWarpCodes) {
+    const int t = (warp - kWarpSoftmax) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    uint32_t cnt = 0;
+    bool ok = true;
+    grid_dependency_wait();  // the lse's, by the kernel before
+    for (uint32_t g = 0; ok && k.step(); ++g) {
+      if ((g & 1) != static_cast<uint32_t>(t)) continue;
+      float acc = 0.f;
+      for (int qt = 0; qt < nq; ++qt, ++cnt) {
+        const uint32_t buf = 2 * t + (cnt & 1);
+        const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
+        const float* nl = p.w.nlse + (static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS;
+        if (!warp_wait(&bars->s_full[buf], (cnt >> 1) & 1, v.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float ks = F8 ? p.qscale * scales[(g % kScaleTiles<false>) * 2 * TILE_KEYS + r] : p.qscale;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < rows; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(tmem + lane_off + buf * 128 + c, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            if (c + x >= rows) break;  // uniform
+            const float n = nl[c + x];
+            // rows that are not counted may hold anything
+            part[x & 3] += n == -INFINITY ? 0.f : ex2(fmaf(__uint_as_float(s[x]), ks, n));
+          }
+        }
+        acc += (part[0] + part[1]) + (part[2] + part[3]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_free[buf]);
+      }
+      if (!ok) break;
+      const int key = k.kt * TILE_KEYS + r;
+      if (key < len) v.score[(static_cast<size_t>(p.a.prefix) * v.heads + k.h) * v.cap + key] += acc;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+cudaError_t maps(const AttendParams& p, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
+  cudaError_t e = query_map(tq, p.a, p.s.per_tile);
+  if (e == cudaSuccess && !p.a.v.kscale) e = page_map(tk, p.a.v.K, p.a.v);
+  if (e == cudaSuccess && !p.a.v.kscale && tv) e = page_map(tv, p.a.v.V, p.a.v);
+  return e;
+}
+
+template <int D, bool F8>
+cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
+  CUtensorMap tq, tk{}, tv{};
+  cudaError_t e = maps(p, &tq, &tk, &tv);
+  if (e != cudaSuccess) return e;
+  using C = Cfg<D, F8>;
+  static int opted_in[kMaxDevices] = {};
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(pool_prefix_kernel<D, F8>), C::SMEM,
+                            opted_in)) != cudaSuccess)
+    return e;
+  pool_prefix_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool F8>
+cudaError_t score_t(const AttendParams& p, cudaStream_t stream) {
+  CUtensorMap tq, tk{};
+  cudaError_t e = maps(p, &tq, &tk, nullptr);
+  if (e != cudaSuccess) return e;
+  using C = ScoreCfg<D, F8>;
+  static int opted_in[kMaxDevices] = {};
+  if ((e = raise_smem_limit(reinterpret_cast<const void*>(pool_prefix_score_kernel<D, F8>), C::SMEM,
+                            opted_in)) != cudaSuccess)
+    return e;
+  return launch_after(pool_prefix_score_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream,
+                      tq, tk, p);
+}
+
+}  // namespace
+
+cudaError_t pool_prefix(const AttendParams& p, cudaStream_t stream) {
+  if (p.a.v.kscale) return p.s.d == 128 ? prefix_t<128, true>(p, stream) : prefix_t<64, true>(p, stream);
+  return p.s.d == 128 ? prefix_t<128, false>(p, stream) : prefix_t<64, false>(p, stream);
+}
+
+cudaError_t pool_prefix_score(const AttendParams& p, cudaStream_t stream) {
+  if (p.a.v.kscale) return p.s.d == 128 ? score_t<128, true>(p, stream) : score_t<64, true>(p, stream);
+  return p.s.d == 128 ? score_t<128, false>(p, stream) : score_t<64, false>(p, stream);
+}
+
+}  // namespace h2o
