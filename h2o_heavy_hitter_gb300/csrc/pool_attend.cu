@@ -223,6 +223,98 @@ __device__ __forceinline__ float order_value(int k) {
   return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
+// The sums over a warp of CH values per lane; lane i < CH gets value i's. Each
+// step halves the values a lane holds, then what is left is summed over lanes.
+template <int CH>
+__device__ __forceinline__ float warp_sums(const float (&x)[CH], int lane) {
+  float y[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) y[i] = x[i];
+  int off = 16;
+#pragma unroll
+  for (int n = CH / 2; n >= 1; n /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? y[i] : y[i + n], keep = up ? y[i + n] : y[i];
+      y[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+  float z = y[0];
+#pragma unroll
+  for (int o = 16 / CH; o; o /= 2) z += __shfl_xor_sync(0xffffffffu, z, o);
+  // value i is in the lanes whose upper bits are i's, most significant first
+  return CH == 1 ? z : __shfl_sync(0xffffffffu, z, (lane * (32 / CH)) & 31);
+}
+
+// One tile's logits and probabilities, thread = key.
+struct TileRows {
+  uint32_t s_tm;
+  float ks, vs;   // scales of the key's logits and of its value
+  bool live;      // the key lies before the sequence's end
+  uint8_t* p;     // row 0 of the P operand at this key's place in a 16-byte chunk
+  int chunk;      // that chunk
+  float* logits;  // row 0's logit of this key, or null
+  int cap, rows;
+};
+
+// Softmax of a tile against the running maximum m of row `lane`, CH rows at a
+// time (unused ones are computed and dropped: branches would serialise the
+// reductions). Raises m only where it grows by more than 2^8 (alpha, rescale);
+// sum: row `lane`'s over this warp's keys. False: the exchange gave up.
+template <int CH, typename Exchange>
+__device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float& alpha,
+                                             bool& rescale, float& sum, Exchange&& exchange) {
+  const int lane = threadIdx.x & 31;
+  uint32_t s[8];
+  float mine = -INFINITY;
+  for (int r0 = 0; r0 < a.rows; r0 += CH) {
+    tmem_ld8(a.s_tm + r0, s);
+    tmem_wait_ld();
+    float top[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const float z = a.live ? __uint_as_float(s[i]) * a.ks : -INFINITY;
+      top[i] = order_value(__reduce_max_sync(0xffffffffu, order_key(z)));
+      if (a.logits && a.live && r0 + i < a.rows) a.logits[static_cast<size_t>(r0 + i) * a.cap] = z;
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (lane == r0 + i) mine = top[i];
+  }
+  float all[4];
+  if (!exchange(mine, all)) return false;
+  const float mx = fmaxf(fmax3(all[0], all[1], all[2]), all[3]);
+  alpha = 1.f;
+  rescale = false;
+  if (lane < a.rows && mx > m + 8.f) {
+    rescale = m != -INFINITY;
+    if (rescale) alpha = ex2(m - mx);
+    m = mx;
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+  sum = 0.f;
+  for (int r0 = 0; r0 < a.rows; r0 += CH) {
+    if (a.rows > CH) {
+      tmem_ld8(a.s_tm + r0, s);
+      tmem_wait_ld();
+    }
+    float pr[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const float n = __shfl_sync(0xffffffffu, ref, r0 + i);
+      pr[i] = a.live ? ex2(fmaf(__uint_as_float(s[i]), a.ks, -n)) : 0.f;
+      // K-major, 128-byte swizzle: 16-byte chunk (key / 8) of a row at chunk ^ (row & 7)
+      const int row = r0 + i;
+      *reinterpret_cast<__nv_bfloat16*>(a.p + row * 128 + ((a.chunk ^ (row & 7)) << 4)) =
+          __float2bfloat16(a.live ? pr[i] * a.vs : 0.f);
+    }
+    const float x = __shfl_sync(0xffffffffu, warp_sums<CH>(pr, lane), (lane - r0) & 31);
+    if (lane >= r0 && lane < r0 + CH) sum = x;
+  }
+  return true;
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     pool_rows_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap t1,
@@ -441,57 +533,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           }
         }
         tc_fence_after();
-        // the tile's maximum of each row
-        uint32_t s[8];
-        float mine = -INFINITY;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          tmem_ld8(s_tm + r0, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (r0 + i >= rows) break;
-            const float z = live ? __uint_as_float(s[i]) * ks : -INFINITY;
-            const float top = order_value(__reduce_max_sync(0xffffffffu, order_key(z)));
-            if (lane == r0 + i) mine = top;
-            if (logits && live) logits[static_cast<size_t>(r0 + i) * v.cap + kt * TILE_KEYS + r] = z;
-          }
-        }
-        float all[4];
-        if (!exchange(mine, all)) {
+        float alpha = 1.f, sum;
+        bool rescale = false;
+        const TileRows tr{s_tm, ks, vs, live,
+                          sP + (t * 2 + buf) * C::P + (r >> 6) * kQBox + (r & 7) * 2, (r & 63) >> 3,
+                          logits ? logits + kt * TILE_KEYS + r : nullptr, v.cap, rows};
+        const bool done = rows == 1   ? tile_softmax<1>(tr, m, alpha, rescale, sum, exchange)
+                          : rows <= 4 ? tile_softmax<4>(tr, m, alpha, rescale, sum, exchange)
+                                      : tile_softmax<8>(tr, m, alpha, rescale, sum, exchange);
+        if (!done) {
           ok = false;
           break;
-        }
-        const float mx = fmaxf(fmax3(all[0], all[1], all[2]), all[3]);
-        // the running maximum is raised only when it grows by more than 2^8
-        float alpha = 1.f;
-        bool rescale = false;
-        if (mx > m + 8.f) {
-          rescale = m != -INFINITY;
-          if (rescale) alpha = ex2(m - mx);
-          m = mx;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        uint8_t* prow = sP + (t * 2 + buf) * C::P + (r >> 6) * kQBox + (r & 7) * 2;
-        float sum = 0.f;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-          if (rows > 8) {
-            tmem_ld8(s_tm + r0, s);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (r0 + i >= rows) break;
-            const float n = __shfl_sync(0xffffffffu, ref, r0 + i);
-            const float pr = live ? ex2(fmaf(__uint_as_float(s[i]), ks, -n)) : 0.f;
-            float a = pr;
-#pragma unroll
-            for (int off = 16; off; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-            if (lane == r0 + i) sum = a;
-            // K-major, 128-byte swizzle: 16-byte chunk (key / 8) of row i at chunk ^ (row & 7)
-            const int row = r0 + i;
-            *reinterpret_cast<__nv_bfloat16*>(prow + row * 128 + ((((r & 63) >> 3) ^ (row & 7)) << 4)) =
-                __float2bfloat16(live ? pr * vs : 0.f);
-          }
         }
         l = fmaf(l, alpha, sum);
         if (__any_sync(0xffffffffu, rescale)) {  // the same in the four warps
@@ -557,161 +609,195 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ joining the pieces
-constexpr int kFinishThreads = 128;
+constexpr int kFinishWarps = 4;
 
-// Where the pieces of a row's unit are.
-struct Pieces {
-  int prefix, recs, rec0, pa;  // records of the prefix; per piece; first; first piece
-  int own, ta;                 // pieces of the own tokens; first
-  int r0;                      // row of query 0 of the group in its prefix tile
+// Where the records of a (entry, key head) unit's rows are: `prefix` of the
+// prefix, then `own` of the own tokens. Record i of row g is at base + i * step + g.
+struct Records {
+  int prefix, own;
+  size_t pbase, pstep, obase;
 };
 
-__device__ __forceinline__ Pieces pieces_of(const AttendParams& p, int b, int h, int plen) {
-  Pieces x{};
-  const int pt = key_tiles(plen);
+// Warp-wide: the four divisions that place the pieces run in as many lanes.
+__device__ __forceinline__ Records records_of(const AttendParams& p, int b, int h, int plen, int lane) {
+  Records x{};
+  const int pt = p.a.prefix >= 0 ? key_tiles(plen) : 0, tiles = p.w.cum[b + 1] - p.w.cum[b];
   const int64_t own = static_cast<int64_t>(p.w.cum[p.s.n]) * p.s.heads;
-  const int qt = b / p.s.per_tile;
-  x.r0 = (b - qt * p.s.per_tile) * p.s.group;
-  x.recs = 1;
-  if (pt && p.s.few) {
-    const int64_t total = static_cast<int64_t>(p.s.heads) * pt + own, at = static_cast<int64_t>(h) * pt;
-    const int c0 = owner(at, total, p.s.grid);
-    x.prefix = owner(at + pt - 1, total, p.s.grid) - c0 + 1;
-    x.pa = h + c0;
-  } else if (pt) {
-    const int64_t total = static_cast<int64_t>(p.s.heads) * p.s.blocks * pt;
-    const int u = h * p.s.blocks + (qt >> 1);
-    const int64_t at = static_cast<int64_t>(u) * pt;
-    const int c0 = owner(at, total, p.s.grid);
-    x.prefix = owner(at + pt - 1, total, p.s.grid) - c0 + 1;
-    x.pa = u + c0;
-    if ((qt | 1) < p.s.nq)
-      x.rec0 = qt & 1;  // a block of two row tiles: a record per tile
-    else
-      x.recs = 2;       // one row tile: a record per half of the keys
-    x.prefix *= x.recs;
+  const int64_t pre = static_cast<int64_t>(p.s.heads) * (p.s.few ? 1 : p.s.blocks) * pt;
+  const int64_t ototal = own + (p.s.few ? pre : 0), ptotal = p.s.few ? ototal : pre;
+  const int qt = b / p.s.per_tile, r0 = (b - qt * p.s.per_tile) * p.s.group;
+  const int u = p.s.few ? h : h * p.s.blocks + (qt >> 1);
+  const int64_t pa = static_cast<int64_t>(u) * pt;
+  const int64_t oa = (p.s.few ? pre : 0) + static_cast<int64_t>(p.w.cum[b]) * p.s.heads + static_cast<int64_t>(h) * tiles;
+  // first and last tile of the prefix unit, of the own one
+  const int64_t at = lane < 2 ? pa + (lane ? pt - 1 : 0) : oa + (lane == 2 ? 0 : tiles - 1);
+  const int64_t total = lane < 2 ? ptotal : ototal;
+  const int c = total > 0 ? owner(at, total, p.s.grid) : 0;
+  const int p0 = __shfl_sync(0xffffffffu, c, 0), p1 = __shfl_sync(0xffffffffu, c, 1);
+  const int o0 = __shfl_sync(0xffffffffu, c, 2), o1 = __shfl_sync(0xffffffffu, c, 3);
+  if (pt) {
+    x.prefix = p1 - p0 + 1;
+    const size_t piece = u + p0;
+    if (p.s.few) {
+      x.pbase = piece * kFewRows + r0;
+      x.pstep = kFewRows;
+    } else if ((qt | 1) < p.s.nq) {  // a block of two row tiles: a record per tile
+      x.pbase = (piece * 2 + (qt & 1)) * TILE_ROWS + r0;
+      x.pstep = 2 * TILE_ROWS;
+    } else {                         // one row tile: a record per half of the keys
+      x.pbase = piece * 2 * TILE_ROWS + r0;
+      x.pstep = TILE_ROWS;
+      x.prefix *= 2;
+    }
   }
-  const int tiles = p.w.cum[b + 1] - p.w.cum[b];
   if (tiles) {
-    const int64_t first = p.s.few ? static_cast<int64_t>(p.s.heads) * pt : 0, total = first + own;
-    const int64_t at = first + static_cast<int64_t>(p.w.cum[b]) * p.s.heads + static_cast<int64_t>(h) * tiles;
-    const int c0 = owner(at, total, p.s.grid);
-    x.own = owner(at + tiles - 1, total, p.s.grid) - c0 + 1;
-    x.ta = b * p.s.heads + h + c0;
+    x.own = o1 - o0 + 1;
+    x.obase = static_cast<size_t>(b * p.s.heads + h + o0) * p.s.group;
   }
   return x;
 }
 
-// Index of record i of row g in its array (the prefix's for i < x.prefix).
-__device__ __forceinline__ size_t record(const AttendParams& p, const Pieces& x, int i, int g) {
-  if (i >= x.prefix) return static_cast<size_t>(x.ta + i - x.prefix) * p.s.group + g;
-  if (p.s.few) return static_cast<size_t>(x.pa + i) * kFewRows + x.r0 + g;
-  return (static_cast<size_t>(x.pa + i / x.recs) * 2 + x.rec0 + i % x.recs) * TILE_ROWS + x.r0 + g;
-}
-
-// A warp's lse (base 2) of row g, the same bits wherever it is computed.
-__device__ __forceinline__ float row_lse(const AttendParams& p, const Pieces& x, int g, int lane) {
-  float m = -INFINITY, l = 0.f;
-  const int all = x.prefix + x.own;
-  for (int i = lane; i < all; i += 32) {
-    const float2 y = (i < x.prefix ? p.w.pml : p.w.tml)[record(p, x, i, g)];
-    const float top = fmaxf(m, y.x);
-    if (top != -INFINITY) {
-      l = l * ex2(m - top) + y.y * ex2(y.x - top);
-      m = top;
-    } else {
-      l += y.y;  // a NaN sum stays one
-    }
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
-    const float top = fmaxf(m, mo);
-    if (top != -INFINITY)
-      l = l * ex2(m - top) + lo * ex2(mo - top);
-    else
-      l += lo;
-    m = top;
-  }
-  return __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
-}
-
-// Blocks (entry, key head; chunk of keys): the rows' outputs and the scores of the
-// own tokens; then, for a prefix with few rows, blocks (n * heads + head; chunk):
-// the prefix's scores. Every block computes the lse's that it needs from the
-// pieces' maxima and sums, a warp per row; chunk 0 joins the outputs.
+// A warp per (entry, key head), and per chunk of keys: joins the rows of the
+// group in the order of the pieces and adds the probabilities of the own tokens
+// to their scores. Every chunk computes the lse's it needs, chunk 0 writes.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
+__global__ void __launch_bounds__(32 * kFinishWarps)
     pool_finish_kernel(const __grid_constant__ AttendParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ float s_lse[kFewRows];
   const PoolView& v = p.a.v;
-  const int group = p.s.group, units = p.s.n * p.s.heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
-  const int step = gridDim.y * kFinishThreads, j0 = blockIdx.y * kFinishThreads + threadIdx.x;
-  if (static_cast<int>(blockIdx.x) >= units) {
-    const int h = blockIdx.x - units, rows = p.s.n * group;
-    for (int i = warp; i < rows; i += kFinishThreads / 32) {
-      const int b = i / group;
-      const float x = p.w.seq[b] < 0 ? INFINITY : row_lse(p, pieces_of(p, b, h, plen), i - b * group, lane);
-      if (lane == 0) s_lse[i] = x;  // +inf: not counted, whatever its logits are
-    }
-    __syncthreads();
-    const float* L = p.w.plogits + static_cast<size_t>(h) * rows * v.cap;
-    float* score = v.score + (static_cast<size_t>(p.a.prefix) * v.heads + h) * v.cap;
-    for (int j = j0; j < plen; j += step) {
-      float sum = 0.f;
-      for (int i = 0; i < rows; ++i)
-        if (s_lse[i] != INFINITY) sum += ex2(L[static_cast<size_t>(i) * v.cap + j] - s_lse[i]);
-      score[j] += sum;
-    }
-    return;
-  }
-  const int b = blockIdx.x / p.s.heads, h = blockIdx.x % p.s.heads, seq = p.w.seq[b];
-  float* nlse = nullptr;  // for the scores of a prefix with many rows
-  if (p.s.blocks && !p.s.few && blockIdx.y == 0)
+  const int group = p.s.group, lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * kFinishWarps + (threadIdx.x >> 5);
+  if (unit >= p.s.n * p.s.heads) return;
+  const int b = unit / p.s.heads, h = unit - b * p.s.heads, seq = p.w.seq[b];
+  float* nlse = nullptr;  // for the scores of the prefix
+  if (p.w.nlse && blockIdx.y == 0)
     nlse = p.w.nlse + (static_cast<size_t>(h) * p.s.nq + b / p.s.per_tile) * TILE_ROWS +
            b % p.s.per_tile * group;
   if (seq < 0) {
-    if (nlse && threadIdx.x < group) nlse[threadIdx.x] = -INFINITY;
+    if (nlse && lane < group) nlse[lane] = -INFINITY;
     return;
   }
-  const Pieces x = pieces_of(p, b, h, plen);
-  for (int g = warp; g < group; g += kFinishThreads / 32) {
-    const float lse = row_lse(p, x, g, lane);
-    if (lane == 0) s_lse[g] = lse;
+  const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
+  const int len = v.meta[2 * seq];
+  const Records x = records_of(p, b, h, plen, lane);
+  const int all = x.prefix + x.own;
+  __shared__ float s_lse[kFinishWarps][kFewRows];
+  float lse_of = -INFINITY;  // of row `lane`
+  for (int g = 0; g < group; ++g) {
+    auto record = [&](int i) -> size_t {
+      return (i < x.prefix ? x.pbase + i * x.pstep : x.obase + static_cast<size_t>(i - x.prefix) * group) + g;
+    };
+    auto ml = [&](int i) -> float2 { return (i < x.prefix ? p.w.pml : p.w.tml)[record(i)]; };
+    float m = -INFINITY, l = 0.f;
+    float2 first = make_float2(-INFINITY, 0.f);  // of record `lane`
+    for (int i = lane; i < all; i += 32) {
+      const float2 y = ml(i);
+      if (i < 32) first = y;
+      const float top = fmaxf(m, y.x);
+      if (top != -INFINITY) {
+        l = l * ex2(m - top) + y.y * ex2(y.x - top);
+        m = top;
+      } else {
+        l += y.y;  // a NaN sum stays one
+      }
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
+      const float top = fmaxf(m, mo);
+      if (top != -INFINITY)
+        l = l * ex2(m - top) + lo * ex2(mo - top);
+      else
+        l += lo;
+      m = top;
+    }
+    const float lse = __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
+    if (lane == g) lse_of = lse;
     if (blockIdx.y) continue;
     float acc[D / 32] = {};
-    for (int i = 0; i < x.prefix + x.own; ++i) {
-      const bool pre = i < x.prefix;
-      const size_t at = record(p, x, i, g);
-      const float wgt = ex2((pre ? p.w.pml : p.w.tml)[at].x - lse);
-      const float* o = (pre ? p.w.po : p.w.to) + at * D + lane * (D / 32);
-      if (wgt == 0.f) continue;
+    for (int i0 = 0; i0 < all; i0 += 32) {
+      const float mine = i0 == 0 ? first.x : i0 + lane < all ? ml(i0 + lane).x : -INFINITY;
+      const float wgt = all ? ex2(mine - lse) : 0.f;
+      const int n = min(32, all - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wgt, i);
+        const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(i0 + i) * D + lane * (D / 32);
+        float part[D / 32];
+        if constexpr (D == 128) {
+          const float4 y = *reinterpret_cast<const float4*>(o);
+          part[0] = y.x, part[1] = y.y, part[2] = y.z, part[3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(o);
+          part[0] = y.x, part[1] = y.y;
+        }
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(wgt, o[c], acc[c]);
+        for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(wi, part[c], acc[c]);
+      }
     }
     const size_t row = (static_cast<size_t>(b) * p.s.heads + h) * group + g;
     uint32_t* out = static_cast<uint32_t*>(p.a.out) + row * (D / 2) + lane * (D / 64);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) out[c] = pack_bf16x2(acc[2 * c], acc[2 * c + 1]);
-    if (lane == 0) {
-      if (p.a.lse) p.a.lse[row] = lse * 0.69314718055994531f;  // ln 2
-      if (nlse) nlse[g] = -lse;
-    }
+  }
+  if (blockIdx.y == 0 && lane < group) {
+    if (p.a.lse) p.a.lse[static_cast<size_t>(unit) * group + lane] = lse_of * 0.69314718055994531f;  // ln 2
+    if (nlse) nlse[lane] = -lse_of;
   }
   if (!p.w.logits) return;
-  __syncthreads();
-  const int len = v.meta[2 * seq];
-  const float* L = p.w.logits + (static_cast<size_t>(b) * p.s.heads + h) * group * v.cap;
+  float* lses = s_lse[threadIdx.x >> 5];
+  lses[lane] = lse_of;
+  __syncwarp();
+  const float* L = p.w.logits + static_cast<size_t>(unit) * group * v.cap;
   float* score = v.score + (static_cast<size_t>(seq) * v.heads + h) * v.cap;
-  for (int j = j0; j < len; j += step) {
-    float sum = 0.f;
-    for (int g = 0; g < group; ++g) sum += ex2(L[static_cast<size_t>(g) * v.cap + j] - s_lse[g]);
-    score[j] += sum;
+  for (int j = (blockIdx.y * 32 + lane) * 4; j < len; j += gridDim.y * 128) {
+    // four slots a lane: a sequence's rows end at a multiple of its page
+    float4 sum = *reinterpret_cast<float4*>(score + j);
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < group; ++g) {
+      const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(g) * v.cap + j);
+      const float n = lses[g];
+      a[0] += ex2(y.x - n);
+      a[1] += ex2(y.y - n);
+      a[2] += ex2(y.z - n);
+      a[3] += ex2(y.w - n);
+    }
+    sum.x += a[0];
+    if (j + 1 < len) sum.y += a[1];
+    if (j + 2 < len) sum.z += a[2];
+    if (j + 3 < len) sum.w += a[3];
+    *reinterpret_cast<float4*>(score + j) = sum;
   }
+}
+
+// Scores of a prefix with few rows, from their logits: block (head; keys), rows in order.
+constexpr int kSumThreads = 128;
+
+__global__ void __launch_bounds__(kSumThreads)
+    pool_prefix_sum_kernel(const __grid_constant__ AttendParams p) {
+  const PoolView& v = p.a.v;
+  const int plen = max(0, checked_length(v, p.a.prefix, false));
+  const int h = blockIdx.x, rows = p.s.n * p.s.group, j = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
+  grid_dependency_wait();
+  if (j >= plen) return;
+  const float* L = p.w.plogits + static_cast<size_t>(h) * rows * v.cap + j;
+  const float* nlse = p.w.nlse + static_cast<size_t>(h) * TILE_ROWS;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    const float n = nlse[i];
+    const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(i) * v.cap);
+    if (n == -INFINITY) continue;  // not counted, whatever its logits are
+    a[0] += ex2(y.x + n);
+    a[1] += ex2(y.y + n);
+    a[2] += ex2(y.z + n);
+    a[3] += ex2(y.w + n);
+  }
+  float* score = v.score + (static_cast<size_t>(p.a.prefix) * v.heads + h) * v.cap + j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i < plen) score[i] += a[i];
 }
 
 // ------------------------------------------------------------------ host side
@@ -745,7 +831,7 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, void* base, Atte
   w.seq = reinterpret_cast<int*>(take(s.n * sizeof(int)));
   w.cum = reinterpret_cast<int*>(take((s.n + 1) * sizeof(int)));
   w.nlse = reinterpret_cast<float*>(
-      take(s.blocks && !s.few ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
+      take(s.blocks && accumulate ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
   w.pml = reinterpret_cast<float2*>(take(prow * sizeof(float2)));
   w.tml = reinterpret_cast<float2*>(take(trow * sizeof(float2)));
   w.po = reinterpret_cast<float*>(take(prow * s.d * sizeof(float)));
@@ -781,16 +867,19 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  // the prefix's scores by blocks of their own; enough chunks for the scores of few long rows
-  const bool own_prefix = p.s.few && p.a.accumulate;
-  const int units = p.s.n * p.s.heads + (own_prefix ? p.s.heads : 0);
+  // enough chunks of keys for the scores of few long rows
+  const int units = p.s.n * p.s.heads, blocks = (units + kFinishWarps - 1) / kFinishWarps;
   const int chunks = p.a.accumulate
-                         ? std::max(1, std::min(8 * p.s.grid / units, (p.a.v.cap + 511) / 512))
+                         ? std::max(1, std::min(8 * p.s.grid / blocks, (p.a.v.cap + 511) / 512))
                          : 1;
-  if ((e = launch_after(pool_finish_kernel<D>, dim3(units, chunks), kFinishThreads, 0, stream, p)) !=
-      cudaSuccess)
+  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks, chunks), 32 * kFinishWarps, 0, stream,
+                        p)) != cudaSuccess)
     return e;
-  return many && p.a.accumulate ? pool_prefix_score(p, stream) : cudaSuccess;
+  if (!p.a.accumulate || p.a.prefix < 0) return cudaSuccess;
+  if (many) return pool_prefix_score(p, stream);
+  return launch_after(pool_prefix_sum_kernel,
+                      dim3(p.s.heads, (p.a.v.cap + 4 * kSumThreads - 1) / (4 * kSumThreads)),
+                      kSumThreads, 0, stream, p);
 }
 
 }  // namespace

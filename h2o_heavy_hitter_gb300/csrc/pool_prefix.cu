@@ -615,15 +615,16 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         const float ks = F8 ? p.qscale * scales[(g % kScaleTiles<false>) * 2 * TILE_KEYS + r] : p.qscale;
         float part[4] = {0.f, 0.f, 0.f, 0.f};
         for (int c = 0; c < rows; c += 32) {
+          const float mine = c + lane < rows ? nl[c + lane] : -INFINITY;
           uint32_t s[32];
           tmem_ld32(tmem + lane_off + buf * 128 + c, s);
           tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            if (c + x >= rows) break;  // uniform
-            const float n = nl[c + x];
-            // rows that are not counted may hold anything
-            part[x & 3] += n == -INFINITY ? 0.f : ex2(fmaf(__uint_as_float(s[x]), ks, n));
+            const float n = __shfl_sync(0xffffffffu, mine, x);
+            // rows that are not counted, and columns that are none, may hold anything
+            const float e = ex2(fmaf(__uint_as_float(s[x]), ks, n));
+            part[x & 3] += n == -INFINITY ? 0.f : e;
           }
         }
         acc += (part[0] + part[1]) + (part[2] + part[3]);

@@ -32,7 +32,7 @@ struct Shape {
 struct AttendScratch {
   int* seq;        // [n] sequence of an entry, -1 skipped
   int* cum;        // [n + 1] own tiles of the entries before
-  float* nlse;     // [heads][nq][128] -lse (base 2) of a prefix row, -inf: not counted
+  float* nlse;     // [heads][nq][128] -lse (base 2) of a prefix row, -inf: not counted (accumulate only)
   float2* pml;     // prefix pieces {max, sum}: many rows [heads * blocks + grid][2][128],
                    // few rows [heads + grid][kFewRows]
   float2* tml;     // own pieces [n * heads + grid][group]
