@@ -657,107 +657,111 @@ __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int 
   return x;
 }
 
-// A warp per (entry, key head), and per chunk of keys: joins the rows of the
-// group in the order of the pieces and adds the probabilities of the own tokens
-// to their scores. Every chunk computes the lse's it needs, chunk 0 writes.
+// Per (entry, key head) and chunk of keys, one to four warps by the size of the
+// group: join the rows, a warp each, in the order of the pieces, and add the
+// probabilities of the own tokens to their scores. Every chunk computes the lse's
+// it needs, chunk 0 writes.
 template <int D>
 __global__ void __launch_bounds__(32 * kFinishWarps)
-    pool_finish_kernel(const __grid_constant__ AttendParams p) {
+    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps) {
   grid_dependency_wait();
   grid_launch_dependents();
+  __shared__ float s_lse[kFinishWarps][kFewRows];
   const PoolView& v = p.a.v;
-  const int group = p.s.group, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * kFinishWarps + (threadIdx.x >> 5);
-  if (unit >= p.s.n * p.s.heads) return;
-  const int b = unit / p.s.heads, h = unit - b * p.s.heads, seq = p.w.seq[b];
+  const int group = p.s.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int local = warp / unit_warps, sub = warp - local * unit_warps;
+  const int unit = blockIdx.x * (kFinishWarps / unit_warps) + local;
+  const bool in = unit < p.s.n * p.s.heads;
+  const int b = in ? unit / p.s.heads : 0, h = in ? unit - b * p.s.heads : 0;
+  const int seq = in ? p.w.seq[b] : -1;
   float* nlse = nullptr;  // for the scores of the prefix
-  if (p.w.nlse && blockIdx.y == 0)
+  if (in && p.w.nlse && blockIdx.y == 0)
     nlse = p.w.nlse + (static_cast<size_t>(h) * p.s.nq + b / p.s.per_tile) * TILE_ROWS +
            b % p.s.per_tile * group;
-  if (seq < 0) {
-    if (nlse && lane < group) nlse[lane] = -INFINITY;
-    return;
-  }
-  const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
-  const int len = v.meta[2 * seq];
-  const Records x = records_of(p, b, h, plen, lane);
-  const int all = x.prefix + x.own;
-  __shared__ float s_lse[kFinishWarps][kFewRows];
-  float lse_of = -INFINITY;  // of row `lane`
-  for (int g = 0; g < group; ++g) {
-    auto record = [&](int i) -> size_t {
-      return (i < x.prefix ? x.pbase + i * x.pstep : x.obase + static_cast<size_t>(i - x.prefix) * group) + g;
-    };
-    auto ml = [&](int i) -> float2 { return (i < x.prefix ? p.w.pml : p.w.tml)[record(i)]; };
-    float m = -INFINITY, l = 0.f;
-    float2 first = make_float2(-INFINITY, 0.f);  // of record `lane`
-    for (int i = lane; i < all; i += 32) {
-      const float2 y = ml(i);
-      if (i < 32) first = y;
-      const float top = fmaxf(m, y.x);
-      if (top != -INFINITY) {
-        l = l * ex2(m - top) + y.y * ex2(y.x - top);
-        m = top;
-      } else {
-        l += y.y;  // a NaN sum stays one
-      }
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
-      const float top = fmaxf(m, mo);
-      if (top != -INFINITY)
-        l = l * ex2(m - top) + lo * ex2(mo - top);
-      else
-        l += lo;
-      m = top;
-    }
-    const float lse = __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
-    if (lane == g) lse_of = lse;
-    if (blockIdx.y) continue;
-    float acc[D / 32] = {};
-    for (int i0 = 0; i0 < all; i0 += 32) {
-      const float mine = i0 == 0 ? first.x : i0 + lane < all ? ml(i0 + lane).x : -INFINITY;
-      const float wgt = all ? ex2(mine - lse) : 0.f;
-      const int n = min(32, all - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, wgt, i);
-        const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(i0 + i) * D + lane * (D / 32);
-        float part[D / 32];
-        if constexpr (D == 128) {
-          const float4 y = *reinterpret_cast<const float4*>(o);
-          part[0] = y.x, part[1] = y.y, part[2] = y.z, part[3] = y.w;
+  int len = 0;
+  if (seq >= 0) {
+    const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
+    len = v.meta[2 * seq];
+    const Records x = records_of(p, b, h, plen, lane);
+    const int all = x.prefix + x.own;
+    for (int g = sub; g < group; g += unit_warps) {
+      auto record = [&](int i) -> size_t {
+        return (i < x.prefix ? x.pbase + i * x.pstep : x.obase + static_cast<size_t>(i - x.prefix) * group) + g;
+      };
+      auto ml = [&](int i) -> float2 { return (i < x.prefix ? p.w.pml : p.w.tml)[record(i)]; };
+      float m = -INFINITY, l = 0.f;
+      float2 first = make_float2(-INFINITY, 0.f);  // of record `lane`
+      for (int i = lane; i < all; i += 32) {
+        const float2 y = ml(i);
+        if (i < 32) first = y;
+        const float top = fmaxf(m, y.x);
+        if (top != -INFINITY) {
+          l = l * ex2(m - top) + y.y * ex2(y.x - top);
+          m = top;
         } else {
-          const float2 y = *reinterpret_cast<const float2*>(o);
-          part[0] = y.x, part[1] = y.y;
+          l += y.y;  // a NaN sum stays one
         }
+      }
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(wi, part[c], acc[c]);
+      for (int off = 16; off; off >>= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
+        const float top = fmaxf(m, mo);
+        if (top != -INFINITY)
+          l = l * ex2(m - top) + lo * ex2(mo - top);
+        else
+          l += lo;
+        m = top;
+      }
+      const float lse = __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
+      if (lane == 0) s_lse[local][g] = lse;
+      if (blockIdx.y) continue;
+      float acc[D / 32] = {};
+      for (int i0 = 0; i0 < all; i0 += 32) {
+        const float mine = i0 == 0 ? first.x : i0 + lane < all ? ml(i0 + lane).x : -INFINITY;
+        const float wgt = all ? ex2(mine - lse) : 0.f;
+        const int n = min(32, all - i0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, wgt, i);
+          const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(i0 + i) * D + lane * (D / 32);
+          float part[D / 32];
+          if constexpr (D == 128) {
+            const float4 y = *reinterpret_cast<const float4*>(o);
+            part[0] = y.x, part[1] = y.y, part[2] = y.z, part[3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(o);
+            part[0] = y.x, part[1] = y.y;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(wi, part[c], acc[c]);
+        }
+      }
+      const size_t row = static_cast<size_t>(unit) * group + g;
+      uint32_t* out = static_cast<uint32_t*>(p.a.out) + row * (D / 2) + lane * (D / 64);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) out[c] = pack_bf16x2(acc[2 * c], acc[2 * c + 1]);
+      if (lane == 0) {
+        if (p.a.lse) p.a.lse[row] = lse * 0.69314718055994531f;  // ln 2
+        if (nlse) nlse[g] = -lse;
       }
     }
-    const size_t row = (static_cast<size_t>(b) * p.s.heads + h) * group + g;
-    uint32_t* out = static_cast<uint32_t*>(p.a.out) + row * (D / 2) + lane * (D / 64);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) out[c] = pack_bf16x2(acc[2 * c], acc[2 * c + 1]);
-  }
-  if (blockIdx.y == 0 && lane < group) {
-    if (p.a.lse) p.a.lse[static_cast<size_t>(unit) * group + lane] = lse_of * 0.69314718055994531f;  // ln 2
-    if (nlse) nlse[lane] = -lse_of;
+  } else if (nlse && sub == 0 && lane < group) {
+    nlse[lane] = -INFINITY;
   }
   if (!p.w.logits) return;
-  float* lses = s_lse[threadIdx.x >> 5];
-  lses[lane] = lse_of;
-  __syncwarp();
+  __syncthreads();
+  if (seq < 0) return;
   const float* L = p.w.logits + static_cast<size_t>(unit) * group * v.cap;
   float* score = v.score + (static_cast<size_t>(seq) * v.heads + h) * v.cap;
-  for (int j = (blockIdx.y * 32 + lane) * 4; j < len; j += gridDim.y * 128) {
+  const int step = gridDim.y * unit_warps * 128;
+  for (int j = ((blockIdx.y * unit_warps + sub) * 32 + lane) * 4; j < len; j += step) {
     // four slots a lane: a sequence's rows end at a multiple of its page
     float4 sum = *reinterpret_cast<float4*>(score + j);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int g = 0; g < group; ++g) {
       const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(g) * v.cap + j);
-      const float n = lses[g];
+      const float n = s_lse[local][g];
       a[0] += ex2(y.x - n);
       a[1] += ex2(y.y - n);
       a[2] += ex2(y.z - n);
@@ -867,13 +871,14 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
+  const int unit_warps = p.s.group >= 4 ? 4 : p.s.group >= 2 ? 2 : 1, units = p.s.n * p.s.heads;
+  const int blocks = (units * unit_warps + kFinishWarps - 1) / kFinishWarps;
   // enough chunks of keys for the scores of few long rows
-  const int units = p.s.n * p.s.heads, blocks = (units + kFinishWarps - 1) / kFinishWarps;
   const int chunks = p.a.accumulate
                          ? std::max(1, std::min(8 * p.s.grid / blocks, (p.a.v.cap + 511) / 512))
                          : 1;
-  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks, chunks), 32 * kFinishWarps, 0, stream,
-                        p)) != cudaSuccess)
+  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks, chunks), 32 * kFinishWarps, 0, stream, p,
+                        unit_warps)) != cudaSuccess)
     return e;
   if (!p.a.accumulate || p.a.prefix < 0) return cudaSuccess;
   if (many) return pool_prefix_score(p, stream);

@@ -187,27 +187,47 @@ __device__ void produce_e4m3(const PoolView& v, uint8_t* ring, RingBars<R>& bars
   uint4 raw[PF][NCH];
   float sc[PF];
   bool live[PF];
-  bool value = false, more = true;  // the next slot to load
-  auto load = [&](uint4 (&x)[NCH], float& s) -> bool {
-    if (!VALUES || !value) more = more && c.step();
-    if (!more) return false;
+  // The pages of the next tile are looked up while this one's tokens are on their
+  // way: ahead, what `next` holds; then the slots (token, head) of this tile's rows.
+  int next[NCH + 1];  // pages of this thread's rows, and of the row whose scale it loads
+  int32_t slot[NCH + 1];
+  auto row_of = [&](int i) { return i < NCH ? (tid + NT * i) / CPR : tid; };
+  bool more = c.step();
+  auto look_up = [&]() {
     const int valid = c.len - c.kt * TILE_KEYS;
+    const int32_t* pages = v.table + static_cast<size_t>(c.seq) * v.width + c.kt * per;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int q = tid + NT * i, row = q / CPR, col = q % CPR;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (row < valid) {
-        const int page = checked_page(v, c.seq, c.kt * per + (row >> v.shift));
-        const size_t slot = ((static_cast<size_t>(page) * v.heads + c.h) << v.shift) + (row & (v.page - 1));
-        x[i] = *reinterpret_cast<const uint4*>((value ? v.V : v.K) + slot * D + col * 16);
+    for (int i = 0; i <= NCH; ++i) {
+      const int row = row_of(i);
+      next[i] = row < TILE_KEYS && row < valid ? pages[row >> v.shift] : -1;
+    }
+  };
+  if (more) look_up();
+  bool value = false;  // the next slot to load
+  auto load = [&](uint4 (&x)[NCH], float& s) -> bool {
+    if (!VALUES || !value) {
+      if (!more) return false;
+      const int valid = c.len - c.kt * TILE_KEYS;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i <= NCH; ++i) {
+        const int row = row_of(i);
+        const bool in = row < TILE_KEYS && row < valid;
+        const bool held = next[i] >= 0 && next[i] < v.pages;
+        bad |= in && !held;
+        slot[i] = in ? (((held ? next[i] : 0) * v.heads + c.h) << v.shift) + (row & (v.page - 1)) : -1;
       }
+      if (bad) atomicOr(v.err, kErrBadState);  // page 0 is read in its place
+      more = c.step();
+      if (more) look_up();
     }
-    s = 0.f;
-    if (tid < TILE_KEYS && tid < valid) {
-      const int page = checked_page(v, c.seq, c.kt * per + (tid >> v.shift));
-      const size_t slot = ((static_cast<size_t>(page) * v.heads + c.h) << v.shift) + (tid & (v.page - 1));
-      s = (value ? v.vscale : v.kscale)[slot];
-    }
+    const uint8_t* base = value ? v.V : v.K;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      x[i] = slot[i] >= 0 ? *reinterpret_cast<const uint4*>(base + static_cast<size_t>(slot[i]) * D +
+                                                             (tid + NT * i) % CPR * 16)
+                          : make_uint4(0, 0, 0, 0);
+    s = slot[NCH] >= 0 ? (value ? v.vscale : v.kscale)[slot[NCH]] : 0.f;
     if (VALUES) value = !value;
     return true;
   };
