@@ -180,8 +180,8 @@ struct TileCursor {
 };
 
 // ------------------------------------------------------------------ few rows
-// Warps: 0 tiles by TMA (bf16 pool), 1 MMA and TMEM, 2 queries, 3..6 and 7..10 the
-// two warpgroups, one per TMEM lane quadrant, 11..18 tiles from E4M3 codes.
+// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 and 7..10 the
+// two warpgroups, one per TMEM lane quadrant, 11..18 E4M3 codes to bf16 tiles.
 constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpRows = 3, kWarpCodes = 11;
 constexpr int kCodeThreads = 256;
 constexpr int kQBox = kFewRows * 128;  // rows x 64 channels (or keys) of an operand with few rows
@@ -190,19 +190,22 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = F8 ? 4 : D == 128 ? 5 : 10;
+  static constexpr int R = (F8 ? 2 : 5) * (128 / D);
+  static constexpr int S = F8 ? 5 * (128 / D) : 1;  // slots of codes
+  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
   static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
   static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
   static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(R) * TILE + 2 * Q + 4 * P + SCALES +
+  static constexpr size_t SMEM = static_cast<size_t>(R) * TILE + 2 * Q + 4 * P + CODES + SCALES +
                                  sizeof(List) + 3072 + 1024;
   // TMEM: S^T of warpgroup t in columns 64 t + 32 (0, 1), its O^T at 128 + 32 t
   static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
 };
 
-template <int R>
+template <int R, int S>
 struct Bars {
   RingBars<R> ring;
+  CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];  // by unit
   uint64_t s_full[2][2];           // [warpgroup][buffer]
   uint64_t p_ready[2][2];
@@ -327,10 +330,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   uint8_t* ring = smem;
   uint8_t* sQ = ring + R * C::TILE;
   uint8_t* sP = sQ + 2 * C::Q;
-  float* scales = reinterpret_cast<float*>(sP + 4 * C::P);
+  uint8_t* codes = sP + 4 * C::P;
+  float* scales = reinterpret_cast<float*>(codes + C::CODES);
   List& list = *reinterpret_cast<List*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  auto* bars = reinterpret_cast<Bars<R>*>(&list + 1);
-  static_assert(sizeof(Bars<R>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
+  auto* bars = reinterpret_cast<Bars<R, C::S>*>(&list + 1);
+  static_assert(sizeof(Bars<R, C::S>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -338,6 +342,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     for (int i = 0; i < R; ++i) {
       mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
       mbar_init(&bars->ring.empty[i], 1);
+    }
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(&bars->codes.full[i], 1);
+      mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
@@ -361,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     tma_prefetch_map(&tq);
     tma_prefetch_map(&t1);
   }
-  if (!F8 && warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tk);
     tma_prefetch_map(&tv);
   }
@@ -377,11 +385,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   const uint32_t tmem = bars->tmem;
   Walk w(p, list, plen, cta);
 
-  if (!F8 && warp == 0) {
-    produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
+  if (warp == 0) {
+    if constexpr (F8)
+      fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
+    else
+      produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    produce_e4m3<D, R, true, kCodeThreads>(v, ring, bars->ring, scales, TileCursor(w),
-                                           threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, R, C::S, true, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales,
+                                                  TileCursor(w), threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       for (int e = 0; w.next(); ++e) {
@@ -848,14 +859,12 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, void* base, Atte
 
 template <int D, bool F8>
 cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, t1, tk{}, tv{};
+  CUtensorMap tq, t1, tk, tv;
   cudaError_t e;
   if ((e = query_map(&tq, p.a, p.s.few ? p.s.n : 1)) != cudaSuccess) return e;
   if ((e = query_map(&t1, p.a, 1)) != cudaSuccess) return e;
-  if (!F8) {
-    if ((e = page_map(&tk, p.a.v.K, p.a.v)) != cudaSuccess) return e;
-    if ((e = page_map(&tv, p.a.v.V, p.a.v)) != cudaSuccess) return e;
-  }
+  if ((e = page_map(&tk, p.a.v.K, p.a.v)) != cudaSuccess) return e;
+  if ((e = page_map(&tv, p.a.v.V, p.a.v)) != cudaSuccess) return e;
   const bool many = p.a.prefix >= 0 && !p.s.few;
   if (many && (e = pool_prefix(p, stream)) != cudaSuccess) return e;
   using C = Cfg<D, F8>;
@@ -892,13 +901,15 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
 cudaError_t page_map(CUtensorMap* m, const void* base, const PoolView& v) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
+  const bool codes = v.kscale != nullptr;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(v.d),
                         static_cast<cuuint64_t>(v.pages) * v.heads * v.page};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(v.d) * 2};
-  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(v.page)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(v.row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(codes ? v.d : 64), static_cast<cuuint32_t>(v.page)};
   cuuint32_t es[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  CUresult r = enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

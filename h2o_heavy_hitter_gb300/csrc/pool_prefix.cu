@@ -22,8 +22,8 @@ namespace h2o {
 namespace {
 
 // ------------------------------------------------------------------ attention
-// Warps: 0 tiles by TMA (bf16 pool), 1 MMA and TMEM, 2 queries, 3..6 half or row
-// tile 0, 7..10: 1 (one per TMEM lane quadrant), 11..14 tiles from E4M3 codes.
+// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 half or row
+// tile 0, 7..10: 1 (one per TMEM lane quadrant), 11..14 E4M3 codes to bf16 tiles.
 constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpSoftmax = 3, kWarpCodes = 11;
 constexpr int kCodeThreads = 128;
 
@@ -31,15 +31,18 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = (F8 ? 4 : 5) * (D == 128 ? 1 : 2);
+  static constexpr int R = (F8 ? 2 : 5) * (128 / D);
+  static constexpr int S = F8 ? 4 * (128 / D) : 1;  // slots of codes
+  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
   static constexpr uint32_t O_COL = 256;  // S buffers at columns 0 and 128, O of half t at 256 + 128 t
   static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + SCALES + 1024 + 1024;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + CODES + SCALES + 1024 + 1024;
 };
 
-template <int R>
+template <int R, int S>
 struct Bars {
   RingBars<R> ring;
+  CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
   uint64_t o_last[2], o_free[2];               // one phase per unit
@@ -103,9 +106,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
   uint8_t* ring = smem + 2 * C::TILE;
-  float* scales = reinterpret_cast<float*>(ring + R * C::TILE);
-  auto* bars = reinterpret_cast<Bars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  static_assert(sizeof(Bars<R>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
+  uint8_t* codes = ring + R * C::TILE;
+  float* scales = reinterpret_cast<float*>(codes + C::CODES);
+  auto* bars = reinterpret_cast<Bars<R, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(Bars<R, C::S>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -123,6 +127,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
       mbar_init(&bars->ring.empty[i], 1);
     }
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(&bars->codes.full[i], 1);
+      mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
+    }
     fence_barrier_init();
   }
   if (warp == kWarpMMA) {
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     tmem_relinquish();
   }
   if (warp == kWarpQ && lane == 0) tma_prefetch_map(&tq);
-  if (!F8 && warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tk);
     tma_prefetch_map(&tv);
   }
@@ -142,11 +150,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   Walk w(p, plen, cta);
   grid_launch_dependents();  // the few-rows kernel, as SMs become free
 
-  if (!F8 && warp == 0) {
-    produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
+  if (warp == 0) {
+    if constexpr (F8)
+      fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
+    else
+      produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    produce_e4m3<D, R, true, kCodeThreads>(v, ring, bars->ring, scales, TileCursor(w),
-                                           threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, R, C::S, true, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales,
+                                                  TileCursor(w), threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t qn = 0;
@@ -437,20 +448,23 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ scores of the prefix
-// Warps: 0 tiles by TMA, 1 MMA and TMEM, 2 queries, 3..6 even key tiles, 7..10 odd
-// ones, 11..14 tiles from E4M3 codes.
+// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 even key tiles, 7..10 odd
+// ones, 11..14 E4M3 codes to bf16 tiles.
 template <int D, bool F8>
 struct ScoreCfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = 4 * (D == 128 ? 1 : 2);
+  static constexpr int R = (F8 ? 2 : 4) * (128 / D);
+  static constexpr int S = F8 ? 4 * (128 / D) : 1;
+  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
   static constexpr int SCALES = F8 ? kScaleTiles<false> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + SCALES + 1024 + 1024;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + CODES + SCALES + 1024 + 1024;
 };
 
-template <int R>
+template <int R, int S>
 struct ScoreBars {
   RingBars<R> ring;
+  CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
   uint32_t tmem;
@@ -490,15 +504,20 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
   uint8_t* ring = smem + 2 * C::TILE;
-  float* scales = reinterpret_cast<float*>(ring + R * C::TILE);
-  auto* bars = reinterpret_cast<ScoreBars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  static_assert(sizeof(ScoreBars<R>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
+  uint8_t* codes = ring + R * C::TILE;
+  float* scales = reinterpret_cast<float*>(codes + C::CODES);
+  auto* bars = reinterpret_cast<ScoreBars<R, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(ScoreBars<R, C::S>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
       mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
       mbar_init(&bars->ring.empty[i], 1);
+    }
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(&bars->codes.full[i], 1);
+      mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
@@ -517,7 +536,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tq);
-    if (!F8) tma_prefetch_map(&tk);
+    tma_prefetch_map(&tk);
   }
   tc_fence_before();
   __syncthreads();
@@ -528,11 +547,14 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   const bool stay = nq <= 2;
   KeyCursor k(p, len, blockIdx.x);
 
-  if (!F8 && warp == 0) {
-    produce_tma<D, R, false>(v, &tk, nullptr, ring, bars->ring, k);
+  if (warp == 0) {
+    if constexpr (F8)
+      fetch_codes<D, C::S, false>(v, &tk, nullptr, codes, bars->codes, k);
+    else
+      produce_tma<D, R, false>(v, &tk, nullptr, ring, bars->ring, k);
   } else if (F8 && warp >= kWarpCodes) {
-    produce_e4m3<D, R, false, kCodeThreads>(v, ring, bars->ring, scales, k,
-                                            threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, R, C::S, false, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales, k,
+                                                   threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t f = 0;
@@ -648,14 +670,14 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
 // ------------------------------------------------------------------ host side
 cudaError_t maps(const AttendParams& p, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
   cudaError_t e = query_map(tq, p.a, p.s.per_tile);
-  if (e == cudaSuccess && !p.a.v.kscale) e = page_map(tk, p.a.v.K, p.a.v);
-  if (e == cudaSuccess && !p.a.v.kscale && tv) e = page_map(tv, p.a.v.V, p.a.v);
+  if (e == cudaSuccess) e = page_map(tk, p.a.v.K, p.a.v);
+  if (e == cudaSuccess && tv) e = page_map(tv, p.a.v.V, p.a.v);
   return e;
 }
 
 template <int D, bool F8>
 cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, tk{}, tv{};
+  CUtensorMap tq, tk, tv;
   cudaError_t e = maps(p, &tq, &tk, &tv);
   if (e != cudaSuccess) return e;
   using C = Cfg<D, F8>;
@@ -669,7 +691,7 @@ cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
 
 template <int D, bool F8>
 cudaError_t score_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, tk{};
+  CUtensorMap tq, tk;
   cudaError_t e = maps(p, &tq, &tk, nullptr);
   if (e != cudaSuccess) return e;
   using C = ScoreCfg<D, F8>;

@@ -54,8 +54,8 @@ struct AttendParams {
 cudaError_t pool_prefix(const AttendParams& p, cudaStream_t stream);
 cudaError_t pool_prefix_score(const AttendParams& p, cudaStream_t stream);
 // Tensor maps (pool_attend.cu): queries [n][heads][group][d] in boxes of
-// `entries` groups of one head x 64 channels; a bf16 pool's keys or values in
-// boxes of a page's tokens x 64 channels.
+// `entries` groups of one head x 64 channels; a pool's keys or values in boxes of
+// a page's tokens x 64 channels (bf16, 128-byte swizzle) or x all codes (E4M3).
 cudaError_t query_map(CUtensorMap* m, const AttendArgs& a, int entries);
 cudaError_t page_map(CUtensorMap* m, const void* base, const PoolView& v);
 
@@ -172,79 +172,79 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
   return r;
 }
 
-// E4M3 pool, NT threads: codes from global memory through registers, PF slots
-// ahead, into the slot as bf16; rows behind the last token become zero. The
-// scales of tile g go to scales[g % kScaleTiles<VALUES>][0: keys, 1: values][128].
-// Each warp arrives once on the slot's barrier.
-template <int D, int R, bool VALUES, int NT, typename Cursor>
-__device__ void produce_e4m3(const PoolView& v, uint8_t* ring, RingBars<R>& bars, float* scales,
-                             Cursor c, int tid) {
+// E4M3 pool: a second ring of S slots takes the codes as they are (128 tokens of
+// D bytes, then 128 scales), by TMA from one warp, like produce_tma; NT other
+// threads turn each into a slot of bf16. (Codes loaded through registers of the
+// converting threads, three slots ahead, took 10,000 clocks a tile of keys and
+// values against 2,500 this way: every use of one load waited for all of them.)
+template <int S>
+struct CodeBars {
+  uint64_t full[S], empty[S];  // empty: an arrival per converting warp
+};
+
+template <int D>
+constexpr int kCodeSlot = TILE_KEYS * D + TILE_KEYS * 4;
+
+template <int D, int S, bool VALUES, typename Cursor>
+__device__ void fetch_codes(const PoolView& v, const CUtensorMap* tk, const CUtensorMap* tv,
+                            uint8_t* codes, CodeBars<S>& bars, Cursor c) {
+  const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
+  uint32_t n = 0;
+  while (c.step()) {
+    const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
+    const int row = lane < boxes
+                        ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
+                        : 0;
+#pragma unroll
+    for (int kv = 0; kv < (VALUES ? 2 : 1); ++kv, ++n) {
+      const uint32_t st = n % S;
+      if (n >= S && !warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return;
+      if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
+      __syncwarp();
+      if (lane < boxes) {
+        uint8_t* dst = codes + st * kCodeSlot<D>;
+        tma_load_2d(dst + (lane << v.shift) * D, kv ? tv : tk, 0, row, &bars.full[st]);
+        bulk_copy_g2s(dst + TILE_KEYS * D + (lane << v.shift) * 4, (kv ? v.vscale : v.kscale) + row,
+                      v.page * 4, &bars.full[st]);
+      }
+    }
+  }
+}
+
+// Rows behind the last token become zero. The scales of tile g go to
+// scales[g % kScaleTiles<VALUES>][0: keys, 1: values][128]. Each warp arrives once
+// on the slot's barrier.
+template <int D, int R, int S, bool VALUES, int NT, typename Cursor>
+__device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<S>& from,
+                              uint8_t* ring, RingBars<R>& to, float* scales, Cursor c, int tid) {
   constexpr int BYTES = TILE_KEYS * D * 2;
   constexpr int CPR = D / 16;               // 16-byte chunks of codes per token
   constexpr int NCH = TILE_KEYS * CPR / NT;  // chunks per thread and slot
-  constexpr int PF = NCH > 2 ? 3 : 4;  // what the registers of a 600-thread block hold
-  const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  uint4 raw[PF][NCH];
-  float sc[PF];
-  bool live[PF];
-  // The pages of the next tile are looked up while this one's tokens are on their
-  // way: ahead, what `next` holds; then the slots (token, head) of this tile's rows.
-  int next[NCH + 1];  // pages of this thread's rows, and of the row whose scale it loads
-  int32_t slot[NCH + 1];
-  auto row_of = [&](int i) { return i < NCH ? (tid + NT * i) / CPR : tid; };
-  bool more = c.step();
-  auto look_up = [&]() {
+  const int lane = threadIdx.x & 31;
+  uint32_t n = 0;
+  while (c.step()) {
     const int valid = c.len - c.kt * TILE_KEYS;
-    const int32_t* pages = v.table + static_cast<size_t>(c.seq) * v.width + c.kt * per;
 #pragma unroll
-    for (int i = 0; i <= NCH; ++i) {
-      const int row = row_of(i);
-      next[i] = row < TILE_KEYS && row < valid ? pages[row >> v.shift] : -1;
-    }
-  };
-  if (more) look_up();
-  bool value = false;  // the next slot to load
-  auto load = [&](uint4 (&x)[NCH], float& s) -> bool {
-    if (!VALUES || !value) {
-      if (!more) return false;
-      const int valid = c.len - c.kt * TILE_KEYS;
-      bool bad = false;
+    for (int kv = 0; kv < (VALUES ? 2 : 1); ++kv, ++n) {
+      const uint32_t sc = n % S, st = n % R;
+      if (!warp_wait(&from.full[sc], (n / S) & 1, v.err)) return;
+      const uint8_t* src = codes + sc * kCodeSlot<D>;
+      uint4 x[NCH];
 #pragma unroll
-      for (int i = 0; i <= NCH; ++i) {
-        const int row = row_of(i);
-        const bool in = row < TILE_KEYS && row < valid;
-        const bool held = next[i] >= 0 && next[i] < v.pages;
-        bad |= in && !held;
-        slot[i] = in ? (((held ? next[i] : 0) * v.heads + c.h) << v.shift) + (row & (v.page - 1)) : -1;
+      for (int i = 0; i < NCH; ++i) {
+        x[i] = reinterpret_cast<const uint4*>(src)[tid + NT * i];
+        if ((tid + NT * i) / CPR >= valid) x[i] = make_uint4(0, 0, 0, 0);
       }
-      if (bad) atomicOr(v.err, kErrBadState);  // page 0 is read in its place
-      more = c.step();
-      if (more) look_up();
-    }
-    const uint8_t* base = value ? v.V : v.K;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-      x[i] = slot[i] >= 0 ? *reinterpret_cast<const uint4*>(base + static_cast<size_t>(slot[i]) * D +
-                                                             (tid + NT * i) % CPR * 16)
-                          : make_uint4(0, 0, 0, 0);
-    s = slot[NCH] >= 0 ? (value ? v.vscale : v.kscale)[slot[NCH]] : 0.f;
-    if (VALUES) value = !value;
-    return true;
-  };
-#pragma unroll
-  for (int u = 0; u < PF; ++u) live[u] = load(raw[u], sc[u]);
-  for (uint32_t n0 = 0;; n0 += PF) {
-#pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      if (!live[u]) return;
-      const uint32_t n = n0 + u, st = n % R;
-      if (n >= R && !warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
+      if (tid < TILE_KEYS)
+        scales[(((VALUES ? n >> 1 : n) % kScaleTiles<VALUES>) * 2 + kv) * TILE_KEYS + tid] =
+            tid < valid ? reinterpret_cast<const float*>(src + TILE_KEYS * D)[tid] : 0.f;
+      if (n >= R && !warp_wait(&to.empty[st], ((n / R) - 1) & 1, v.err)) return;
       uint8_t* dst = ring + st * BYTES;
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         const int q = tid + NT * i, row = q / CPR, col = q % CPR;
-        const uint2 a = e4m3x4_to_bf16(raw[u][i].x), b = e4m3x4_to_bf16(raw[u][i].y);
-        const uint2 e = e4m3x4_to_bf16(raw[u][i].z), f = e4m3x4_to_bf16(raw[u][i].w);
+        const uint2 a = e4m3x4_to_bf16(x[i].x), b = e4m3x4_to_bf16(x[i].y);
+        const uint2 e = e4m3x4_to_bf16(x[i].z), f = e4m3x4_to_bf16(x[i].w);
         uint8_t* at = dst + (col >> 2) * kBoxBytes + row * 128;
         const int c0 = 2 * (col & 3);
         // the two boxes of a row lie in the same banks: the halves of a row write
@@ -254,13 +254,12 @@ __device__ void produce_e4m3(const PoolView& v, uint8_t* ring, RingBars<R>& bars
         *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? odd : even;
         *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (row & 7)) << 4)) = swap ? even : odd;
       }
-      const uint32_t g = VALUES ? n >> 1 : n;
-      if (tid < TILE_KEYS)
-        scales[((g % kScaleTiles<VALUES>) * 2 + (VALUES ? n & 1 : 0)) * TILE_KEYS + tid] = sc[u];
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.full[st]);
-      live[u] = load(raw[u], sc[u]);
+      if (lane == 0) {
+        mbar_arrive(&to.full[st]);
+        mbar_arrive(&from.empty[sc]);
+      }
     }
   }
 }
