@@ -180,9 +180,10 @@ struct TileCursor {
 };
 
 // ------------------------------------------------------------------ few rows
-// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 and 7..10 the
-// two warpgroups, one per TMEM lane quadrant, 11..18 E4M3 codes to bf16 tiles.
-constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpRows = 3, kWarpCodes = 11;
+// Warps: 0 tiles of keys or codes by TMA, 1 MMA and TMEM, 2 queries, 3 tiles of
+// values, 4..7 and 8..11 the two warpgroups, one per TMEM lane quadrant, 12..19
+// E4M3 codes to bf16 tiles.
+constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpV = 3, kWarpRows = 4, kWarpCodes = 12;
 constexpr int kCodeThreads = 256;
 constexpr int kQBox = kFewRows * 128;  // rows x 64 channels (or keys) of an operand with few rows
 
@@ -190,21 +191,22 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = (F8 ? 2 : 5) * (128 / D);
-  static constexpr int S = F8 ? 5 * (128 / D) : 1;  // slots of codes
+  static constexpr int RK = 2 * (128 / D), RV = (F8 ? 1 : 3) * (128 / D);  // slots of tiles
+  static constexpr int S = F8 ? 3 * (128 / D) : 1;                         // slots of codes
   static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
   static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
   static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
   static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(R) * TILE + 2 * Q + 4 * P + CODES + SCALES +
+  static constexpr size_t SMEM = static_cast<size_t>(RK + RV) * TILE + 2 * Q + 4 * P + CODES + SCALES +
                                  sizeof(List) + 3072 + 1024;
   // TMEM: S^T of warpgroup t in columns 64 t + 32 (0, 1), its O^T at 128 + 32 t
   static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
 };
 
-template <int R, int S>
+template <int RK, int RV, int S>
 struct Bars {
-  RingBars<R> ring;
+  RingBars<RK> keys;
+  RingBars<RV> values;
   CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];  // by unit
   uint64_t s_full[2][2];           // [warpgroup][buffer]
@@ -324,29 +326,35 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const __grid_constant__ AttendParams p) {
   using C = Cfg<D, F8>;
-  constexpr int R = C::R;
+  constexpr int RK = C::RK, RV = C::RV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint8_t* ring = smem;
-  uint8_t* sQ = ring + R * C::TILE;
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + RK * C::TILE;
+  uint8_t* sQ = sV + RV * C::TILE;
   uint8_t* sP = sQ + 2 * C::Q;
   uint8_t* codes = sP + 4 * C::P;
   float* scales = reinterpret_cast<float*>(codes + C::CODES);
   List& list = *reinterpret_cast<List*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  auto* bars = reinterpret_cast<Bars<R, C::S>*>(&list + 1);
-  static_assert(sizeof(Bars<R, C::S>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
+  auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(&list + 1);
+  static_assert(sizeof(Bars<RK, RV, C::S>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R; ++i) {
-      mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->ring.empty[i], 1);
+    for (int i = 0; i < RK; ++i) {
+      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->keys.empty[i], 1);
+    }
+    for (int i = 0; i < RV; ++i) {
+      mbar_init(&bars->values.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->values.empty[i], 1);
     }
     for (int i = 0; i < C::S; ++i) {
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
@@ -389,10 +397,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     if constexpr (F8)
       fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
     else
-      produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
+      produce_tma<D>(v, &tk, sK, bars->keys, TileCursor(w));
+  } else if (!F8 && warp == kWarpV) {
+    produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, R, C::S, true, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales,
-                                                  TileCursor(w), threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, RK, RV, C::S, true, kCodeThreads>(
+        v, codes, bars->codes, sK, bars->keys, sV, &bars->values, scales, TileCursor(w),
+        threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       for (int e = 0; w.next(); ++e) {
@@ -412,11 +423,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     // of the warpgroup's tile before the last, whose O^T is issued by then; the
     // MMAs of one thread complete in order.
     if (lane == 0) {
-      const uint64_t dk0 = desc_kmajor<D>(ring, 0), dq0 = smem_desc(sQ, 16, 1024);
+      const uint64_t dk0 = desc_kmajor<D>(sK, 0), dq0 = smem_desc(sQ, 16, 1024);
       const uint64_t dp0 = smem_desc(sP, 16, 1024);
       // V^T = the V tile with d as the long side of A (MN-major): 64 channels a box;
       // d = 64 has one box, which then serves as rows 64..127 too (not read)
-      const uint64_t dv0 = smem_desc(ring, D == 128 ? kBoxBytes : 0, 1024);
+      const uint64_t dv0 = smem_desc(sV, D == 128 ? kBoxBytes : 0, 1024);
       uint32_t g = 0, c[2] = {0, 0};  // tiles, and tiles of each warpgroup
       int e = 0;
       bool ok = true;
@@ -426,9 +437,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         uint32_t c, g, idesc;
       } pv;
       auto issue_pv = [&]() -> bool {
-        const uint32_t st = (2 * pv.g + 1) % R, buf = pv.c & 1;
+        const uint32_t st = pv.g % RV, buf = pv.c & 1;
         if (!mbar_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
-            !mbar_wait(&bars->ring.full[st], ((2 * pv.g + 1) / R) & 1, v.err) ||
+            !mbar_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err) ||
             (pv.first && pv.e >= 2 && !mbar_wait(&bars->o_free[pv.t], ((pv.e >> 1) - 1) & 1, v.err)))
           return false;
         tc_fence_after();
@@ -439,7 +450,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
           umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
                   pv.idesc | (1u << 15), (!pv.first || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->ring.empty[st]);
+        umma_commit(&bars->values.empty[st]);
         umma_commit(&bars->pv_done[pv.t][buf]);
         if (pv.last) umma_commit(&bars->o_last[pv.t]);
         return true;
@@ -449,8 +460,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         const uint32_t idesc = idesc_bf16(TILE_KEYS, w.rows() <= 16 ? 16 : 32, 0, 0);
         if (!mbar_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
-          const uint32_t st = (2 * g) % R, buf = c[t] & 1;
-          if (!mbar_wait(&bars->ring.full[st], ((2 * g) / R) & 1, v.err)) {
+          const uint32_t st = g % RK, buf = c[t] & 1;
+          if (!mbar_wait(&bars->keys.full[st], (g / RK) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -462,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             umma_ss(tmem + t * 64 + buf * 32, kb + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
                     qd + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
           umma_commit(&bars->s_full[t][buf]);
-          umma_commit(&bars->ring.empty[st]);
+          umma_commit(&bars->keys.empty[st]);
           if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
           if (pv.live && !issue_pv()) {
             ok = false;
@@ -516,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       }
       float m = -INFINITY, l = 0.f;  // of row `lane`
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g, ++c) {
-        const uint32_t buf = c & 1, st = (2 * g + 1) % R;
+        const uint32_t buf = c & 1, st = g % RV;
         const uint32_t s_tm = tmem + lane_off + t * 64 + buf * 32;
         const int valid = w.len - kt * TILE_KEYS;
         const bool live = r < valid;
@@ -527,7 +538,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         float ks = p.qscale, vs = 1.f;
         if (F8 || valid < TILE_KEYS) {
           // the value tile stays in its slot until this warpgroup's probabilities are used
-          if (!warp_wait(&bars->ring.full[st], ((2 * g + 1) / R) & 1, v.err)) {
+          if (!warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
+                         F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           } else {  // values behind the end count as zero, whatever they are
             for (int i = r; i < (TILE_KEYS - valid) * (D / 8); i += 128) {
               const int row = valid + i / (D / 8), ch = i % (D / 8);
-              *reinterpret_cast<uint4*>(ring + st * C::TILE + (ch >> 3) * kBoxBytes + row * 128 +
+              *reinterpret_cast<uint4*>(sV + st * C::TILE + (ch >> 3) * kBoxBytes + row * 128 +
                                         (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
           }

@@ -22,26 +22,28 @@ namespace h2o {
 namespace {
 
 // ------------------------------------------------------------------ attention
-// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 half or row
-// tile 0, 7..10: 1 (one per TMEM lane quadrant), 11..14 E4M3 codes to bf16 tiles.
-constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpSoftmax = 3, kWarpCodes = 11;
+// Warps: 0 tiles of keys or codes by TMA, 1 MMA and TMEM, 2 queries, 3 tiles of
+// values, 4..7 half or row tile 0, 8..11: 1 (one per TMEM lane quadrant), 12..15
+// E4M3 codes to bf16 tiles.
+constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpV = 3, kWarpSoftmax = 4, kWarpCodes = 12;
 constexpr int kCodeThreads = 128;
 
 template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = (F8 ? 2 : 5) * (128 / D);
-  static constexpr int S = F8 ? 4 * (128 / D) : 1;  // slots of codes
+  static constexpr int RK = 2 * (128 / D), RV = (F8 ? 1 : 3) * (128 / D);  // slots of tiles
+  static constexpr int S = F8 ? 3 * (128 / D) : 1;                         // slots of codes
   static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
   static constexpr uint32_t O_COL = 256;  // S buffers at columns 0 and 128, O of half t at 256 + 128 t
   static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + CODES + SCALES + 1024 + 1024;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + RK + RV) * TILE + CODES + SCALES + 1024 + 1024;
 };
 
-template <int R, int S>
+template <int RK, int RV, int S>
 struct Bars {
-  RingBars<R> ring;
+  RingBars<RK> keys;
+  RingBars<RV> values;
   CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
@@ -101,15 +103,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tv,
                        const __grid_constant__ AttendParams p) {
   using C = Cfg<D, F8>;
-  constexpr int R = C::R;
+  constexpr int RK = C::RK, RV = C::RV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
-  uint8_t* ring = smem + 2 * C::TILE;
-  uint8_t* codes = ring + R * C::TILE;
+  uint8_t* sK = smem + 2 * C::TILE;
+  uint8_t* sV = sK + RK * C::TILE;
+  uint8_t* codes = sV + RV * C::TILE;
   float* scales = reinterpret_cast<float*>(codes + C::CODES);
-  auto* bars = reinterpret_cast<Bars<R, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  static_assert(sizeof(Bars<R, C::S>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
+  auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(Bars<RK, RV, C::S>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -123,14 +126,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->o_last[i], 1);
       mbar_init(&bars->o_free[i], 4);
     }
-    for (int i = 0; i < R; ++i) {
-      mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->ring.empty[i], 1);
+    for (int i = 0; i < RK; ++i) {
+      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->keys.empty[i], 1);
+    }
+    for (int i = 0; i < RV; ++i) {
+      mbar_init(&bars->values.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->values.empty[i], 1);
     }
     for (int i = 0; i < C::S; ++i) {
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     fence_barrier_init();
   }
   if (warp == kWarpMMA) {
@@ -154,10 +162,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     if constexpr (F8)
       fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
     else
-      produce_tma<D, R, true>(v, &tk, &tv, ring, bars->ring, TileCursor(w));
+      produce_tma<D>(v, &tk, sK, bars->keys, TileCursor(w));
+  } else if (!F8 && warp == kWarpV) {
+    produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, R, C::S, true, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales,
-                                                  TileCursor(w), threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, RK, RV, C::S, true, kCodeThreads>(
+        v, codes, bars->codes, sK, bars->keys, sV, &bars->values, scales, TileCursor(w),
+        threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t qn = 0;
@@ -184,8 +195,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_bf16(TILE_ROWS, TILE_KEYS, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(TILE_ROWS, D, 0, 1);
-      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(ring, 0);
-      const uint64_t dv0 = smem_desc(ring, kBoxBytes, 1024);
+      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(sK, 0);
+      const uint64_t dv0 = smem_desc(sV, kBoxBytes, 1024);
       uint32_t g = 0, qn = 0, j = 0;
       int e = 0;
       bool ok = true;
@@ -195,9 +206,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         uint32_t j, g;
       } pv;
       auto issue_pv = [&]() -> bool {
-        const uint32_t st = (2 * pv.g + 1) % R, buf = pv.j & 1;
+        const uint32_t st = pv.g % RV, buf = pv.j & 1;
         if (!mbar_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
-            !mbar_wait(&bars->ring.full[st], ((2 * pv.g + 1) / R) & 1, v.err))
+            !mbar_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err))
           return false;
         if (pv.first && pv.e > 0) {
           for (int t = 0; t < 2; ++t)
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
         }
         umma_commit(&bars->pv_done[buf]);
-        if (pv.frees) umma_commit(&bars->ring.empty[st]);
+        if (pv.frees) umma_commit(&bars->values.empty[st]);
         if (pv.last)
           for (int t = 0; t < 2; ++t)
             if (!pv.two || t == pv.t) umma_commit(&bars->o_last[t]);
@@ -226,11 +237,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       while (ok && w.next()) {
         const int nt = w.two ? 2 : 1;
         for (int kt = w.kt0; ok && kt < w.kt1; ++kt, ++g) {
-          const uint32_t st = (2 * g) % R;
+          const uint32_t st = g % RK;
           for (int t = 0; ok && t < nt; ++t, ++j) {
             const uint32_t qb = (qn + t) & 1;
             if ((kt == w.kt0 && !mbar_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
-                (t == 0 && !mbar_wait(&bars->ring.full[st], ((2 * g) / R) & 1, v.err))) {
+                (t == 0 && !mbar_wait(&bars->keys.full[st], (g / RK) & 1, v.err))) {
               ok = false;
               break;
             }
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
               umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
             }
             umma_commit(&bars->s_full[j & 1]);
-            if (t == nt - 1) umma_commit(&bars->ring.empty[st]);
+            if (t == nt - 1) umma_commit(&bars->keys.empty[st]);
             if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
             if (pv.live && !issue_pv()) {
               ok = false;
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       float m = -INFINITY, l = 0.f;
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
         const uint32_t jj = j0 + (kt - w.kt0) * step, j = w.two ? jj + t : jj;
-        const uint32_t s_tm = tmem + lane_off + (j & 1) * 128, st = (2 * g + 1) % R;
+        const uint32_t s_tm = tmem + lane_off + (j & 1) * 128, st = g % RV;
         if (!warp_wait(&bars->s_full[j & 1], (j >> 1) & 1, v.err)) {
           ok = false;
           break;
@@ -290,7 +301,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         const int valid = w.len - kt * TILE_KEYS;  // may exceed 128
         if (F8 || valid < TILE_KEYS) {
           // the value tile stays in its slot until these probabilities are used
-          if (!warp_wait(&bars->ring.full[st], ((2 * g + 1) / R) & 1, v.err)) {
+          if (!warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
+                         F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const int from = max(lo, valid);
           for (int x = tid; x < (hi - from) * (D / 8); x += 128) {
             const int row = from + x / (D / 8), c = x % (D / 8);
-            *reinterpret_cast<uint4*>(ring + st * C::TILE + (c >> 3) * kBoxBytes + row * 128 +
+            *reinterpret_cast<uint4*>(sV + st * C::TILE + (c >> 3) * kBoxBytes + row * 128 +
                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -448,8 +460,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ scores of the prefix
-// Warps: 0 tiles or codes by TMA, 1 MMA and TMEM, 2 queries, 3..6 even key tiles, 7..10 odd
-// ones, 11..14 E4M3 codes to bf16 tiles.
+// Warps as above, 4..7 even key tiles, 8..11 odd ones.
 template <int D, bool F8>
 struct ScoreCfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
@@ -463,7 +474,7 @@ struct ScoreCfg {
 
 template <int R, int S>
 struct ScoreBars {
-  RingBars<R> ring;
+  RingBars<R> keys;
   CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
@@ -512,13 +523,14 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
-      mbar_init(&bars->ring.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->ring.empty[i], 1);
+      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
+      mbar_init(&bars->keys.empty[i], 1);
     }
     for (int i = 0; i < C::S; ++i) {
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
@@ -551,10 +563,11 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
     if constexpr (F8)
       fetch_codes<D, C::S, false>(v, &tk, nullptr, codes, bars->codes, k);
     else
-      produce_tma<D, R, false>(v, &tk, nullptr, ring, bars->ring, k);
+      produce_tma<D>(v, &tk, ring, bars->keys, k);
   } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, R, C::S, false, kCodeThreads>(v, codes, bars->codes, ring, bars->ring, scales, k,
-                                                   threadIdx.x - 32 * kWarpCodes);
+    convert_codes<D, R, 1, C::S, false, kCodeThreads>(v, codes, bars->codes, ring, bars->keys,
+                                                      nullptr, nullptr, scales, k,
+                                                      threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t f = 0;
@@ -590,7 +603,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         const bool done = !stay || k.last_of_head();  // the row tiles' last use
         const uint32_t st = g % R;
         const int t = g & 1;
-        if (!mbar_wait(&bars->ring.full[st], (g / R) & 1, v.err)) break;
+        if (!mbar_wait(&bars->keys.full[st], (g / R) & 1, v.err)) break;
         for (int qt = 0; qt < nq; ++qt) {
           const uint32_t f = f0 + qt, qb = f & 1, buf = 2 * t + (cnt[t] & 1);
           if ((fresh && !mbar_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
@@ -611,7 +624,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           umma_commit(&bars->s_full[buf]);
           if (F8) mbar_arrive(&bars->s_full[buf]);
           if (done) umma_commit(&bars->q_empty[qb]);
-          if (qt == nq - 1) umma_commit(&bars->ring.empty[st]);
+          if (qt == nq - 1) umma_commit(&bars->keys.empty[st]);
           ++cnt[t];
         }
       }

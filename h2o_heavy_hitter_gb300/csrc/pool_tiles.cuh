@@ -105,9 +105,9 @@ __device__ __forceinline__ int owner(int64_t at, int64_t total, int grid) {
 }
 
 // ------------------------------------------------------------------ tiles into shared memory
-// A ring of R slots, each one tile of keys or values as bf16, 128-byte swizzled:
-// boxes of 128 tokens x 64 channels. Slots are filled in the order K, V, K, V,
-// ... of a cursor's tiles (K only where values are not wanted).
+// A ring of R slots, each one tile of keys or of values as bf16, 128-byte
+// swizzled: boxes of 128 tokens x 64 channels. Keys and values have rings of their
+// own, since a tile of values is held until its probabilities are known.
 template <int R>
 struct RingBars {
   uint64_t full[R], empty[R];
@@ -130,29 +130,24 @@ __device__ __forceinline__ int checked_page(const PoolView& v, int seq, int j) {
 // bf16 pool, one warp: lane i fetches the boxes of page i of a tile by TMA;
 // pages behind the last token are left out, so rows of the slot behind it hold
 // anything. Cursor: step() moves to the next tile (false: none), with seq, len, h, kt.
-template <int D, int R, bool VALUES, typename Cursor>
-__device__ void produce_tma(const PoolView& v, const CUtensorMap* tk, const CUtensorMap* tv,
-                            uint8_t* ring, RingBars<R>& bars, Cursor c) {
-  constexpr int BYTES = TILE_KEYS * D * 2;
+template <int D, int R, typename Cursor>
+__device__ void produce_tma(const PoolView& v, const CUtensorMap* map, uint8_t* ring,
+                            RingBars<R>& bars, Cursor c) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  uint32_t n = 0;
-  while (c.step()) {
+  for (uint32_t n = 0; c.step(); ++n) {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
+    const uint32_t st = n % R;
+    if (n >= R && !warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
+    if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * D * 2);
+    __syncwarp();
+    if (lane < boxes) {
 #pragma unroll
-    for (int kv = 0; kv < (VALUES ? 2 : 1); ++kv, ++n) {
-      const uint32_t st = n % R;
-      if (n >= R && !warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
-      if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * D * 2);
-      __syncwarp();
-      if (lane < boxes) {
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_2d(ring + st * BYTES + b * kBoxBytes + (lane << v.shift) * 128, kv ? tv : tk,
-                      b * 64, row, &bars.full[st]);
-      }
+      for (int b = 0; b < D / 64; ++b)
+        tma_load_2d(ring + st * (TILE_KEYS * D * 2) + b * kBoxBytes + (lane << v.shift) * 128, map,
+                    b * 64, row, &bars.full[st]);
     }
   }
 }
@@ -172,96 +167,125 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
   return r;
 }
 
-// E4M3 pool: a second ring of S slots takes the codes as they are (128 tokens of
-// D bytes, then 128 scales), by TMA from one warp, like produce_tma; NT other
-// threads turn each into a slot of bf16. (Codes loaded through registers of the
-// converting threads, three slots ahead, took 10,000 clocks a tile of keys and
-// values against 2,500 this way: every use of one load waited for all of them.)
+// E4M3 pool: one more ring of S slots takes the codes as they are (128 tokens of
+// D bytes, then 128 scales), by TMA from one warp; NT other threads turn each into
+// a slot of bf16. Keys go one tile ahead of values (K0, K1, V0, K2, V1, ...), so
+// that the next tile's keys are converted before the wait for this one's values'
+// slot. (Codes loaded through registers of the converting threads took 10,000
+// clocks a tile of keys and values: every use of one load waited for all of them.)
 template <int S>
 struct CodeBars {
   uint64_t full[S], empty[S];  // empty: an arrival per converting warp
+  // Both scales of tile g are written: by g & 1, an arrival per converting warp.
+  // (A reader may wait for it before the values of tile g - 1 are converted, but
+  // never before those of g - 2: on the values' own barrier, whose phases may be
+  // single tiles, that wait could take the phase before for its own.)
+  uint64_t scaled[2];
 };
 
 template <int D>
 constexpr int kCodeSlot = TILE_KEYS * D + TILE_KEYS * 4;
 
+// The order of the code ring: calls f(cursor, n, g, value) for the n-th slot, tile g.
+template <bool VALUES, typename Cursor, typename F>
+__device__ __forceinline__ void each_code_tile(Cursor keys, F&& f) {
+  Cursor values = keys;
+  uint32_t n = 0, g = 0;
+  bool more = keys.step();
+  if (!more || !f(keys, n++, g, false)) return;
+  for (;; ++g) {
+    more = keys.step();
+    if (more && !f(keys, n++, g + 1, false)) return;
+    if (VALUES) {
+      values.step();
+      if (!f(values, n++, g, true)) return;
+    }
+    if (!more) return;
+  }
+}
+
 template <int D, int S, bool VALUES, typename Cursor>
 __device__ void fetch_codes(const PoolView& v, const CUtensorMap* tk, const CUtensorMap* tv,
-                            uint8_t* codes, CodeBars<S>& bars, Cursor c) {
+                            uint8_t* codes, CodeBars<S>& bars, const Cursor& begin) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  uint32_t n = 0;
-  while (c.step()) {
+  each_code_tile<VALUES>(begin, [&](const Cursor& c, uint32_t n, uint32_t, bool value) -> bool {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
-#pragma unroll
-    for (int kv = 0; kv < (VALUES ? 2 : 1); ++kv, ++n) {
-      const uint32_t st = n % S;
-      if (n >= S && !warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return;
-      if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
-      __syncwarp();
-      if (lane < boxes) {
-        uint8_t* dst = codes + st * kCodeSlot<D>;
-        tma_load_2d(dst + (lane << v.shift) * D, kv ? tv : tk, 0, row, &bars.full[st]);
-        bulk_copy_g2s(dst + TILE_KEYS * D + (lane << v.shift) * 4, (kv ? v.vscale : v.kscale) + row,
-                      v.page * 4, &bars.full[st]);
-      }
+    const uint32_t st = n % S;
+    if (n >= S && !warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
+    __syncwarp();
+    if (lane < boxes) {
+      uint8_t* dst = codes + st * kCodeSlot<D>;
+      tma_load_2d(dst + (lane << v.shift) * D, value ? tv : tk, 0, row, &bars.full[st]);
+      bulk_copy_g2s(dst + TILE_KEYS * D + (lane << v.shift) * 4, (value ? v.vscale : v.kscale) + row,
+                    v.page * 4, &bars.full[st]);
     }
-  }
+    return true;
+  });
 }
 
 // Rows behind the last token become zero. The scales of tile g go to
 // scales[g % kScaleTiles<VALUES>][0: keys, 1: values][128]. Each warp arrives once
 // on the slot's barrier.
-template <int D, int R, int S, bool VALUES, int NT, typename Cursor>
+template <int D, int RK, int RV, int S, bool VALUES, int NT, typename Cursor>
 __device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<S>& from,
-                              uint8_t* ring, RingBars<R>& to, float* scales, Cursor c, int tid) {
+                              uint8_t* kring, RingBars<RK>& kbars, uint8_t* vring,
+                              RingBars<RV>* vbars, float* scales, const Cursor& begin, int tid) {
   constexpr int BYTES = TILE_KEYS * D * 2;
   constexpr int CPR = D / 16;               // 16-byte chunks of codes per token
   constexpr int NCH = TILE_KEYS * CPR / NT;  // chunks per thread and slot
   const int lane = threadIdx.x & 31;
-  uint32_t n = 0;
-  while (c.step()) {
+  each_code_tile<VALUES>(begin, [&](const Cursor& c, uint32_t n, uint32_t g, bool value) -> bool {
     const int valid = c.len - c.kt * TILE_KEYS;
+    const uint32_t sc = n % S;
+    if (!warp_wait(&from.full[sc], (n / S) & 1, v.err)) return false;
+    const uint8_t* src = codes + sc * kCodeSlot<D>;
+    uint4 x[NCH];
 #pragma unroll
-    for (int kv = 0; kv < (VALUES ? 2 : 1); ++kv, ++n) {
-      const uint32_t sc = n % S, st = n % R;
-      if (!warp_wait(&from.full[sc], (n / S) & 1, v.err)) return;
-      const uint8_t* src = codes + sc * kCodeSlot<D>;
-      uint4 x[NCH];
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        x[i] = reinterpret_cast<const uint4*>(src)[tid + NT * i];
-        if ((tid + NT * i) / CPR >= valid) x[i] = make_uint4(0, 0, 0, 0);
-      }
-      if (tid < TILE_KEYS)
-        scales[(((VALUES ? n >> 1 : n) % kScaleTiles<VALUES>) * 2 + kv) * TILE_KEYS + tid] =
-            tid < valid ? reinterpret_cast<const float*>(src + TILE_KEYS * D)[tid] : 0.f;
-      if (n >= R && !warp_wait(&to.empty[st], ((n / R) - 1) & 1, v.err)) return;
-      uint8_t* dst = ring + st * BYTES;
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const int q = tid + NT * i, row = q / CPR, col = q % CPR;
-        const uint2 a = e4m3x4_to_bf16(x[i].x), b = e4m3x4_to_bf16(x[i].y);
-        const uint2 e = e4m3x4_to_bf16(x[i].z), f = e4m3x4_to_bf16(x[i].w);
-        uint8_t* at = dst + (col >> 2) * kBoxBytes + row * 128;
-        const int c0 = 2 * (col & 3);
-        // the two boxes of a row lie in the same banks: the halves of a row write
-        // their even and odd chunks in opposite order
-        const bool swap = col >= 4;
-        const uint4 even = make_uint4(a.x, a.y, b.x, b.y), odd = make_uint4(e.x, e.y, f.x, f.y);
-        *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? odd : even;
-        *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (row & 7)) << 4)) = swap ? even : odd;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&to.full[st]);
-        mbar_arrive(&from.empty[sc]);
-      }
+    for (int i = 0; i < NCH; ++i) {
+      x[i] = reinterpret_cast<const uint4*>(src)[tid + NT * i];
+      if ((tid + NT * i) / CPR >= valid) x[i] = make_uint4(0, 0, 0, 0);
     }
-  }
+    float scale = 0.f;
+    if (tid < TILE_KEYS && tid < valid) scale = reinterpret_cast<const float*>(src + TILE_KEYS * D)[tid];
+    uint64_t* full;
+    uint8_t* dst;
+    if (VALUES && value) {
+      if (g >= RV && !warp_wait(&vbars->empty[g % RV], ((g / RV) - 1) & 1, v.err)) return false;
+      full = &vbars->full[g % RV];
+      dst = vring + g % RV * BYTES;
+    } else {
+      if (g >= RK && !warp_wait(&kbars.empty[g % RK], ((g / RK) - 1) & 1, v.err)) return false;
+      full = &kbars.full[g % RK];
+      dst = kring + g % RK * BYTES;
+    }
+    if (tid < TILE_KEYS) scales[((g % kScaleTiles<VALUES>) * 2 + value) * TILE_KEYS + tid] = scale;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int q = tid + NT * i, row = q / CPR, col = q % CPR;
+      const uint2 a = e4m3x4_to_bf16(x[i].x), b = e4m3x4_to_bf16(x[i].y);
+      const uint2 e = e4m3x4_to_bf16(x[i].z), f = e4m3x4_to_bf16(x[i].w);
+      uint8_t* at = dst + (col >> 2) * kBoxBytes + row * 128;
+      const int c0 = 2 * (col & 3);
+      // the two boxes of a row lie in the same banks: the halves of a row write
+      // their even and odd chunks in opposite order
+      const bool swap = col >= 4;
+      const uint4 even = make_uint4(a.x, a.y, b.x, b.y), odd = make_uint4(e.x, e.y, f.x, f.y);
+      *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? odd : even;
+      *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (row & 7)) << 4)) = swap ? even : odd;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(full);
+      mbar_arrive(&from.empty[sc]);
+      if (VALUES && value) mbar_arrive(&from.scaled[g & 1]);
+    }
+    return true;
+  });
 }
 #endif  // __CUDACC__
 
