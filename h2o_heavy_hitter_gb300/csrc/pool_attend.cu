@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     if (lane == 0) {
       for (int e = 0; w.next(); ++e) {
         const int qb = e & 1;
-        if (e >= 2 && !mbar_wait(&bars->q_empty[qb], ((e >> 1) - 1) & 1, v.err)) break;
+        if (e >= 2 && !pool_wait(&bars->q_empty[qb], ((e >> 1) - 1) & 1, v.err)) break;
         mbar_arrive_expect_tx(&bars->q_full[qb], w.rows() * D * 2);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
@@ -438,9 +438,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       } pv;
       auto issue_pv = [&]() -> bool {
         const uint32_t st = pv.g % RV, buf = pv.c & 1;
-        if (!mbar_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
-            !mbar_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err) ||
-            (pv.first && pv.e >= 2 && !mbar_wait(&bars->o_free[pv.t], ((pv.e >> 1) - 1) & 1, v.err)))
+        if (!pool_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
+            !pool_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err) ||
+            (pv.first && pv.e >= 2 && !pool_wait(&bars->o_free[pv.t], ((pv.e >> 1) - 1) & 1, v.err)))
           return false;
         tc_fence_after();
         const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
@@ -458,10 +458,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       while (ok && w.next()) {
         const int t = e & 1, qb = e & 1;
         const uint32_t idesc = idesc_bf16(TILE_KEYS, w.rows() <= 16 ? 16 : 32, 0, 0);
-        if (!mbar_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
+        if (!pool_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
           const uint32_t st = g % RK, buf = c[t] & 1;
-          if (!mbar_wait(&bars->keys.full[st], (g / RK) & 1, v.err)) {
+          if (!pool_wait(&bars->keys.full[st], (g / RK) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       xm[quad][lane] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->xbar[t]);
-      if (!warp_wait(&bars->xbar[t], x & 1, v.err)) return false;
+      if (!pool_warp_wait(&bars->xbar[t], x & 1, v.err)) return false;
       ++x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) all[i] = xm[i][lane];
@@ -531,14 +531,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         const uint32_t s_tm = tmem + lane_off + t * 64 + buf * 32;
         const int valid = w.len - kt * TILE_KEYS;
         const bool live = r < valid;
-        if (!warp_wait(&bars->s_full[t][buf], (c >> 1) & 1, v.err)) {
+        if (!pool_warp_wait(&bars->s_full[t][buf], (c >> 1) & 1, v.err)) {
           ok = false;
           break;
         }
         float ks = p.qscale, vs = 1.f;
         if (F8 || valid < TILE_KEYS) {
           // the value tile stays in its slot until this warpgroup's probabilities are used
-          if (!warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
+          if (!pool_warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
                          F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
             ok = false;
             break;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         l = fmaf(l, alpha, sum);
         if (__any_sync(0xffffffffu, rescale)) {  // the same in the four warps
           // the O^T before this one must be complete
-          if (!warp_wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1, v.err)) {
+          if (!pool_warp_wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       float part[4];
       if (!exchange(l, part)) break;
       l = (part[0] + part[1]) + (part[2] + part[3]);
-      if (!warp_wait(&bars->o_last[t], (e >> 1) & 1, v.err)) break;
+      if (!pool_warp_wait(&bars->o_last[t], (e >> 1) & 1, v.err)) break;
       tc_fence_after();
       const size_t rec = static_cast<size_t>(w.piece) * (w.prefix ? kFewRows : p.s.group);
       float* out = (w.prefix ? p.w.po : p.w.to) + rec * D;

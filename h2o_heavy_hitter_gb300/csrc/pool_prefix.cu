@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       while (ok && w.next()) {
         for (int t = 0; t < (w.two ? 2 : 1); ++t, ++qn) {
           const uint32_t qb = qn & 1;
-          if (qn >= 2 && !mbar_wait(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, v.err)) {
+          if (qn >= 2 && !pool_wait(&bars->q_empty[qb], ((qn >> 1) - 1) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -207,12 +207,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       } pv;
       auto issue_pv = [&]() -> bool {
         const uint32_t st = pv.g % RV, buf = pv.j & 1;
-        if (!mbar_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
-            !mbar_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err))
+        if (!pool_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
+            !pool_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err))
           return false;
         if (pv.first && pv.e > 0) {
           for (int t = 0; t < 2; ++t)
-            if ((!pv.two || t == pv.t) && !mbar_wait(&bars->o_free[t], (pv.e - 1) & 1, v.err))
+            if ((!pv.two || t == pv.t) && !pool_wait(&bars->o_free[t], (pv.e - 1) & 1, v.err))
               return false;
         }
         tc_fence_after();
@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const uint32_t st = g % RK;
           for (int t = 0; ok && t < nt; ++t, ++j) {
             const uint32_t qb = (qn + t) & 1;
-            if ((kt == w.kt0 && !mbar_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
-                (t == 0 && !mbar_wait(&bars->keys.full[st], (g / RK) & 1, v.err))) {
+            if ((kt == w.kt0 && !pool_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
+                (t == 0 && !pool_wait(&bars->keys.full[st], (g / RK) & 1, v.err))) {
               ok = false;
               break;
             }
@@ -294,14 +294,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
         const uint32_t jj = j0 + (kt - w.kt0) * step, j = w.two ? jj + t : jj;
         const uint32_t s_tm = tmem + lane_off + (j & 1) * 128, st = g % RV;
-        if (!warp_wait(&bars->s_full[j & 1], (j >> 1) & 1, v.err)) {
+        if (!pool_warp_wait(&bars->s_full[j & 1], (j >> 1) & 1, v.err)) {
           ok = false;
           break;
         }
         const int valid = w.len - kt * TILE_KEYS;  // may exceed 128
         if (F8 || valid < TILE_KEYS) {
           // the value tile stays in its slot until these probabilities are used
-          if (!warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
+          if (!pool_warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
                          F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
             ok = false;
             break;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           if (__any_sync(0xffffffffu, rescale)) {
             // (on its own barrier, whose phase before belongs to the P V of j - 3: a
             // parity wait may be one phase behind or level, never two)
-            if (!w.two && !warp_wait(&bars->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, v.err)) {
+            if (!w.two && !pool_warp_wait(&bars->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, v.err)) {
               ok = false;
               break;
             }
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       }
       if (!ok) break;
       // ---- the piece: O out of TMEM, which the next unit may then use
-      if (!warp_wait(&bars->o_last[t], e & 1, v.err)) break;
+      if (!pool_warp_wait(&bars->o_last[t], e & 1, v.err)) break;
       tc_fence_after();
       if (active) {
         const size_t rec = (static_cast<size_t>(w.piece) * 2 + t) * TILE_ROWS + r;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         last = k.h;
         for (int qt = 0; qt < nq; ++qt, ++f) {
           const uint32_t qb = f & 1;
-          if (f >= 2 && !mbar_wait(&bars->q_empty[qb], ((f >> 1) - 1) & 1, v.err)) {
+          if (f >= 2 && !pool_wait(&bars->q_empty[qb], ((f >> 1) - 1) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -603,11 +603,11 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         const bool done = !stay || k.last_of_head();  // the row tiles' last use
         const uint32_t st = g % R;
         const int t = g & 1;
-        if (!mbar_wait(&bars->keys.full[st], (g / R) & 1, v.err)) break;
+        if (!pool_wait(&bars->keys.full[st], (g / R) & 1, v.err)) break;
         for (int qt = 0; qt < nq; ++qt) {
           const uint32_t f = f0 + qt, qb = f & 1, buf = 2 * t + (cnt[t] & 1);
-          if ((fresh && !mbar_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
-              (cnt[t] >= 2 && !mbar_wait(&bars->s_free[buf], ((cnt[t] >> 1) - 1) & 1, v.err))) {
+          if ((fresh && !pool_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
+              (cnt[t] >= 2 && !pool_wait(&bars->s_free[buf], ((cnt[t] >> 1) - 1) & 1, v.err))) {
             ok = false;
             break;
           }
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         const uint32_t buf = 2 * t + (cnt & 1);
         const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
         const float* nl = p.w.nlse + (static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS;
-        if (!warp_wait(&bars->s_full[buf], (cnt >> 1) & 1, v.err)) {
+        if (!pool_warp_wait(&bars->s_full[buf], (cnt >> 1) & 1, v.err)) {
           ok = false;
           break;
         }

@@ -77,6 +77,20 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t sm
 }
 
 #ifdef __CUDACC__
+// ------------------------------------------------------------------ bounded waits
+// mbar_wait with its loop out of line: these kernels run some dozen waits in as
+// many roles at once, and their code shares the instruction cache.
+static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return mbar_wait(bar, parity, err);
+}
+__device__ __forceinline__ bool pool_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, err);
+}
+// The result is made warp-uniform (see warp_wait).
+__device__ __forceinline__ bool pool_warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, pool_wait(bar, parity, err));
+}
+
 // ------------------------------------------------------------------ lengths, shares
 // A sequence's length, -1 (reported when `report`) for a state that no call leaves.
 __device__ __forceinline__ int checked_length(const PoolView& v, int seq, bool report) {
@@ -140,7 +154,7 @@ __device__ void produce_tma(const PoolView& v, const CUtensorMap* map, uint8_t* 
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
     const uint32_t st = n % R;
-    if (n >= R && !warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
+    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
     if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * D * 2);
     __syncwarp();
     if (lane < boxes) {
@@ -186,21 +200,35 @@ struct CodeBars {
 template <int D>
 constexpr int kCodeSlot = TILE_KEYS * D + TILE_KEYS * 4;
 
-// The order of the code ring: calls f(cursor, n, g, value) for the n-th slot, tile g.
+// The order of the code ring: calls f(tile, n, g, value) for the n-th slot, tile g.
+// One call in one loop: the body is large, and several warps' bodies share the
+// instruction cache.
+struct CodeTile {
+  int seq, len, h, kt;
+};
+
 template <bool VALUES, typename Cursor, typename F>
 __device__ __forceinline__ void each_code_tile(Cursor keys, F&& f) {
   Cursor values = keys;
-  uint32_t n = 0, g = 0;
+  uint32_t gk = 0, gv = 0;
   bool more = keys.step();
-  if (!more || !f(keys, n++, g, false)) return;
-  for (;; ++g) {
-    more = keys.step();
-    if (more && !f(keys, n++, g + 1, false)) return;
-    if (VALUES) {
+  for (uint32_t n = 0;; ++n) {
+    const bool value = VALUES && (gk - gv == 2 || (!more && gk > gv));
+    if (!value && !more) return;
+    CodeTile c;
+    if (value) {
       values.step();
-      if (!f(values, n++, g, true)) return;
+      c = {values.seq, values.len, values.h, values.kt};
+    } else {
+      c = {keys.seq, keys.len, keys.h, keys.kt};
     }
-    if (!more) return;
+    if (!f(c, n, value ? gv : gk, value)) return;
+    if (value) {
+      ++gv;
+    } else {
+      ++gk;
+      more = keys.step();
+    }
   }
 }
 
@@ -208,13 +236,13 @@ template <int D, int S, bool VALUES, typename Cursor>
 __device__ void fetch_codes(const PoolView& v, const CUtensorMap* tk, const CUtensorMap* tv,
                             uint8_t* codes, CodeBars<S>& bars, const Cursor& begin) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  each_code_tile<VALUES>(begin, [&](const Cursor& c, uint32_t n, uint32_t, bool value) -> bool {
+  each_code_tile<VALUES>(begin, [&](const CodeTile& c, uint32_t n, uint32_t, bool value) -> bool {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
     const uint32_t st = n % S;
-    if (n >= S && !warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return false;
+    if (n >= S && !pool_warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return false;
     if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
     __syncwarp();
     if (lane < boxes) {
@@ -238,10 +266,10 @@ __device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<
   constexpr int CPR = D / 16;               // 16-byte chunks of codes per token
   constexpr int NCH = TILE_KEYS * CPR / NT;  // chunks per thread and slot
   const int lane = threadIdx.x & 31;
-  each_code_tile<VALUES>(begin, [&](const Cursor& c, uint32_t n, uint32_t g, bool value) -> bool {
+  each_code_tile<VALUES>(begin, [&](const CodeTile& c, uint32_t n, uint32_t g, bool value) -> bool {
     const int valid = c.len - c.kt * TILE_KEYS;
     const uint32_t sc = n % S;
-    if (!warp_wait(&from.full[sc], (n / S) & 1, v.err)) return false;
+    if (!pool_warp_wait(&from.full[sc], (n / S) & 1, v.err)) return false;
     const uint8_t* src = codes + sc * kCodeSlot<D>;
     uint4 x[NCH];
 #pragma unroll
@@ -254,11 +282,11 @@ __device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<
     uint64_t* full;
     uint8_t* dst;
     if (VALUES && value) {
-      if (g >= RV && !warp_wait(&vbars->empty[g % RV], ((g / RV) - 1) & 1, v.err)) return false;
+      if (g >= RV && !pool_warp_wait(&vbars->empty[g % RV], ((g / RV) - 1) & 1, v.err)) return false;
       full = &vbars->full[g % RV];
       dst = vring + g % RV * BYTES;
     } else {
-      if (g >= RK && !warp_wait(&kbars.empty[g % RK], ((g / RK) - 1) & 1, v.err)) return false;
+      if (g >= RK && !pool_warp_wait(&kbars.empty[g % RK], ((g / RK) - 1) & 1, v.err)) return false;
       full = &kbars.full[g % RK];
       dst = kring + g % RK * BYTES;
     }
