@@ -407,11 +407,19 @@ def h2o_pool_destroy(pool: H2OPool) -> None:
     pool.close()
 
 
-def _list_ptr(seqs, name: str = "seqs", n: int | None = None) -> int:
+def _ptr(pool: H2OPool, t, dtype: torch.dtype, shape: tuple, name: str) -> int:
+    """_dev_ptr against the pool's device, with the checks that pass made first and fast: a
+    step of a small batch is bound by them."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.get_device() == pool.device and t.is_contiguous()):
+        return t.data_ptr()
+    return _dev_ptr(t, dtype, shape, name)
+
+
+def _list_ptr(pool: H2OPool, seqs, name: str = "seqs", n: int | None = None) -> int:
     if isinstance(seqs, torch.Tensor) and seqs.dim() != 1:
         raise ValueError(f"{name} must have one dimension, got {tuple(seqs.shape)}")
-    n = len(seqs) if n is None else n
-    return _dev_ptr(seqs, torch.int32, (n,), name)
+    return _ptr(pool, seqs, torch.int32, (len(seqs) if n is None else n,), name)
 
 
 def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
@@ -443,38 +451,44 @@ def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
 def h2o_pool_write(pool: H2OPool, layer: int, seqs, K, V, lens=None, score=None) -> None:
     """Appends tokens to sequences: bf16 K, V [n, H, T, d], the first lens[i] (CUDA int32 [n];
     default T) of entry i, with initial scores fp32 [n, H, T] (default 0)."""
-    ps = _list_ptr(seqs)
-    n, T = len(seqs), K.shape[2] if K.dim() == 4 else 0
+    ps = _list_ptr(pool, seqs)
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("K must be a tensor [n, heads, T, head_dim]")
+    n, T = len(seqs), K.shape[2]
     shape = (n, pool.heads, T, pool.head_dim)
-    pk = _dev_ptr(K, torch.bfloat16, shape, "K")
-    pv = _dev_ptr(V, torch.bfloat16, shape, "V")
-    pl = None if lens is None else _dev_ptr(lens, torch.int32, (n,), "lens")
-    pc = None if score is None else _dev_ptr(score, torch.float32, shape[:3], "score")
+    pk = _ptr(pool, K, torch.bfloat16, shape, "K")
+    pv = _ptr(pool, V, torch.bfloat16, shape, "V")
+    pl = None if lens is None else _ptr(pool, lens, torch.int32, (n,), "lens")
+    pc = None if score is None else _ptr(pool, score, torch.float32, shape[:3], "score")
     _check(load_library().h2o_pool_write(pool.handle, layer, n, ps, pk, pv, T, pl, pc))
 
 
 def h2o_pool_fork(pool: H2OPool, layer: int, src, dst) -> None:
     """Makes the empty sequences dst continuations of src that share their whole pages
     (layer -1: in every layer)."""
-    a, b = _list_ptr(src, "src"), _list_ptr(dst, "dst", len(src))
-    _check(load_library().h2o_pool_fork(pool.handle, layer, len(src), a, b))
+    n = len(src)
+    a, b = _list_ptr(pool, src, "src"), _list_ptr(pool, dst, "dst", n)
+    _check(load_library().h2o_pool_fork(pool.handle, layer, n, a, b))
 
 
 def h2o_pool_copy(pool: H2OPool, layer: int, src, dst) -> None:
     """h2o_pool_fork that copies every page instead of sharing the whole ones."""
-    a, b = _list_ptr(src, "src"), _list_ptr(dst, "dst", len(src))
-    _check(load_library().h2o_pool_copy(pool.handle, layer, len(src), a, b))
+    n = len(src)
+    a, b = _list_ptr(pool, src, "src"), _list_ptr(pool, dst, "dst", n)
+    _check(load_library().h2o_pool_copy(pool.handle, layer, n, a, b))
 
 
 def h2o_pool_free(pool: H2OPool, layer: int, seqs) -> None:
     """Empties sequences (layer -1: in every layer); pages that nobody holds are free again."""
-    _check(load_library().h2o_pool_free(pool.handle, layer, len(seqs), _list_ptr(seqs)))
+    ps = _list_ptr(pool, seqs)
+    _check(load_library().h2o_pool_free(pool.handle, layer, len(seqs), ps))
 
 
 def h2o_pool_compact(pool: H2OPool, layer: int, seqs, h: int, r: int) -> None:
     """Keeps the r last tokens and the h others of largest score of every head of each
     sequence longer than h + r (layer -1: in every layer)."""
-    _check(load_library().h2o_pool_compact(pool.handle, layer, len(seqs), _list_ptr(seqs), h, r))
+    ps = _list_ptr(pool, seqs)
+    _check(load_library().h2o_pool_compact(pool.handle, layer, len(seqs), ps, h, r))
 
 
 def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=None, lse=None,
@@ -483,19 +497,19 @@ def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=No
     ``prefix`` (shared by the batch; -1: none) and each sequence's own. Returns (out bf16
     [n, q_heads, d], lse fp32 [n, q_heads]); with ``accumulate`` the probabilities are added to
     the accumulated scores. Rows of -1 entries are not written."""
-    ps = _list_ptr(seqs)
+    ps = _list_ptr(pool, seqs)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [n, q_heads, head_dim]")
-    shape = (len(seqs), q.shape[1], pool.head_dim)
-    pq = _dev_ptr(q, torch.bfloat16, shape, "q")
+    n, heads = len(seqs), q.shape[1]
+    shape = (n, heads, pool.head_dim)
+    pq = _ptr(pool, q, torch.bfloat16, shape, "q")
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-    _check(load_library().h2o_pool_attend(pool.handle, layer, shape[0], ps, prefix, pq, shape[1],
-                                          _dev_ptr(out, torch.bfloat16, shape, "out"),
-                                          _dev_ptr(lse, torch.float32, shape[:2], "lse"),
-                                          int(accumulate)))
+        lse = q.new_empty(shape[:2], dtype=torch.float32)
+    _check(load_library().h2o_pool_attend(
+        pool.handle, layer, n, ps, prefix, pq, heads, _ptr(pool, out, torch.bfloat16, shape, "out"),
+        _ptr(pool, lse, torch.float32, shape[:2], "lse"), accumulate))
     return out, lse
 
 

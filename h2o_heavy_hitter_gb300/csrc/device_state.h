@@ -23,4 +23,22 @@ constexpr int kMaxDevices = 64;
 // records the epoch in which it was set. Safe to call from several threads.
 cudaError_t raise_smem_limit(const void* kernel, size_t bytes, int (&opted_in)[kMaxDevices]);
 
+// A launch that may begin while the kernel before it drains: the kernel waits
+// (grid_dependency_wait) before it touches what that one writes.
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(static_cast<unsigned>(threads));
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+
 }  // namespace h2o

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "device_state.h"
 #include "pool.h"
 #include "scan.cuh"
 
@@ -124,6 +125,22 @@ __device__ int take_pages(const PoolView& v, int need, int32_t* fresh, int* wsum
   return first + need <= found ? first : -1;
 }
 
+// How a block's warps go over the pages of n entries: a warp per entry, or several
+// when there are fewer entries than warps.
+struct Spread {
+  int first, step;  // entries
+  int lane, lanes;  // threads of an entry
+  __device__ explicit Spread(int n) {
+    constexpr int warps = kPlanThreads / 32;
+    int per = 1;
+    while (per < warps && n * per * 2 <= warps) per *= 2;
+    lanes = 32 * per;
+    first = threadIdx.x / lanes;
+    step = warps / per;
+    lane = threadIdx.x % lanes;
+  }
+};
+
 // ------------------------------------------------------------------ fork, copy
 // plan of an entry: {served, length, -, -}
 __global__ void __launch_bounds__(kPlanThreads)
@@ -137,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.x) * fresh_stride;
   int32_t* plan = plan_all + static_cast<size_t>(blockIdx.x) * n * kPlanInts;
   const int i = threadIdx.x;
+  grid_launch_dependents();
   int to = list_entry(v, dst, n, s_list);
   const int from = i < n ? src[i] : -1;
   int len = 0, next = 0;
@@ -172,12 +190,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     v.meta[2 * to] = len;
     v.meta[2 * to + 1] = next;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = warp; e < n; e += kPlanThreads / 32) {
+  const Spread w(n);
+  for (int e = w.first; e < n; e += w.step) {
     const int b = s_list[e];
     if (b < 0) continue;
     const int whole = share ? s_len[e] >> v.shift : 0, np = pages_of(v, s_len[e]);
-    for (int j = lane; j < np; j += 32) {
+#pragma unroll 4
+    for (int j = w.lane; j < np; j += w.lanes) {
       int p;
       if (j < whole) {
         p = held_page(v, s_src[e], j);
@@ -191,84 +210,95 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// Copies `n` 16-byte chunks with a warp, four loads in flight per lane.
-__device__ __forceinline__ void warp_copy(uint8_t* dst, const uint8_t* src, int n, int lane) {
+// Copies `n` 16-byte chunks with LANES threads, four loads in flight per thread.
+template <int LANES>
+__device__ __forceinline__ void copy_chunks(uint8_t* dst, const uint8_t* src, int n, int lane) {
   int c = lane;
-  for (; c + 96 < n; c += 128) {
+  for (; c + 3 * LANES < n; c += 4 * LANES) {
     uint4 x[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) x[u] = reinterpret_cast<const uint4*>(src)[c + 32 * u];
+    for (int u = 0; u < 4; ++u) x[u] = reinterpret_cast<const uint4*>(src)[c + LANES * u];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(dst)[c + 32 * u] = x[u];
+    for (int u = 0; u < 4; ++u) reinterpret_cast<uint4*>(dst)[c + LANES * u] = x[u];
   }
-  for (; c < n; c += 32) reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(src)[c];
+  for (; c < n; c += LANES) reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(src)[c];
+}
+
+// n four-byte values, 16-byte aligned at both ends.
+template <int LANES, typename T>
+__device__ __forceinline__ void copy_values(T* dst, const T* src, int n, int lane) {
+  copy_chunks<LANES>(reinterpret_cast<uint8_t*>(dst), reinterpret_cast<const uint8_t*>(src), n / 4, lane);
+  const int rest = (n & ~3) + lane;
+  if (rest < n) dst[rest] = src[rest];
 }
 
 // Copies the first `live` slots of a page's head.
+template <int LANES>
 __device__ __forceinline__ void copy_slots(const PoolView& v, int to, int from, int head, int live,
                                            int lane) {
   const size_t a = slot_base(v, from, head), b = slot_base(v, to, head);
   const int chunks = live * (v.row_bytes / 16);
-  warp_copy(v.K + b * v.row_bytes, v.K + a * v.row_bytes, chunks, lane);
-  warp_copy(v.V + b * v.row_bytes, v.V + a * v.row_bytes, chunks, lane);
-  for (int s = lane; s < live; s += 32) v.pos[b + s] = v.pos[a + s];
-  if (v.kscale)
-    for (int s = lane; s < live; s += 32) {
-      v.kscale[b + s] = v.kscale[a + s];
-      v.vscale[b + s] = v.vscale[a + s];
-    }
+  copy_chunks<LANES>(v.K + b * v.row_bytes, v.K + a * v.row_bytes, chunks, lane);
+  copy_chunks<LANES>(v.V + b * v.row_bytes, v.V + a * v.row_bytes, chunks, lane);
+  copy_values<LANES>(v.pos + b, v.pos + a, live, lane);
+  if (v.kscale) {
+    copy_values<LANES>(v.kscale + b, v.kscale + a, live, lane);
+    copy_values<LANES>(v.vscale + b, v.vscale + a, live, lane);
+  }
 }
 
-// One warp per (entry, head, slab of kSlab slots): the slab's scores, and the
+// LANES threads per (entry, head, slab of kSlab slots): the slab's scores, and the
 // tokens of its pages that were not shared. A head's slots of a page are
 // contiguous, so a partial page is one run of bytes per head.
 constexpr int kSlab = 256;
 
+template <int LANES>
 __global__ void __launch_bounds__(256)
     fork_copy_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
                      const int32_t* __restrict__ dst, bool share,
-                     const int32_t* __restrict__ plan_all) {
+                     const int32_t* plan_all) {
   const PoolView v = at_layer(v0, blockIdx.z);
   const int32_t* plan = plan_all + static_cast<size_t>(blockIdx.z) * n * kPlanInts;
-  const int lane = threadIdx.x & 31;
-  const int task = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x % LANES;
+  const int task = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int e = task / v.heads, head = task % v.heads;
+  grid_dependency_wait();
   if (e >= n || !plan[e * kPlanInts]) return;
   const int len = plan[e * kPlanInts + 1], lo = blockIdx.y * kSlab, hi = min(len, lo + kSlab);
   if (lo >= hi) return;
   const int from = src[e], to = dst[e];
-  const float* sa = v.score + (static_cast<size_t>(from) * v.heads + head) * v.cap;
-  float* sb = v.score + (static_cast<size_t>(to) * v.heads + head) * v.cap;
-  for (int s = lo + lane; s < hi; s += 32) sb[s] = sa[s];
+  copy_values<LANES>(v.score + (static_cast<size_t>(to) * v.heads + head) * v.cap + lo,
+                     v.score + (static_cast<size_t>(from) * v.heads + head) * v.cap + lo, hi - lo, lane);
   const int first = share ? max(lo >> v.shift, len >> v.shift) : lo >> v.shift;
   for (int j = first; j << v.shift < hi; ++j) {
     const int a = held_page(v, from, j), b = held_page(v, to, j);
-    if (a >= 0 && b >= 0) copy_slots(v, b, a, head, min(v.page, len - (j << v.shift)), lane);
+    if (a >= 0 && b >= 0) copy_slots<LANES>(v, b, a, head, min(v.page, len - (j << v.shift)), lane);
   }
 }
 
 // ------------------------------------------------------------------ free
 __global__ void __launch_bounds__(kPlanThreads)
     free_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs) {
-  __shared__ int s_list[kPlanThreads];
+  __shared__ int s_list[kPlanThreads], s_len[kPlanThreads];
   const PoolView v = at_layer(v0, blockIdx.x);
-  int seq = list_entry(v, seqs, n, s_list);
-  if (seq >= 0 && seq_length(v, seq) < 0) seq = -1;
+  int seq = list_entry(v, seqs, n, s_list), len = 0;
+  if (seq >= 0 && (len = seq_length(v, seq)) < 0) seq = -1;
   __syncthreads();  // every thread has compared the list
   s_list[threadIdx.x] = seq;
+  s_len[threadIdx.x] = len;
+  if (seq >= 0) *reinterpret_cast<int2*>(v.meta + 2 * seq) = make_int2(0, 0);
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = warp; e < n; e += kPlanThreads / 32) {
+  const Spread w(n);
+  for (int e = w.first; e < n; e += w.step) {
     const int s = s_list[e];
     if (s < 0) continue;
-    const int np = pages_of(v, v.meta[2 * s]);
-    for (int j = lane; j < np; j += 32) {
+    const int np = pages_of(v, s_len[e]);
+#pragma unroll 4
+    for (int j = w.lane; j < np; j += w.lanes) {
       const int p = held_page(v, s, j);
       if (p >= 0) drop_page(v, p);
       v.table[static_cast<size_t>(s) * v.width + j] = -1;
     }
-    __syncwarp();
-    if (lane < 2) v.meta[2 * s + lane] = 0;
   }
 }
 
@@ -281,6 +311,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       s_first[kPlanThreads];
   __shared__ int wsum[33];
   const int i = threadIdx.x;
+  grid_launch_dependents();
   int seq = list_entry(v, seqs, n, s_list);
   __syncthreads();
   int len = 0, next = 0, t = 0;
@@ -329,11 +360,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     v.meta[2 * seq + 1] = next + t;
   }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = warp; e < n; e += kPlanThreads / 32) {
+  const Spread w(n);
+  for (int e = w.first; e < n; e += w.step) {
     const int b = s_list[e];
     if (b < 0) continue;
-    for (int j = lane; j < s_new[e]; j += 32) {
+    for (int j = w.lane; j < s_new[e]; j += w.lanes) {
       const int p = fresh[s_first[e] + j];
       v.ref[p] = 1;
       v.table[static_cast<size_t>(b) * v.width + s_len[e] + j] = p;
@@ -351,10 +382,11 @@ template <int D, bool F8>
 __global__ void __launch_bounds__(256)
     write_kernel(PoolView v, int n, const int32_t* __restrict__ seqs,
                  const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V, int T,
-                 const float* __restrict__ score, const int32_t* __restrict__ plan) {
+                 const float* __restrict__ score, const int32_t* plan) {
   constexpr int LPT = 8, EPL = D / LPT, NV = EPL / 8;
   const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
   const int t = blockIdx.y * kWriteTokens + threadIdx.x / LPT, l = threadIdx.x % LPT;
+  grid_dependency_wait();
   if (t >= plan[e * kPlanInts]) return;  // whole groups of eight lanes leave together
   const unsigned gmask = 0xffu << (threadIdx.x & 31 & ~(LPT - 1));
   const int seq = seqs[e], slot = plan[e * kPlanInts + 1] + t;
@@ -407,19 +439,27 @@ __device__ __forceinline__ unsigned score_key(float x) {
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectKeys = 48 * 1024;  // scores whose keys are held in shared memory
+constexpr int kDigit = 11;              // bits of a radix step: 3 steps
 
 // Blocks (head, entry, layer) select; the block with head == heads of entry 0
 // plans its layer: plan of an entry = {first fresh page or -1, -, -, -}. The
 // selection reads lengths and scores only and the plan writes neither, so the
 // two run side by side. where[]: slot (page * page size + offset) of each kept
-// token, ascending; kept[]: its score.
+// token, ascending; kept[]: its score. The h-th largest key is found by an
+// MSB-first radix select over keys held in shared memory (a row of up to kSelectKeys
+// scores is read from HBM once); then a warp counts, and in a second pass places,
+// the kept ones of its contiguous part by votes.
 __global__ void __launch_bounds__(kSelectThreads)
     compact_select_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs, int h, int r,
                           int32_t* fresh_all, int fresh_stride, int32_t* plan_all,
-                          int32_t* __restrict__ where, float* __restrict__ kept) {
+                          int32_t* __restrict__ where, float* __restrict__ kept, int held) {
+  extern __shared__ unsigned keys[];  // `held` of them
   const PoolView v = at_layer(v0, blockIdx.z);
-  const int k = h + r, tid = threadIdx.x, nt = blockDim.x;
+  const int k = h + r, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int wsum[33];
+  grid_launch_dependents();
   if (blockIdx.x == static_cast<unsigned>(v.heads)) {
     if (blockIdx.y) return;
     __shared__ int s_list[kPlanThreads];
@@ -433,7 +473,7 @@ __global__ void __launch_bounds__(kSelectThreads)
     if (tid < n) plan[tid * kPlanInts] = seq >= 0 ? first : -1;
     return;
   }
-  __shared__ unsigned hist[256];
+  __shared__ unsigned hist[1 << kDigit];
   __shared__ unsigned s_prefix;
   __shared__ int s_rank;
   const int head = blockIdx.x, e = blockIdx.y, seq = seqs[e];
@@ -442,58 +482,85 @@ __global__ void __launch_bounds__(kSelectThreads)
   if (T <= k || T > v.cap) return;
   const float* cs = v.score + (static_cast<size_t>(seq) * v.heads + head) * v.cap;
   const int n_cand = T - r;
+  const bool local = n_cand <= held;
+  if (local && h > 0) {
+    int p = 4 * tid;
+    for (; p + 3 < n_cand; p += 4 * kSelectThreads) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + p);
+      *reinterpret_cast<uint4*>(keys + p) =
+          make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
+    }
+    for (; p < n_cand; ++p) keys[p] = score_key(cs[p]);
+  }
+  auto key = [&](int p) { return local ? keys[p] : score_key(cs[p]); };
   // Keep candidate p iff its key is above tau, or equals tau and p is not
-  // among the first `skip` candidates of that key: an MSB-first radix select.
+  // among the first `skip` candidates of that key.
   unsigned tau = 0xffffffffu;
   int skip = 0x7fffffff;
   if (h > 0) {
     unsigned prefix = 0, mask = 0;
     int rank = n_cand - h;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += nt) hist[i] = 0;
+    for (int shift = 32 - kDigit; mask != 0xffffffffu; shift -= kDigit) {
+      const int s = max(shift, 0), bits = shift < 0 ? kDigit + shift : kDigit;
+      const unsigned low = (1u << bits) - 1;
+      for (int i = tid; i < 1 << kDigit; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
-      for (int p = tid; p < n_cand; p += nt) {
-        const unsigned u = score_key(cs[p]);
-        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+      for (int p = tid; p < n_cand; p += kSelectThreads) {
+        const unsigned u = key(p);
+        if ((u & mask) == prefix) atomicAdd(&hist[(u >> s) & low], 1u);
       }
       __syncthreads();
-      radix_pick(hist, rank, prefix, shift, &s_prefix, &s_rank);
+      // the bin of the rank-th key: two bins a thread, one block scan
+      const int a = static_cast<int>(hist[2 * tid]), b = static_cast<int>(hist[2 * tid + 1]);
+      int total;
+      const int before = block_exclusive_scan(a + b, wsum, &total);
+      if (before <= rank && rank < before + a + b) {
+        const bool second = rank >= before + a;
+        s_prefix = prefix | (static_cast<unsigned>(2 * tid + second) << s);
+        s_rank = rank - before - (second ? a : 0);
+      }
       __syncthreads();
       prefix = s_prefix;
       rank = s_rank;
-      mask |= 0xffu << shift;
+      mask |= low << s;
     }
     tau = prefix;
     skip = rank;
   }
-  const int seg = (T + nt - 1) / nt;
-  const int p0 = min(T, tid * seg), p1 = min(T, p0 + seg);
-  int eq = 0;
-  if (h > 0)
-    for (int p = p0; p < min(p1, n_cand); ++p) eq += score_key(cs[p]) == tau;
-  int dummy;
-  const int eq_base = block_exclusive_scan(eq, wsum, &dummy);
-  auto keep = [&](int p, int& q) -> bool {
-    if (p >= n_cand) return true;
-    if (h == 0) return false;
-    const unsigned u = score_key(cs[p]);
-    return u > tau || (u == tau && q++ >= skip);
-  };
-  int mine = 0;
-  {
-    int q = eq_base;
-    for (int p = p0; p < p1; ++p) mine += keep(p, q);
+  // a warp's part: whole groups of 32 candidates, counted above and at tau
+  const int groups = (T + 31) / 32, per = (groups + kSelectWarps - 1) / kSelectWarps;
+  const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
+  int above = 0, equal = 0;  // above: kept whatever the ties are
+  for (int g = g0; g < g1; ++g) {
+    const int p = 32 * g + lane;
+    const bool cand = p < n_cand && h > 0;
+    const unsigned u = cand ? key(p) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, cand ? u > tau : p >= n_cand && p < T));
+    equal += __popc(__ballot_sync(0xffffffffu, cand && u == tau));
   }
-  int s = block_exclusive_scan(mine, wsum, &dummy);
+  int dummy;
+  const int eq0 = __shfl_sync(0xffffffffu, block_exclusive_scan(lane ? 0 : equal, wsum, &dummy), 0);
+  const int ties = max(0, eq0 + equal - max(skip, eq0));  // of this part, those past the skipped
+  int at = __shfl_sync(0xffffffffu, block_exclusive_scan(lane ? 0 : above + ties, wsum, &dummy), 0);
   const size_t out = ((static_cast<size_t>(blockIdx.z) * n + e) * v.heads + head) * k;
-  int q = eq_base;
-  for (int p = p0; p < p1; ++p)
-    if (keep(p, q)) {
-      const int page = held_page(v, seq, p >> v.shift);
+  const unsigned below = (1u << lane) - 1;
+  int eq = eq0;
+  for (int g = g0; g < g1; ++g) {
+    const int p = 32 * g + lane;
+    const bool cand = p < n_cand && h > 0;
+    const unsigned u = cand ? key(p) : 0u;
+    const unsigned same = __ballot_sync(0xffffffffu, cand && u == tau);
+    const bool keep = cand ? u > tau || (u == tau && eq + __popc(same & below) >= skip)
+                           : p >= n_cand && p < T;
+    const unsigned all = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const int s = at + __popc(all & below), page = held_page(v, seq, p >> v.shift);
       where[out + s] = page < 0 ? -1 : (page << v.shift) + (p & (v.page - 1));
       kept[out + s] = cs[p];
-      ++s;
     }
+    at += __popc(all);
+    eq += __popc(same);
+  }
 }
 
 // One warp per kGather kept slots of a head: all loads of a lane are in flight
@@ -504,14 +571,15 @@ constexpr int kGather = 4;
 template <int ROW>
 __global__ void __launch_bounds__(256)
     compact_gather_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs, int k,
-                          const int32_t* __restrict__ fresh_all, int fresh_stride,
-                          const int32_t* __restrict__ plan_all, const int32_t* __restrict__ where,
-                          const float* __restrict__ kept) {
+                          const int32_t* fresh_all, int fresh_stride,
+                          const int32_t* plan_all, const int32_t* where,
+                          const float* kept) {
   constexpr int CH = ROW / 16;                     // 16-byte chunks of a vector
   constexpr int PER = 2 * CH;                      // chunks of a slot: key, then value
   constexpr int NC = (PER * kGather + 31) / 32;    // chunks per lane
   const PoolView v = at_layer(v0, blockIdx.z);
   const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
+  grid_dependency_wait();
   const int first = plan_all[(static_cast<size_t>(blockIdx.z) * n + e) * kPlanInts];
   if (first < 0) return;
   const int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.z) * fresh_stride + first;
@@ -573,9 +641,14 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
                                                         share ? n : n * v.width, plan);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid((n * v.heads + 7) / 8, (v.cap + kSlab - 1) / kSlab, layers);
-  fork_copy_kernel<<<grid, 256, 0, stream>>>(v, n, src, dst, share, plan);
-  return cudaGetLastError();
+  // a warp per task where the tasks fill the GPU, else a block (32 heads x 4
+  // entries, 50 tokens each: 19.4 us by warps, see the design notes for blocks)
+  const int tasks = n * v.heads, slabs = (v.cap + kSlab - 1) / kSlab;
+  const bool many = static_cast<long>(tasks) * layers >= 8192;
+  const int per_block = many ? 8 : 1;
+  const dim3 grid((tasks + per_block - 1) / per_block, slabs, layers);
+  return launch_after(many ? fork_copy_kernel<32> : fork_copy_kernel<256>, grid, 256, 0, stream, v, n,
+                      src, dst, share, static_cast<const int32_t*>(plan));
 }
 
 cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
@@ -597,8 +670,8 @@ cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void
   auto vv = static_cast<const __nv_bfloat16*>(V);
   auto kern = v.d == 128 ? (v.kscale ? write_kernel<128, true> : write_kernel<128, false>)
                          : (v.kscale ? write_kernel<64, true> : write_kernel<64, false>);
-  kern<<<grid, 256, 0, stream>>>(v, n, seqs, kk, vv, T, score, plan);
-  return cudaGetLastError();
+  return launch_after(kern, grid, 256, 0, stream, v, n, seqs, kk, vv, T, score,
+                      static_cast<const int32_t*>(plan));
 }
 
 cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* seqs, int h, int r,
@@ -607,15 +680,21 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
   const int k = h + r;
   if (n == 0 || k >= v.cap) return cudaSuccess;  // no sequence can be longer than h + r
   const int stride = n * ((k + v.page - 1) >> v.shift);
-  compact_select_kernel<<<dim3(v.heads + 1, n, layers), kSelectThreads, 0, stream>>>(
-      v, n, seqs, h, r, fresh, stride, plan, where, kept);
-  cudaError_t e = cudaGetLastError();
+  // the keys of a row in shared memory, where rows can be that long
+  const int held = std::min(v.cap, kSelectKeys);
+  static int opted_in[kMaxDevices] = {};
+  cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(compact_select_kernel),
+                                   kSelectKeys * sizeof(unsigned), opted_in);
   if (e != cudaSuccess) return e;
+  compact_select_kernel<<<dim3(v.heads + 1, n, layers), kSelectThreads, held * sizeof(unsigned),
+                          stream>>>(v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const dim3 grid(n * v.heads, (k + 8 * kGather - 1) / (8 * kGather), layers);
   auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>
               : v.row_bytes == 128 ? compact_gather_kernel<128> : compact_gather_kernel<64>;
-  kern<<<grid, 256, 0, stream>>>(v, n, seqs, k, fresh, stride, plan, where, kept);
-  return cudaGetLastError();
+  return launch_after(kern, grid, 256, 0, stream, v, n, seqs, k, static_cast<const int32_t*>(fresh),
+                      stride, static_cast<const int32_t*>(plan), static_cast<const int32_t*>(where),
+                      static_cast<const float*>(kept));
 }
 
 }  // namespace h2o

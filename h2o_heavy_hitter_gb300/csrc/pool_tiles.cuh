@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "device_state.h"
 #include "kernels.h"
 #include "pool.h"
 #include "scan.cuh"
@@ -58,23 +59,6 @@ cudaError_t pool_prefix_score(const AttendParams& p, cudaStream_t stream);
 // a page's tokens x 64 channels (bf16, 128-byte swizzle) or x all codes (E4M3).
 cudaError_t query_map(CUtensorMap* m, const AttendArgs& a, int entries);
 cudaError_t page_map(CUtensorMap* m, const void* base, const PoolView& v);
-
-// A launch that may begin while the kernel before it drains.
-template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, size_t smem,
-                         cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = grid;
-  lc.blockDim = dim3(static_cast<unsigned>(threads));
-  lc.dynamicSmemBytes = smem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, args...);
-}
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------------ bounded waits
