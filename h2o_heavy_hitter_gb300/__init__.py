@@ -505,11 +505,16 @@ def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=No
     pq = _ptr(pool, q, torch.bfloat16, shape, "q")
     if out is None:
         out = torch.empty_like(q)
+        po = out.data_ptr()
+    else:
+        po = _ptr(pool, out, torch.bfloat16, shape, "out")
     if lse is None:
-        lse = q.new_empty(shape[:2], dtype=torch.float32)
-    _check(load_library().h2o_pool_attend(
-        pool.handle, layer, n, ps, prefix, pq, heads, _ptr(pool, out, torch.bfloat16, shape, "out"),
-        _ptr(pool, lse, torch.float32, shape[:2], "lse"), accumulate))
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+        pl = lse.data_ptr()
+    else:
+        pl = _ptr(pool, lse, torch.float32, shape[:2], "lse")
+    _check(load_library().h2o_pool_attend(pool.handle, layer, n, ps, prefix, pq, heads, po, pl,
+                                          accumulate))
     return out, lse
 
 

@@ -66,7 +66,12 @@ struct AttendArgs {
   void* out;             // bf16 [n][heads * group][d]
   float* lse;            // [n][heads * group], natural log; may be null
   int accumulate;        // add the probabilities to the scores
+  const CUtensorMap* kmap;  // host: the layer's keys and values (pool_page_map)
+  const CUtensorMap* vmap;
 };
+// Tensor map of a layer's keys or values in boxes of a page's tokens x 64
+// channels (bf16, 128-byte swizzle) or x all codes (E4M3).
+cudaError_t pool_page_map(CUtensorMap* m, const void* base, const PoolView& v);
 size_t pool_attend_scratch(const AttendArgs& a);
 cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream);
 }  // namespace h2o

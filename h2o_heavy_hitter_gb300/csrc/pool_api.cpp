@@ -6,6 +6,7 @@
 
 #include <new>
 #include <string>
+#include <vector>
 
 #include "h2o.h"
 #include "host.h"
@@ -19,6 +20,7 @@ struct h2o_pool {
   int kv_format = 0;
   void* base = nullptr;  // single allocation
   h2o::PoolView v{};     // layer 0
+  std::vector<CUtensorMap> maps;  // keys and values of every layer
 };
 
 namespace {
@@ -180,6 +182,17 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
   v.table = reinterpret_cast<int32_t*>(take(table));
   cudaError_t e = cudaMemsetAsync(p->base, 0, zeros, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(v.pos, 0xff, per_slot + table, s);
+  try {
+    p->maps.resize(2 * L);
+  } catch (const std::exception&) {
+    h2o_pool_destroy(p);
+    return fail(H2O_ENOMEM, "out of host memory");
+  }
+  for (int l = 0; l < layers && e == cudaSuccess; ++l) {
+    const h2o::PoolView x = layer_view(p, l);
+    e = h2o::pool_page_map(&p->maps[2 * l], x.K, x);
+    if (e == cudaSuccess) e = h2o::pool_page_map(&p->maps[2 * l + 1], x.V, x);
+  }
   if (e != cudaSuccess) {
     h2o_pool_destroy(p);
     return cuda_fail(e, "pool initialisation");
@@ -292,6 +305,8 @@ int h2o_pool_attend(h2o_pool* p, int layer, int n, const int32_t* seqs, int pref
     a.out = out;
     a.lse = lse;
     a.accumulate = accumulate != 0;
+    a.kmap = &p->maps[2 * layer];
+    a.vmap = &p->maps[2 * layer + 1];
     cudaStream_t s = current_stream();
     Scratch mem(h2o::pool_attend_scratch(a), s);
     return launch_status(h2o::pool_attend(a, mem.p, s), "pool attention launch");

@@ -871,12 +871,12 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, void* base, Atte
 
 template <int D, bool F8>
 cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, t1, tk, tv;
+  CUtensorMap tq, t1;
+  const CUtensorMap &tk = *p.a.kmap, &tv = *p.a.vmap;
   cudaError_t e;
-  if ((e = query_map(&tq, p.a, p.s.few ? p.s.n : 1)) != cudaSuccess) return e;
   if ((e = query_map(&t1, p.a, 1)) != cudaSuccess) return e;
-  if ((e = page_map(&tk, p.a.v.K, p.a.v)) != cudaSuccess) return e;
-  if ((e = page_map(&tv, p.a.v.V, p.a.v)) != cudaSuccess) return e;
+  tq = t1;  // used for a prefix with few rows only
+  if (p.s.few && (e = query_map(&tq, p.a, p.s.n)) != cudaSuccess) return e;
   const bool many = p.a.prefix >= 0 && !p.s.few;
   if (many && (e = pool_prefix(p, stream)) != cudaSuccess) return e;
   using C = Cfg<D, F8>;
@@ -910,7 +910,7 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t page_map(CUtensorMap* m, const void* base, const PoolView& v) {
+cudaError_t pool_page_map(CUtensorMap* m, const void* base, const PoolView& v) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   const bool codes = v.kscale != nullptr;

@@ -681,17 +681,11 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ host side
-cudaError_t maps(const AttendParams& p, CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
-  cudaError_t e = query_map(tq, p.a, p.s.per_tile);
-  if (e == cudaSuccess) e = page_map(tk, p.a.v.K, p.a.v);
-  if (e == cudaSuccess && tv) e = page_map(tv, p.a.v.V, p.a.v);
-  return e;
-}
-
 template <int D, bool F8>
 cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, tk, tv;
-  cudaError_t e = maps(p, &tq, &tk, &tv);
+  CUtensorMap tq;
+  const CUtensorMap &tk = *p.a.kmap, &tv = *p.a.vmap;
+  cudaError_t e = query_map(&tq, p.a, p.s.per_tile);
   if (e != cudaSuccess) return e;
   using C = Cfg<D, F8>;
   static int opted_in[kMaxDevices] = {};
@@ -704,8 +698,9 @@ cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
 
 template <int D, bool F8>
 cudaError_t score_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, tk;
-  cudaError_t e = maps(p, &tq, &tk, nullptr);
+  CUtensorMap tq;
+  const CUtensorMap& tk = *p.a.kmap;
+  cudaError_t e = query_map(&tq, p.a, p.s.per_tile);
   if (e != cudaSuccess) return e;
   using C = ScoreCfg<D, F8>;
   static int opted_in[kMaxDevices] = {};

@@ -54,11 +54,9 @@ struct AttendParams {
 // first leaves pieces, the second adds the prefix's scores.
 cudaError_t pool_prefix(const AttendParams& p, cudaStream_t stream);
 cudaError_t pool_prefix_score(const AttendParams& p, cudaStream_t stream);
-// Tensor maps (pool_attend.cu): queries [n][heads][group][d] in boxes of
-// `entries` groups of one head x 64 channels; a pool's keys or values in boxes of
-// a page's tokens x 64 channels (bf16, 128-byte swizzle) or x all codes (E4M3).
+// Tensor map of the queries [n][heads][group][d] in boxes of `entries` groups of
+// one head x 64 channels (pool_attend.cu).
 cudaError_t query_map(CUtensorMap* m, const AttendArgs& a, int entries);
-cudaError_t page_map(CUtensorMap* m, const void* base, const PoolView& v);
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------------ bounded waits
