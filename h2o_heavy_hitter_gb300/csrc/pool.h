@@ -70,8 +70,8 @@ struct AttendArgs {
   const CUtensorMap* vmap;
 };
 // Tensor map of a layer's keys or values in boxes of a page's tokens x 64
-// channels (bf16, 128-byte swizzle) or x all codes (E4M3).
-cudaError_t pool_page_map(CUtensorMap* m, const void* base, const PoolView& v);
+// channels (bf16, 128-byte swizzle) or x all codes (E4M3; keys swizzled by d bytes).
+cudaError_t pool_page_map(CUtensorMap* m, const PoolView& v, bool keys);
 size_t pool_attend_scratch(const AttendArgs& a);
 cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream);
 }  // namespace h2o

@@ -190,8 +190,8 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
   }
   for (int l = 0; l < layers && e == cudaSuccess; ++l) {
     const h2o::PoolView x = layer_view(p, l);
-    e = h2o::pool_page_map(&p->maps[2 * l], x.K, x);
-    if (e == cudaSuccess) e = h2o::pool_page_map(&p->maps[2 * l + 1], x.V, x);
+    e = h2o::pool_page_map(&p->maps[2 * l], x, true);
+    if (e == cudaSuccess) e = h2o::pool_page_map(&p->maps[2 * l + 1], x, false);
   }
   if (e != cudaSuccess) {
     h2o_pool_destroy(p);

@@ -191,13 +191,14 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int RK = 2 * (128 / D), RV = (F8 ? 1 : 3) * (128 / D);  // slots of tiles
-  static constexpr int S = F8 ? 3 * (128 / D) : 1;                         // slots of codes
-  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
+  static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;  // keys are used as they are stored
+  static constexpr int RK = (F8 ? 3 : 2) * (128 / D), RV = (F8 ? 2 : 3) * (128 / D);
+  static constexpr int S = F8 ? 2 * (128 / D) : 1;  // slots of value codes
+  static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
   static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
   static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
-  static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(RK + RV) * TILE + 2 * Q + 4 * P + CODES + SCALES +
+  static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(RK) * KTILE + RV * TILE + 2 * Q + 4 * P + CODES + SCALES +
                                  sizeof(List) + 3072 + 1024;
   // TMEM: S^T of warpgroup t in columns 64 t + 32 (0, 1), its O^T at 128 + 32 t
   static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
@@ -207,7 +208,7 @@ template <int RK, int RV, int S>
 struct Bars {
   RingBars<RK> keys;
   RingBars<RV> values;
-  CodeBars<S> codes;
+  RingBars<S> codes;
   uint64_t q_full[2], q_empty[2];  // by unit
   uint64_t s_full[2][2];           // [warpgroup][buffer]
   uint64_t p_ready[2][2];
@@ -256,6 +257,7 @@ __device__ __forceinline__ float warp_sums(const float (&x)[CH], int lane) {
 struct TileRows {
   uint32_t s_tm;
   float ks, vs;   // scales of the key's logits and of its value
+  float fac;      // E4M3: scale of row `lane`'s logits
   bool live;      // the key lies before the sequence's end
   uint8_t* p;     // row 0 of the P operand at this key's place in a 16-byte chunk
   int chunk;      // that chunk
@@ -267,7 +269,7 @@ struct TileRows {
 // time (unused ones are computed and dropped: branches would serialise the
 // reductions). Raises m only where it grows by more than 2^8 (alpha, rescale);
 // sum: row `lane`'s over this warp's keys. False: the exchange gave up.
-template <int CH, typename Exchange>
+template <int CH, bool F8, typename Exchange>
 __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float& alpha,
                                              bool& rescale, float& sum, Exchange&& exchange) {
   const int lane = threadIdx.x & 31;
@@ -279,7 +281,8 @@ __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float&
     float top[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const float z = a.live ? __uint_as_float(s[i]) * a.ks : -INFINITY;
+      const float k = F8 ? a.ks * __shfl_sync(0xffffffffu, a.fac, r0 + i) : a.ks;
+      const float z = a.live ? __uint_as_float(s[i]) * k : -INFINITY;
       top[i] = order_value(__reduce_max_sync(0xffffffffu, order_key(z)));
       if (a.logits && a.live && r0 + i < a.rows) a.logits[static_cast<size_t>(r0 + i) * a.cap] = z;
     }
@@ -308,7 +311,8 @@ __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float&
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const float n = __shfl_sync(0xffffffffu, ref, r0 + i);
-      pr[i] = a.live ? ex2(fmaf(__uint_as_float(s[i]), a.ks, -n)) : 0.f;
+      const float k = F8 ? a.ks * __shfl_sync(0xffffffffu, a.fac, r0 + i) : a.ks;
+      pr[i] = a.live ? ex2(fmaf(__uint_as_float(s[i]), k, -n)) : 0.f;
       // K-major, 128-byte swizzle: 16-byte chunk (key / 8) of a row at chunk ^ (row & 7)
       const int row = r0 + i;
       *reinterpret_cast<__nv_bfloat16*>(a.p + row * 128 + ((a.chunk ^ (row & 7)) << 4)) =
@@ -323,6 +327,7 @@ __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float&
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     pool_rows_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap t1,
+                     const __grid_constant__ CUtensorMap tq2, const __grid_constant__ CUtensorMap t2,
                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const __grid_constant__ AttendParams p) {
   using C = Cfg<D, F8>;
@@ -330,12 +335,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sK = smem;
-  uint8_t* sV = sK + RK * C::TILE;
+  uint8_t* sV = sK + RK * C::KTILE;
   uint8_t* sQ = sV + RV * C::TILE;
   uint8_t* sP = sQ + 2 * C::Q;
   uint8_t* codes = sP + 4 * C::P;
-  float* scales = reinterpret_cast<float*>(codes + C::CODES);
-  List& list = *reinterpret_cast<List*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  float* kscales = reinterpret_cast<float*>(codes + C::CODES);  // [RK][128]
+  float* cscales = kscales + RK * TILE_KEYS;                    // [S][128], of value codes
+  float* vscales = cscales + C::S * TILE_KEYS;                  // [kScaleTiles][128]
+  List& list = *reinterpret_cast<List*>(reinterpret_cast<uint8_t*>(kscales) + C::SCALES);
   auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(&list + 1);
   static_assert(sizeof(Bars<RK, RV, C::S>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
@@ -343,8 +350,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < RK; ++i) {
-      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->keys.empty[i], 1);
+      mbar_init(&bars->keys.full[i], 1);
+      mbar_init(&bars->keys.empty[i], F8 ? 1 + 4 : 1);  // the product, and the readers of the scales
     }
     for (int i = 0; i < RV; ++i) {
       mbar_init(&bars->values.full[i], F8 ? kCodeThreads / 32 : 1);
@@ -354,7 +361,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
@@ -395,25 +401,29 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 
   if (warp == 0) {
     if constexpr (F8)
-      fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
+      produce_codes<D>(v, &tk, v.kscale, sK, kscales, bars->keys, TileCursor(w));
     else
       produce_tma<D>(v, &tk, sK, bars->keys, TileCursor(w));
-  } else if (!F8 && warp == kWarpV) {
-    produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
+  } else if (warp == kWarpV) {
+    if constexpr (F8)
+      produce_codes<D>(v, &tv, v.vscale, codes, cscales, bars->codes, TileCursor(w));
+    else
+      produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, RK, RV, C::S, true, kCodeThreads>(
-        v, codes, bars->codes, sK, bars->keys, sV, &bars->values, scales, TileCursor(w),
-        threadIdx.x - 32 * kWarpCodes);
+    convert_values<D, RV, C::S, kCodeThreads>(v, codes, cscales, bars->codes, sV, bars->values, vscales,
+                                              TileCursor(w), threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       for (int e = 0; w.next(); ++e) {
         const int qb = e & 1;
         if (e >= 2 && !pool_wait(&bars->q_empty[qb], ((e >> 1) - 1) & 1, v.err)) break;
         mbar_arrive_expect_tx(&bars->q_full[qb], w.rows() * D * 2);
+        // boxes of 64 channels, or the two codes of every value
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_4d(sQ + qb * C::Q + c * kQBox, w.prefix ? &tq : &t1, c * 64, 0, w.h,
-                      w.prefix ? 0 : w.b, &bars->q_full[qb]);
+        for (int c = 0; c < (F8 ? 2 : D / 64); ++c)
+          tma_load_4d(sQ + qb * C::Q + c * (F8 ? kFewRows * D : kQBox),
+                      c == 1 && F8 ? (w.prefix ? &tq2 : &t2) : (w.prefix ? &tq : &t1), F8 ? 0 : c * 64, 0,
+                      w.h, w.prefix ? 0 : w.b, &bars->q_full[qb]);
       }
     }
   } else if (warp == kWarpMMA) {
@@ -423,7 +433,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     // of the warpgroup's tile before the last, whose O^T is issued by then; the
     // MMAs of one thread complete in order.
     if (lane == 0) {
-      const uint64_t dk0 = desc_kmajor<D>(sK, 0), dq0 = smem_desc(sQ, 16, 1024);
+      const uint64_t dk0 = F8 ? desc_codes<D>(sK) : desc_kmajor<D>(sK, 0);
+      const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : smem_desc(sQ, 16, 1024);
       const uint64_t dp0 = smem_desc(sP, 16, 1024);
       // V^T = the V tile with d as the long side of A (MN-major): 64 channels a box;
       // d = 64 has one box, which then serves as rows 64..127 too (not read)
@@ -457,7 +468,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       };
       while (ok && w.next()) {
         const int t = e & 1, qb = e & 1;
-        const uint32_t idesc = idesc_bf16(TILE_KEYS, w.rows() <= 16 ? 16 : 32, 0, 0);
+        const int cols = w.rows() <= 16 ? 16 : 32;
+        const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0), idesc8 = idesc_e4m3(TILE_KEYS, cols);
         if (!pool_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
           const uint32_t st = g % RK, buf = c[t] & 1;
@@ -466,12 +478,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+          const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::Q >> 4));
+          const uint32_t d_tm = tmem + t * 64 + buf * 32;
+          if constexpr (F8) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tmem + t * 64 + buf * 32, kb + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
-                    qd + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
+              umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
+                           qd + kk / (D / 32) * (kFewRows * D >> 4) + kk % (D / 32) * 2, idesc8, kk > 0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(d_tm, kb + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
+                      qd + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+          }
           umma_commit(&bars->s_full[t][buf]);
           umma_commit(&bars->keys.empty[st]);
           if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
@@ -526,6 +546,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         logits = p.w.logits + (static_cast<size_t>(w.b) * p.s.heads + w.h) * rows * v.cap;
       }
       float m = -INFINITY, l = 0.f;  // of row `lane`
+      float fac = 1.f;               // E4M3: of row `lane`'s codes
+      if (F8 && lane < rows)
+        fac = p.w.qfac[w.prefix ? (static_cast<size_t>(lane / p.s.group) * p.s.heads + w.h) * p.s.group +
+                                      lane % p.s.group
+                                : (static_cast<size_t>(w.b) * p.s.heads + w.h) * p.s.group + lane];
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g, ++c) {
         const uint32_t buf = c & 1, st = g % RV;
         const uint32_t s_tm = tmem + lane_off + t * 64 + buf * 32;
@@ -536,17 +561,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           break;
         }
         float ks = p.qscale, vs = 1.f;
+        if (F8) {
+          // the keys' product is done, so their tile has arrived; it stays until the arrival here
+          if (!pool_warp_wait(&bars->keys.full[g % RK], (g / RK) & 1, v.err)) {
+            ok = false;
+            break;
+          }
+          ks *= kscales[g % RK * TILE_KEYS + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->keys.empty[g % RK]);
+        }
         if (F8 || valid < TILE_KEYS) {
           // the value tile stays in its slot until this warpgroup's probabilities are used
-          if (!pool_warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
-                         F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
+          if (!pool_warp_wait(&bars->values.full[st], (g / RV) & 1, v.err)) {
             ok = false;
             break;
           }
           if (F8) {
-            const float* sc = scales + (g % kScaleTiles<true>) * 2 * TILE_KEYS + r;
-            ks *= sc[0];
-            vs = sc[TILE_KEYS];
+            vs = vscales[g % kScaleTiles * TILE_KEYS + r];
           } else {  // values behind the end count as zero, whatever they are
             for (int i = r; i < (TILE_KEYS - valid) * (D / 8); i += 128) {
               const int row = valid + i / (D / 8), ch = i % (D / 8);
@@ -558,12 +590,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         tc_fence_after();
         float alpha = 1.f, sum;
         bool rescale = false;
-        const TileRows tr{s_tm, ks, vs, live,
+        const TileRows tr{s_tm, ks, vs, fac, live,
                           sP + (t * 2 + buf) * C::P + (r >> 6) * kQBox + (r & 7) * 2, (r & 63) >> 3,
                           logits ? logits + kt * TILE_KEYS + r : nullptr, v.cap, rows};
-        const bool done = rows == 1   ? tile_softmax<1>(tr, m, alpha, rescale, sum, exchange)
-                          : rows <= 4 ? tile_softmax<4>(tr, m, alpha, rescale, sum, exchange)
-                                      : tile_softmax<8>(tr, m, alpha, rescale, sum, exchange);
+        const bool done = rows == 1   ? tile_softmax<1, F8>(tr, m, alpha, rescale, sum, exchange)
+                          : rows <= 4 ? tile_softmax<4, F8>(tr, m, alpha, rescale, sum, exchange)
+                                      : tile_softmax<8, F8>(tr, m, alpha, rescale, sum, exchange);
         if (!done) {
           ok = false;
           break;
@@ -629,6 +661,61 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+}
+
+// ------------------------------------------------------------------ queries of an E4M3 pool
+// A query row as two E4M3 codes a value, x = fac (first + second): the row is
+// scaled by a power of two to a magnitude in [128, 256); the first code has the
+// upper four of a bf16 value's eight significant bits, the second what is left,
+// down to steps of 2^-9: no more than 2^-17 of the row's largest value is lost in
+// any value. A row with an infinity or a NaN gets a NaN for its factor. A warp
+// per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+    pool_split_queries_kernel(const __nv_bfloat16* __restrict__ q, int rows, uint8_t* q8, float* qfac) {
+  constexpr int N = D / 32;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  uint32_t raw[N / 2];
+  if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(raw) = reinterpret_cast<const uint2*>(q + static_cast<size_t>(row) * D)[lane];
+  else
+    raw[0] = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(row) * D)[lane];
+  float x[N], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = __uint_as_float(i & 1 ? raw[i / 2] & 0xffff0000u : raw[i / 2] << 16);
+    amax = fmaxf(amax, fabsf(x[i]));
+  }
+  bool wild = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) wild |= !(fabsf(x[i]) < INFINITY);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  wild = __any_sync(0xffffffffu, wild);
+  // 2^(7 - exponent of amax), within fp32's normal numbers
+  const int e = min(max(7 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), -126), 126);
+  const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  uint32_t codes[2] = {0, 0};  // this lane's N codes of each half
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float a = x[i] * up, b = x[i + 1] * up;
+    const uint32_t hi = f32x2_to_e4m3x2(a, b);
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+    codes[0] |= hi << (8 * i);
+    codes[1] |= f32x2_to_e4m3x2(a - f.x, b - f.y) << (8 * i);
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint8_t* out = q8 + (static_cast<size_t>(half) * rows + row) * D + lane * N;
+    if constexpr (N == 4)
+      *reinterpret_cast<uint32_t*>(out) = codes[half];
+    else
+      *reinterpret_cast<uint16_t*>(out) = static_cast<uint16_t>(codes[half]);
+  }
+  if (lane == 0)
+    qfac[row] = wild ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -842,7 +929,8 @@ Shape shape_of(const AttendArgs& a, int sms) {
   return s;
 }
 
-size_t scratch_layout(const Shape& s, int cap, bool accumulate, void* base, AttendScratch* out) {
+size_t scratch_layout(const Shape& s, int cap, bool accumulate, bool codes, void* base,
+                      AttendScratch* out) {
   size_t at = 0;
   auto take = [&](size_t bytes) -> char* {
     if (!bytes) return nullptr;
@@ -865,18 +953,35 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, void* base, Atte
   w.to = reinterpret_cast<float*>(take(trow * s.d * sizeof(float)));
   w.logits = reinterpret_cast<float*>(take(accumulate ? all * cap * sizeof(float) : 0));
   w.plogits = reinterpret_cast<float*>(take(accumulate && s.few ? all * cap * sizeof(float) : 0));
+  w.q8 = reinterpret_cast<uint8_t*>(take(codes ? 2 * all * s.d : 0));
+  w.qfac = reinterpret_cast<float*>(take(codes ? all * sizeof(float) : 0));
   if (out) *out = w;
   return at;
 }
 
 template <int D, bool F8>
 cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq, t1;
+  CUtensorMap tq, t1, tq2, t2;  // tq: for a prefix with few rows only; the second codes: E4M3 only
   const CUtensorMap &tk = *p.a.kmap, &tv = *p.a.vmap;
   cudaError_t e;
-  if ((e = query_map(&t1, p.a, 1)) != cudaSuccess) return e;
-  tq = t1;  // used for a prefix with few rows only
-  if (p.s.few && (e = query_map(&tq, p.a, p.s.n)) != cudaSuccess) return e;
+  if (F8) {
+    const int rows = p.s.n * p.s.heads * p.s.group;
+    pool_split_queries_kernel<D><<<(rows + 7) / 8, 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(p.a.q), rows, p.w.q8, p.w.qfac);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = query_code_map(&t1, p, 0, 1)) != cudaSuccess) return e;
+    if ((e = query_code_map(&t2, p, 1, 1)) != cudaSuccess) return e;
+  } else {
+    if ((e = query_map(&t1, p.a, 1)) != cudaSuccess) return e;
+    t2 = t1;
+  }
+  tq = t1;
+  tq2 = t2;
+  if (p.s.few) {
+    e = F8 ? query_code_map(&tq, p, 0, p.s.n) : query_map(&tq, p.a, p.s.n);
+    if (e == cudaSuccess && F8) e = query_code_map(&tq2, p, 1, p.s.n);
+    if (e != cudaSuccess) return e;
+  }
   const bool many = p.a.prefix >= 0 && !p.s.few;
   if (many && (e = pool_prefix(p, stream)) != cudaSuccess) return e;
   using C = Cfg<D, F8>;
@@ -886,9 +991,10 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
     return e;
   if (many) {
     e = launch_after(pool_rows_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream, tq, t1,
-                     tk, tv, p);
+                     tq2, t2, tk, tv, p);
   } else {
-    pool_rows_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, t1, tk, tv, p);
+    pool_rows_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, t1, tq2, t2, tk, tv,
+                                                                            p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
@@ -910,38 +1016,57 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t pool_page_map(CUtensorMap* m, const void* base, const PoolView& v) {
+namespace {
+cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
+                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
-  const bool codes = v.kscale != nullptr;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(v.d),
-                        static_cast<cuuint64_t>(v.pages) * v.heads * v.page};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(v.row_bytes)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(codes ? v.d : 64), static_cast<cuuint32_t>(v.page)};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, type, rank, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Swizzle of E4M3 operands with rows of d bytes.
+CUtensorMapSwizzle code_swizzle(int d) {
+  return d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+}
+
+cudaError_t queries(CUtensorMap* m, const AttendArgs& a, int entries, const void* base, bool codes) {
+  const cuuint64_t d = a.v.d, g = a.group, h = a.v.heads, row = codes ? d : 2 * d;
+  const cuuint64_t dims[4] = {d, g, h, static_cast<cuuint64_t>(a.n)};
+  const cuuint64_t strides[3] = {row, g * row, h * g * row};
+  const cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(d) : 64, static_cast<cuuint32_t>(a.group), 1,
+                             static_cast<cuuint32_t>(entries)};
+  return encode(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+                strides, box, codes ? code_swizzle(a.v.d) : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+}  // namespace
+
+cudaError_t pool_page_map(CUtensorMap* m, const PoolView& v, bool keys) {
+  const bool codes = v.kscale != nullptr;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(v.d),
+                              static_cast<cuuint64_t>(v.pages) * v.heads * v.page};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(v.row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(codes ? v.d : 64), static_cast<cuuint32_t>(v.page)};
+  return encode(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                keys ? v.K : v.V, dims, strides, box,
+                !codes ? CU_TENSOR_MAP_SWIZZLE_128B : keys ? code_swizzle(v.d) : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 cudaError_t query_map(CUtensorMap* m, const AttendArgs& a, int entries) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t d = a.v.d, g = a.group, h = a.v.heads;
-  cuuint64_t dims[4] = {d, g, h, static_cast<cuuint64_t>(a.n)};
-  cuuint64_t strides[3] = {d * 2, g * d * 2, h * g * d * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.group), 1, static_cast<cuuint32_t>(entries)};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims, strides,
-                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return queries(m, a, entries, a.q, false);
+}
+
+cudaError_t query_code_map(CUtensorMap* m, const AttendParams& p, int half, int entries) {
+  const size_t rows = static_cast<size_t>(p.s.n) * p.s.heads * p.s.group;
+  return queries(m, p.a, entries, p.w.q8 + half * rows * p.s.d, true);
 }
 
 size_t pool_attend_scratch(const AttendArgs& a) {
-  return scratch_layout(shape_of(a, num_sms()), a.v.cap, a.accumulate, nullptr, nullptr);
+  return scratch_layout(shape_of(a, num_sms()), a.v.cap, a.accumulate, a.v.kscale, nullptr, nullptr);
 }
 
 cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream) {
@@ -949,7 +1074,7 @@ cudaError_t pool_attend(const AttendArgs& a, void* scratch, cudaStream_t stream)
   AttendParams p{};
   p.a = a;
   p.s = shape_of(a, num_sms());
-  scratch_layout(p.s, a.v.cap, a.accumulate, scratch, &p.w);
+  scratch_layout(p.s, a.v.cap, a.accumulate, a.v.kscale, scratch, &p.w);
   p.qscale = kLog2e / sqrtf(static_cast<float>(a.v.d));
   if (a.v.kscale) return a.v.d == 128 ? attend_t<128, true>(p, stream) : attend_t<64, true>(p, stream);
   return a.v.d == 128 ? attend_t<128, false>(p, stream) : attend_t<64, false>(p, stream);

@@ -32,19 +32,20 @@ template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int RK = 2 * (128 / D), RV = (F8 ? 1 : 3) * (128 / D);  // slots of tiles
-  static constexpr int S = F8 ? 3 * (128 / D) : 1;                         // slots of codes
-  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
+  static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;  // keys are used as they are stored
+  static constexpr int RK = (F8 ? 3 : 2) * (128 / D), RV = (F8 ? 2 : 3) * (128 / D);
+  static constexpr int S = F8 ? 2 * (128 / D) : 1;  // slots of value codes
+  static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
   static constexpr uint32_t O_COL = 256;  // S buffers at columns 0 and 128, O of half t at 256 + 128 t
-  static constexpr int SCALES = F8 ? kScaleTiles<true> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + RK + RV) * TILE + CODES + SCALES + 1024 + 1024;
+  static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + RV) * TILE + RK * KTILE + CODES + SCALES + 1024 + 1024;
 };
 
 template <int RK, int RV, int S>
 struct Bars {
   RingBars<RK> keys;
   RingBars<RV> values;
-  CodeBars<S> codes;
+  RingBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
   uint64_t o_last[2], o_free[2];               // one phase per unit
@@ -99,7 +100,8 @@ struct TileCursor {
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
-    pool_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+    pool_prefix_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tq2,
+                       const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv,
                        const __grid_constant__ AttendParams p) {
   using C = Cfg<D, F8>;
@@ -108,10 +110,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
   uint8_t* sK = smem + 2 * C::TILE;
-  uint8_t* sV = sK + RK * C::TILE;
+  uint8_t* sV = sK + RK * C::KTILE;
   uint8_t* codes = sV + RV * C::TILE;
-  float* scales = reinterpret_cast<float*>(codes + C::CODES);
-  auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  float* kscales = reinterpret_cast<float*>(codes + C::CODES);  // [RK][128]
+  float* cscales = kscales + RK * TILE_KEYS;                    // [S][128], of value codes
+  float* vscales = cscales + C::S * TILE_KEYS;                  // [kScaleTiles][128]
+  auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(reinterpret_cast<uint8_t*>(kscales) + C::SCALES);
   static_assert(sizeof(Bars<RK, RV, C::S>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -127,8 +131,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->o_free[i], 4);
     }
     for (int i = 0; i < RK; ++i) {
-      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->keys.empty[i], 1);
+      mbar_init(&bars->keys.full[i], 1);
+      mbar_init(&bars->keys.empty[i], F8 ? 1 + 8 : 1);  // the products, and the readers of the scales
     }
     for (int i = 0; i < RV; ++i) {
       mbar_init(&bars->values.full[i], F8 ? kCodeThreads / 32 : 1);
@@ -138,7 +142,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     fence_barrier_init();
   }
   if (warp == kWarpMMA) {
@@ -160,15 +163,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 
   if (warp == 0) {
     if constexpr (F8)
-      fetch_codes<D, C::S, true>(v, &tk, &tv, codes, bars->codes, TileCursor(w));
+      produce_codes<D>(v, &tk, v.kscale, sK, kscales, bars->keys, TileCursor(w));
     else
       produce_tma<D>(v, &tk, sK, bars->keys, TileCursor(w));
-  } else if (!F8 && warp == kWarpV) {
-    produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
+  } else if (warp == kWarpV) {
+    if constexpr (F8)
+      produce_codes<D>(v, &tv, v.vscale, codes, cscales, bars->codes, TileCursor(w));
+    else
+      produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, RK, RV, C::S, true, kCodeThreads>(
-        v, codes, bars->codes, sK, bars->keys, sV, &bars->values, scales, TileCursor(w),
-        threadIdx.x - 32 * kWarpCodes);
+    convert_values<D, RV, C::S, kCodeThreads>(v, codes, cscales, bars->codes, sV, bars->values, vscales,
+                                              TileCursor(w), threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t qn = 0;
@@ -181,10 +186,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             break;
           }
           mbar_arrive_expect_tx(&bars->q_full[qb], p.s.per_tile * p.s.group * D * 2);
+          // boxes of 64 channels, or the two codes of every value
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + qb * C::TILE + c * kBoxBytes, &tq, c * 64, 0, w.h,
-                        (2 * w.b + t) * p.s.per_tile, &bars->q_full[qb]);
+          for (int c = 0; c < (F8 ? 2 : D / 64); ++c)
+            tma_load_4d(sQ + qb * C::TILE + c * (F8 ? C::KTILE : kBoxBytes), c == 1 && F8 ? &tq2 : &tq,
+                        F8 ? 0 : c * 64, 0, w.h, (2 * w.b + t) * p.s.per_tile, &bars->q_full[qb]);
         }
       }
     }
@@ -195,7 +201,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_bf16(TILE_ROWS, TILE_KEYS, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(TILE_ROWS, D, 0, 1);
-      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(sK, 0);
+      const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : desc_kmajor<D>(sQ, 0);
+      const uint64_t dk0 = F8 ? desc_codes<D>(sK) : desc_kmajor<D>(sK, 0);
       const uint64_t dv0 = smem_desc(sV, kBoxBytes, 1024);
       uint32_t g = 0, qn = 0, j = 0;
       int e = 0;
@@ -246,13 +253,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
               break;
             }
             tc_fence_after();
-            const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+            const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
             const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
             const uint32_t d_tm = tmem + (j & 1) * 128;
+            if constexpr (F8) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-              umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
+              for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
+                umma_ss_8bit(d_tm, qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2,
+                             kb + kk % (D / 32) * 2, idesc_e4m3(TILE_ROWS, TILE_KEYS), kk > 0);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+                umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
+              }
             }
             umma_commit(&bars->s_full[j & 1]);
             if (t == nt - 1) umma_commit(&bars->keys.empty[st]);
@@ -290,7 +304,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       const int rows = w.rows(t), step = w.two ? 2 : 1;
       const bool active = quad * 32 < rows;  // warp-uniform
       const int chunks = w.two ? 2 : 1, col0 = w.two ? 0 : 64 * t;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, qscale = p.qscale;
+      if (F8 && r < rows) {  // the row's codes have a scale
+        const int entry = (2 * w.b + (w.two ? t : 0)) * p.s.per_tile + r / p.s.group;
+        qscale *= p.w.qfac[(static_cast<size_t>(entry) * p.s.heads + w.h) * p.s.group + r % p.s.group];
+      }
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
         const uint32_t jj = j0 + (kt - w.kt0) * step, j = w.two ? jj + t : jj;
         const uint32_t s_tm = tmem + lane_off + (j & 1) * 128, st = g % RV;
@@ -299,17 +317,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           break;
         }
         const int valid = w.len - kt * TILE_KEYS;  // may exceed 128
-        if (F8 || valid < TILE_KEYS) {
-          // the value tile stays in its slot until these probabilities are used
-          if (!pool_warp_wait(F8 ? &bars->codes.scaled[g & 1] : &bars->values.full[st],
-                         F8 ? (g >> 1) & 1 : (g / RV) & 1, v.err)) {
-            ok = false;
-            break;
-          }
+        // the value tile stays in its slot until these probabilities are used; the
+        // keys' product is done, so their tile has arrived, and it stays until the arrival below
+        if ((F8 && !pool_warp_wait(&bars->keys.full[g % RK], (g / RK) & 1, v.err)) ||
+            ((F8 || valid < TILE_KEYS) &&
+             !pool_warp_wait(&bars->values.full[st], (g / RV) & 1, v.err))) {
+          ok = false;
+          break;
         }
         tc_fence_after();
-        const float4* ks = reinterpret_cast<const float4*>(scales + (g % kScaleTiles<true>) * 2 * TILE_KEYS);
-        const float4* vs = ks + TILE_KEYS / 4;
+        const float4* ks = reinterpret_cast<const float4*>(kscales + g % RK * TILE_KEYS);
+        const float4* vs = reinterpret_cast<const float4*>(vscales + g % kScaleTiles * TILE_KEYS);
         // 64 logits from column `first`, unscaled by 1 / sqrt(d); those behind the end -inf
         auto load = [&](uint32_t (&s)[64], int first) {
           tmem_ld32(s_tm + first, s);
@@ -345,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                 m4[y] = fmax3(m4[y], __uint_as_float(s[x + y]), __uint_as_float(s[x + 4 + y]));
             mx = fmax3(fmax3(mx, m4[0], m4[1]), m4[2], m4[3]);
           }
-          mx *= p.qscale;
+          mx *= qscale;
           float alpha = 1.f;
           bool rescale = false;
           if (mx > m + 8.f) {
@@ -354,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             m = mx;
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t sc2 = f2_pack(p.qscale, p.qscale), nm2 = f2_pack(-ref, -ref);
+          const uint64_t sc2 = f2_pack(qscale, qscale), nm2 = f2_pack(-ref, -ref);
           uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
           for (int c = 0; c < chunks; ++c) {
             const int first = col0 + 64 * c;
@@ -421,7 +439,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_n(&bars->p_ready[j & 1], w.two ? 2 : 1);
+        if (lane == 0) {
+          mbar_arrive_n(&bars->p_ready[j & 1], w.two ? 2 : 1);
+          if (F8) mbar_arrive(&bars->keys.empty[g % RK]);
+        }
       }
       if (!ok) break;
       // ---- the piece: O out of TMEM, which the next unit may then use
@@ -463,19 +484,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 // Warps as above, 4..7 even key tiles, 8..11 odd ones.
 template <int D, bool F8>
 struct ScoreCfg {
-  static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
+  static constexpr int THREADS = 32 * kWarpCodes;
   static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int R = (F8 ? 2 : 4) * (128 / D);
-  static constexpr int S = F8 ? 4 * (128 / D) : 1;
-  static constexpr int CODES = F8 ? S * kCodeSlot<D> : 0;
-  static constexpr int SCALES = F8 ? kScaleTiles<false> * 2 * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + R) * TILE + CODES + SCALES + 1024 + 1024;
+  static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;
+  static constexpr int R = (F8 ? 8 : 4) * (128 / D);
+  static constexpr int SCALES = F8 ? R * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(2) * TILE + R * KTILE + SCALES + 1024 + 1024;
 };
 
-template <int R, int S>
+template <int R>
 struct ScoreBars {
   RingBars<R> keys;
-  CodeBars<S> codes;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
   uint32_t tmem;
@@ -507,6 +526,7 @@ struct KeyCursor {
 template <int D, bool F8>
 __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
     pool_prefix_score_kernel(const __grid_constant__ CUtensorMap tq,
+                             const __grid_constant__ CUtensorMap tq2,
                              const __grid_constant__ CUtensorMap tk,
                              const __grid_constant__ AttendParams p) {
   using C = ScoreCfg<D, F8>;
@@ -515,29 +535,22 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
   uint8_t* ring = smem + 2 * C::TILE;
-  uint8_t* codes = ring + R * C::TILE;
-  float* scales = reinterpret_cast<float*>(codes + C::CODES);
-  auto* bars = reinterpret_cast<ScoreBars<R, C::S>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  static_assert(sizeof(ScoreBars<R, C::S>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
+  float* scales = reinterpret_cast<float*>(ring + R * C::KTILE);  // [R][128]
+  auto* bars = reinterpret_cast<ScoreBars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
+  static_assert(sizeof(ScoreBars<R>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
-      mbar_init(&bars->keys.full[i], F8 ? kCodeThreads / 32 : 1);
-      mbar_init(&bars->keys.empty[i], 1);
+      mbar_init(&bars->keys.full[i], 1);
+      mbar_init(&bars->keys.empty[i], F8 ? 1 + 4 : 1);  // the products, and the readers of the scales
     }
-    for (int i = 0; i < C::S; ++i) {
-      mbar_init(&bars->codes.full[i], 1);
-      mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
-    }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->codes.scaled[i], kCodeThreads / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      // E4M3: the issuing thread arrives too, having seen the tile's scales written
-      mbar_init(&bars->s_full[i], F8 ? 2 : 1);
+      mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], 4);
     }
     fence_barrier_init();
@@ -561,13 +574,9 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
 
   if (warp == 0) {
     if constexpr (F8)
-      fetch_codes<D, C::S, false>(v, &tk, nullptr, codes, bars->codes, k);
+      produce_codes<D>(v, &tk, v.kscale, ring, scales, bars->keys, k);
     else
       produce_tma<D>(v, &tk, ring, bars->keys, k);
-  } else if (F8 && warp >= kWarpCodes) {
-    convert_codes<D, R, 1, C::S, false, kCodeThreads>(v, codes, bars->codes, ring, bars->keys,
-                                                      nullptr, nullptr, scales, k,
-                                                      threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
       uint32_t f = 0;
@@ -584,15 +593,16 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           }
           mbar_arrive_expect_tx(&bars->q_full[qb], p.s.per_tile * group * D * 2);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + qb * C::TILE + c * kBoxBytes, &tq, c * 64, 0, k.h, qt * p.s.per_tile,
-                        &bars->q_full[qb]);
+          for (int c = 0; c < (F8 ? 2 : D / 64); ++c)
+            tma_load_4d(sQ + qb * C::TILE + c * (F8 ? C::KTILE : kBoxBytes), c == 1 && F8 ? &tq2 : &tq,
+                        F8 ? 0 : c * 64, 0, k.h, qt * p.s.per_tile, &bars->q_full[qb]);
         }
       }
     }
   } else if (warp == kWarpMMA) {
     if (lane == 0) {
-      const uint64_t dq0 = desc_kmajor<D>(sQ, 0), dk0 = desc_kmajor<D>(ring, 0);
+      const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : desc_kmajor<D>(sQ, 0);
+      const uint64_t dk0 = F8 ? desc_codes<D>(ring) : desc_kmajor<D>(ring, 0);
       uint32_t f0 = 0, cnt[2] = {0, 0};  // f0: fill of the head's (or tile's) row tile 0
       bool ok = true;
       int last = -1;
@@ -613,16 +623,25 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           }
           tc_fence_after();
           const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
-          const uint32_t idesc = idesc_bf16(TILE_KEYS, (rows + 15) / 16 * 16, 0, 0);
-          const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::TILE >> 4));
+          const int cols = (rows + 15) / 16 * 16;
+          const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
+          const uint32_t d_tm = tmem + buf * 128;
+          if constexpr (F8) {
+            const uint32_t idesc = idesc_e4m3(TILE_KEYS, cols);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-            umma_ss(tmem + buf * 128, kb + off, qd + off, idesc, kk > 0);
+            for (int kk = 0; kk < 2 * (D / 32); ++kk)
+              umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
+                           qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2, idesc, kk > 0);
+          } else {
+            const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+              umma_ss(d_tm, kb + off, qd + off, idesc, kk > 0);
+            }
           }
           umma_commit(&bars->s_full[buf]);
-          if (F8) mbar_arrive(&bars->s_full[buf]);
           if (done) umma_commit(&bars->q_empty[qb]);
           if (qt == nq - 1) umma_commit(&bars->keys.empty[st]);
           ++cnt[t];
@@ -637,7 +656,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
     grid_dependency_wait();  // the lse's, by the kernel before
     for (uint32_t g = 0; ok && k.step(); ++g) {
       if ((g & 1) != static_cast<uint32_t>(t)) continue;
-      float acc = 0.f;
+      float acc = 0.f, ks = p.qscale;
       for (int qt = 0; qt < nq; ++qt, ++cnt) {
         const uint32_t buf = 2 * t + (cnt & 1);
         const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
@@ -647,10 +666,23 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        const float ks = F8 ? p.qscale * scales[(g % kScaleTiles<false>) * 2 * TILE_KEYS + r] : p.qscale;
+        if (F8 && qt == 0) {  // the tile has arrived, and stays until the arrival here
+          if (!pool_warp_wait(&bars->keys.full[g % R], (g / R) & 1, v.err)) {
+            ok = false;
+            break;
+          }
+          ks = p.qscale * scales[g % R * TILE_KEYS + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->keys.empty[g % R]);
+        }
         float part[4] = {0.f, 0.f, 0.f, 0.f};
         for (int c = 0; c < rows; c += 32) {
-          const float mine = c + lane < rows ? nl[c + lane] : -INFINITY;
+          const int row = c + lane;
+          const float mine = row < rows ? nl[row] : -INFINITY;
+          float fac = 1.f;
+          if (F8 && row < rows)
+            fac = p.w.qfac[(static_cast<size_t>(qt * p.s.per_tile + row / group) * p.s.heads + k.h) * group +
+                           row % group];
           uint32_t s[32];
           tmem_ld32(tmem + lane_off + buf * 128 + c, s);
           tmem_wait_ld();
@@ -658,7 +690,8 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           for (int x = 0; x < 32; ++x) {
             const float n = __shfl_sync(0xffffffffu, mine, x);
             // rows that are not counted, and columns that are none, may hold anything
-            const float e = ex2(fmaf(__uint_as_float(s[x]), ks, n));
+            const float f = F8 ? ks * __shfl_sync(0xffffffffu, fac, x) : ks;
+            const float e = ex2(fmaf(__uint_as_float(s[x]), f, n));
             part[x & 3] += n == -INFINITY ? 0.f : e;
           }
         }
@@ -683,24 +716,28 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
 // ------------------------------------------------------------------ host side
 template <int D, bool F8>
 cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq;
+  CUtensorMap tq, tq2;
   const CUtensorMap &tk = *p.a.kmap, &tv = *p.a.vmap;
-  cudaError_t e = query_map(&tq, p.a, p.s.per_tile);
+  cudaError_t e = F8 ? query_code_map(&tq, p, 0, p.s.per_tile) : query_map(&tq, p.a, p.s.per_tile);
+  if (e == cudaSuccess && F8) e = query_code_map(&tq2, p, 1, p.s.per_tile);
+  if (!F8) tq2 = tq;
   if (e != cudaSuccess) return e;
   using C = Cfg<D, F8>;
   static int opted_in[kMaxDevices] = {};
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(pool_prefix_kernel<D, F8>), C::SMEM,
                             opted_in)) != cudaSuccess)
     return e;
-  pool_prefix_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p);
+  pool_prefix_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, tq2, tk, tv, p);
   return cudaGetLastError();
 }
 
 template <int D, bool F8>
 cudaError_t score_t(const AttendParams& p, cudaStream_t stream) {
-  CUtensorMap tq;
+  CUtensorMap tq, tq2;
   const CUtensorMap& tk = *p.a.kmap;
-  cudaError_t e = query_map(&tq, p.a, p.s.per_tile);
+  cudaError_t e = F8 ? query_code_map(&tq, p, 0, p.s.per_tile) : query_map(&tq, p.a, p.s.per_tile);
+  if (e == cudaSuccess && F8) e = query_code_map(&tq2, p, 1, p.s.per_tile);
+  if (!F8) tq2 = tq;
   if (e != cudaSuccess) return e;
   using C = ScoreCfg<D, F8>;
   static int opted_in[kMaxDevices] = {};
@@ -708,7 +745,7 @@ cudaError_t score_t(const AttendParams& p, cudaStream_t stream) {
                             opted_in)) != cudaSuccess)
     return e;
   return launch_after(pool_prefix_score_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream,
-                      tq, tk, p);
+                      tq, tq2, tk, p);
 }
 
 }  // namespace

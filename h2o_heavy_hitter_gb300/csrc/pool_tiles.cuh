@@ -41,6 +41,8 @@ struct AttendScratch {
   float* to;       // own pieces' outputs
   float* logits;   // [n][heads][group][cap] base-2 logits of the own tokens (accumulate only)
   float* plogits;  // [heads][n * group][cap] of the prefix (accumulate, few rows only)
+  uint8_t* q8;     // E4M3 pool: the queries as two codes each, [2][n][heads][group][d]
+  float* qfac;     // and what a row's codes are to be multiplied by, [n][heads][group]
 };
 
 struct AttendParams {
@@ -55,8 +57,10 @@ struct AttendParams {
 cudaError_t pool_prefix(const AttendParams& p, cudaStream_t stream);
 cudaError_t pool_prefix_score(const AttendParams& p, cudaStream_t stream);
 // Tensor map of the queries [n][heads][group][d] in boxes of `entries` groups of
-// one head x 64 channels (pool_attend.cu).
+// one head x 64 channels, or of one half of their codes (0, 1) x all channels
+// (pool_attend.cu).
 cudaError_t query_map(CUtensorMap* m, const AttendArgs& a, int entries);
+cudaError_t query_code_map(CUtensorMap* m, const AttendParams& p, int half, int entries);
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------------ bounded waits
@@ -101,19 +105,16 @@ __device__ __forceinline__ int owner(int64_t at, int64_t total, int grid) {
 }
 
 // ------------------------------------------------------------------ tiles into shared memory
-// A ring of R slots, each one tile of keys or of values as bf16, 128-byte
-// swizzled: boxes of 128 tokens x 64 channels. Keys and values have rings of their
-// own, since a tile of values is held until its probabilities are known.
+// A ring of R slots, each one tile of keys or of values. Keys and values have
+// rings of their own, since a tile of values is held until its probabilities are
+// known. bf16 operands: 128-byte swizzle, boxes of 128 tokens x 64 channels. E4M3
+// keys are operands as they are (8-bit products): 128 tokens of D bytes, swizzled
+// by D bytes; the queries are then two codes a value, so that no bit of theirs is
+// lost. E4M3 values become bf16 first, since P has the range of bf16.
 template <int R>
 struct RingBars {
   uint64_t full[R], empty[R];
 };
-
-// Tiles whose scales are kept: more than can be between a slot's refill and the
-// reader of its scales (a value tile is held until its reader is done, a key
-// tile only until its product is).
-template <bool VALUES>
-constexpr int kScaleTiles = VALUES ? 8 : 16;
 
 // A page of a sequence; one outside the pool is reported, and page 0 read in its place.
 __device__ __forceinline__ int checked_page(const PoolView& v, int seq, int j) {
@@ -163,116 +164,58 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
   return r;
 }
 
-// E4M3 pool: one more ring of S slots takes the codes as they are (128 tokens of
-// D bytes, then 128 scales), by TMA from one warp; NT other threads turn each into
-// a slot of bf16. Keys go one tile ahead of values (K0, K1, V0, K2, V1, ...), so
-// that the next tile's keys are converted before the wait for this one's values'
-// slot. (Codes loaded through registers of the converting threads took 10,000
-// clocks a tile of keys and values: every use of one load waited for all of them.)
-template <int S>
-struct CodeBars {
-  uint64_t full[S], empty[S];  // empty: an arrival per converting warp
-  // Both scales of tile g are written: by g & 1, an arrival per converting warp.
-  // (A reader may wait for it before the values of tile g - 1 are converted, but
-  // never before those of g - 2: on the values' own barrier, whose phases may be
-  // single tiles, that wait could take the phase before for its own.)
-  uint64_t scaled[2];
-};
-
-template <int D>
-constexpr int kCodeSlot = TILE_KEYS * D + TILE_KEYS * 4;
-
-// The order of the code ring: calls f(tile, n, g, value) for the n-th slot, tile g.
-// One call in one loop: the body is large, and several warps' bodies share the
-// instruction cache.
-struct CodeTile {
-  int seq, len, h, kt;
-};
-
-template <bool VALUES, typename Cursor, typename F>
-__device__ __forceinline__ void each_code_tile(Cursor keys, F&& f) {
-  Cursor values = keys;
-  uint32_t gk = 0, gv = 0;
-  bool more = keys.step();
-  for (uint32_t n = 0;; ++n) {
-    const bool value = VALUES && (gk - gv == 2 || (!more && gk > gv));
-    if (!value && !more) return;
-    CodeTile c;
-    if (value) {
-      values.step();
-      c = {values.seq, values.len, values.h, values.kt};
-    } else {
-      c = {keys.seq, keys.len, keys.h, keys.kt};
-    }
-    if (!f(c, n, value ? gv : gk, value)) return;
-    if (value) {
-      ++gv;
-    } else {
-      ++gk;
-      more = keys.step();
-    }
-  }
-}
-
-template <int D, int S, bool VALUES, typename Cursor>
-__device__ void fetch_codes(const PoolView& v, const CUtensorMap* tk, const CUtensorMap* tv,
-                            uint8_t* codes, CodeBars<S>& bars, const Cursor& begin) {
+// E4M3 pool, one warp: codes as they are, and their scales behind them in `scales`
+// [R][128]. What lies behind the last token holds anything.
+template <int D, int R, typename Cursor>
+__device__ void produce_codes(const PoolView& v, const CUtensorMap* map, const float* scale,
+                              uint8_t* ring, float* scales, RingBars<R>& bars, Cursor c) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  each_code_tile<VALUES>(begin, [&](const CodeTile& c, uint32_t n, uint32_t, bool value) -> bool {
+  for (uint32_t n = 0; c.step(); ++n) {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
-    const uint32_t st = n % S;
-    if (n >= S && !pool_warp_wait(&bars.empty[st], ((n / S) - 1) & 1, v.err)) return false;
+    const uint32_t st = n % R;
+    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
     if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
     __syncwarp();
     if (lane < boxes) {
-      uint8_t* dst = codes + st * kCodeSlot<D>;
-      tma_load_2d(dst + (lane << v.shift) * D, value ? tv : tk, 0, row, &bars.full[st]);
-      bulk_copy_g2s(dst + TILE_KEYS * D + (lane << v.shift) * 4, (value ? v.vscale : v.kscale) + row,
-                    v.page * 4, &bars.full[st]);
+      tma_load_2d(ring + st * (TILE_KEYS * D) + (lane << v.shift) * D, map, 0, row, &bars.full[st]);
+      bulk_copy_g2s(scales + st * TILE_KEYS + (lane << v.shift), scale + row, v.page * 4, &bars.full[st]);
     }
-    return true;
-  });
+  }
 }
 
-// Rows behind the last token become zero. The scales of tile g go to
-// scales[g % kScaleTiles<VALUES>][0: keys, 1: values][128]. Each warp arrives once
-// on the slot's barrier.
-template <int D, int RK, int RV, int S, bool VALUES, int NT, typename Cursor>
-__device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<S>& from,
-                              uint8_t* kring, RingBars<RK>& kbars, uint8_t* vring,
-                              RingBars<RV>* vbars, float* scales, const Cursor& begin, int tid) {
-  constexpr int BYTES = TILE_KEYS * D * 2;
+// E4M3 pool, NT threads: tiles of value codes (linear, S slots) to bf16 operands,
+// and their scales to out_scales [kScaleTiles][128] by tile; rows behind the last
+// token become zero. Each warp arrives once on a slot's barriers. (Codes loaded
+// through registers of the converting threads took 10,000 clocks a tile of keys
+// and values: every use of one load waited for all of them.)
+constexpr int kScaleTiles = 8;  // more tiles than lie between a conversion and its reader
+
+template <int D, int R, int S, int NT, typename Cursor>
+__device__ void convert_values(const PoolView& v, const uint8_t* codes, const float* scales,
+                               RingBars<S>& from, uint8_t* ring, RingBars<R>& to,
+                               float* out_scales, Cursor c, int tid) {
   constexpr int CPR = D / 16;               // 16-byte chunks of codes per token
   constexpr int NCH = TILE_KEYS * CPR / NT;  // chunks per thread and slot
   const int lane = threadIdx.x & 31;
-  each_code_tile<VALUES>(begin, [&](const CodeTile& c, uint32_t n, uint32_t g, bool value) -> bool {
+  for (uint32_t n = 0; c.step(); ++n) {
     const int valid = c.len - c.kt * TILE_KEYS;
-    const uint32_t sc = n % S;
-    if (!pool_warp_wait(&from.full[sc], (n / S) & 1, v.err)) return false;
-    const uint8_t* src = codes + sc * kCodeSlot<D>;
+    const uint32_t sc = n % S, st = n % R;
+    if (!pool_warp_wait(&from.full[sc], (n / S) & 1, v.err)) return;
+    const uint4* src = reinterpret_cast<const uint4*>(codes + sc * (TILE_KEYS * D));
     uint4 x[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      x[i] = reinterpret_cast<const uint4*>(src)[tid + NT * i];
+      x[i] = src[tid + NT * i];
       if ((tid + NT * i) / CPR >= valid) x[i] = make_uint4(0, 0, 0, 0);
     }
     float scale = 0.f;
-    if (tid < TILE_KEYS && tid < valid) scale = reinterpret_cast<const float*>(src + TILE_KEYS * D)[tid];
-    uint64_t* full;
-    uint8_t* dst;
-    if (VALUES && value) {
-      if (g >= RV && !pool_warp_wait(&vbars->empty[g % RV], ((g / RV) - 1) & 1, v.err)) return false;
-      full = &vbars->full[g % RV];
-      dst = vring + g % RV * BYTES;
-    } else {
-      if (g >= RK && !pool_warp_wait(&kbars.empty[g % RK], ((g / RK) - 1) & 1, v.err)) return false;
-      full = &kbars.full[g % RK];
-      dst = kring + g % RK * BYTES;
-    }
-    if (tid < TILE_KEYS) scales[((g % kScaleTiles<VALUES>) * 2 + value) * TILE_KEYS + tid] = scale;
+    if (tid < TILE_KEYS && tid < valid) scale = scales[sc * TILE_KEYS + tid];
+    if (n >= R && !pool_warp_wait(&to.empty[st], ((n / R) - 1) & 1, v.err)) return;
+    if (tid < TILE_KEYS) out_scales[(n % kScaleTiles) * TILE_KEYS + tid] = scale;
+    uint8_t* dst = ring + st * (TILE_KEYS * D * 2);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int q = tid + NT * i, row = q / CPR, col = q % CPR;
@@ -290,12 +233,16 @@ __device__ void convert_codes(const PoolView& v, const uint8_t* codes, CodeBars<
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(full);
+      mbar_arrive(&to.full[st]);
       mbar_arrive(&from.empty[sc]);
-      if (VALUES && value) mbar_arrive(&from.scaled[g & 1]);
     }
-    return true;
-  });
+  }
+}
+
+// K-major E4M3 operand with rows of D bytes: k-step kk is 32 bytes further.
+template <int D>
+__device__ __forceinline__ uint64_t desc_codes(const uint8_t* tile) {
+  return D == 128 ? smem_desc(tile, 16, 1024) : smem_desc_64(tile, 16, 512);
 }
 #endif  // __CUDACC__
 

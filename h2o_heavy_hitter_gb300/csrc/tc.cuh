@@ -82,6 +82,17 @@ __device__ __forceinline__ uint64_t smem_desc(const void* p, uint32_t lbo_bytes,
   return d;
 }
 
+// The same with 64-byte swizzle (mode 4): atoms of 8 rows x 64 bytes.
+__device__ __forceinline__ uint64_t smem_desc_64(const void* p, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return smem_desc(p, lbo_bytes, sbo_bytes) + (static_cast<uint64_t>(2) << 61);
+}
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 A/B (format code 0), both
+// K-major, and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // Instruction descriptor of kind::f16 with bf16 A/B and fp32 accumulation.
 // a_mn / b_mn select MN-major (transposed) operands.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
@@ -100,6 +111,16 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a, uint64_t b,
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem], 8-bit operands (32 bytes of K per instruction)
+__device__ __forceinline__ void umma_ss_8bit(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
