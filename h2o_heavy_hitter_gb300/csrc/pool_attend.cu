@@ -48,26 +48,32 @@ struct List {
 // Fills the list: skipped and refused entries have seq -1 and no tiles. An entry
 // is refused for an index outside the pool, the prefix's, or one named before;
 // repeats are looked for one by one only where a hashed bit says that there may
-// be some. Blockwide; `bits`: 4 KB; `report`: this block sets the error word.
+// be some. Every CTA begins with this, so it takes few barriers. Blockwide;
+// `bits`: 4 KB; `report`: this block sets the error word.
 __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int* wsum,
                            bool report) {
   const PoolView& v = a.v;
-  const int tid = threadIdx.x, nt = blockDim.x, n = a.n;
-  for (int i = tid; i < 1024; i += nt) bits[i] = 0;
-  __syncthreads();
-  bool seen = false;
-  for (int b = tid; b < n; b += nt) {
+  const int tid = threadIdx.x, nt = blockDim.x, n = a.n, lane = tid & 31, warp = tid >> 5;
+  // each thread takes `per` entries in a row
+  const int per = (n + nt - 1) / nt, b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  for (int b = b0; b < b1; ++b) {
     int s = a.seqs[b];
     if (s != -1 && (s < 0 || s >= v.seqs || s == a.prefix)) {
       if (report) atomicOr(v.err, kErrBadList);
       s = -1;
     }
-    list.seq[b] = s;
     list.len[b] = s >= 0 ? checked_length(v, s, report) : -1;
+    list.seq[b] = s;
+  }
+  for (int i = tid; i < 1024; i += nt) bits[i] = 0;
+  __syncthreads();
+  bool seen = false;
+  for (int b = b0; b < b1; ++b) {
+    const int s = list.seq[b];
     if (s >= 0) seen |= (atomicOr(&bits[(s >> 5) & 1023], 1u << (s & 31)) >> (s & 31)) & 1u;
   }
   if (__syncthreads_or(seen)) {
-    for (int b = tid; b < n; b += nt) {
+    for (int b = b0; b < b1; ++b) {
       const int s = a.seqs[b];
       if (s < 0) continue;
       for (int j = 0; j < b; ++j)
@@ -78,21 +84,26 @@ __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int*
         }
     }
   }
-  __syncthreads();
-  const int per = (n + nt - 1) / nt, b0 = min(n, tid * per), b1 = min(n, b0 + per);
   int mine = 0;
   for (int b = b0; b < b1; ++b) {
     if (list.len[b] < 0) list.seq[b] = -1;
     mine += key_tiles(max(0, list.len[b]));
   }
-  int total;
-  int at = block_exclusive_scan(mine, wsum, &total);
+  int at = mine;  // inclusive over the warp, then over the block
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, at, off);
+    if (lane >= off) at += y;
+  }
+  if (lane == 31) wsum[warp] = at;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) at += wsum[w];
+  at -= mine;
   for (int b = b0; b < b1; ++b) {
     list.cum[b] = at;
     at += key_tiles(max(0, list.len[b]));
   }
-  if (tid == 0) list.cum[n] = total;
-  __syncthreads();
+  if (tid == nt - 1) list.cum[n] = at;
 }
 
 // A walk along one CTA's share of the units: first the prefix's (few rows only),
@@ -389,13 +400,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   }
   build_list(p.a, list, reinterpret_cast<uint32_t*>(sP), bars->wsum, cta == 0);
   const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, cta + threadIdx.x == 0)) : 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (cta == 0) {
     for (int i = threadIdx.x; i < p.s.n; i += C::THREADS) p.w.seq[i] = list.seq[i];
     for (int i = threadIdx.x; i <= p.s.n; i += C::THREADS) p.w.cum[i] = list.cum[i];
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = bars->tmem;
   Walk w(p, list, plen, cta);
 
