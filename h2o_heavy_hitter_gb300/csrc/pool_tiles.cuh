@@ -101,7 +101,11 @@ __device__ __forceinline__ int64_t share_begin(int64_t total, int grid, int cta)
 
 // CTA whose share holds tile `at`.
 __device__ __forceinline__ int owner(int64_t at, int64_t total, int grid) {
-  return static_cast<int>(((at + 1) * sharers(total, grid) - 1) / total);
+  const int64_t c = sharers(total, grid), x = (at + 1) * c - 1;
+  // (a division of 64 bits takes five times as long, and every row needs four)
+  if ((total * c) >> 32 == 0)
+    return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(total));
+  return static_cast<int>(x / total);
 }
 
 // ------------------------------------------------------------------ tiles into shared memory
