@@ -250,7 +250,7 @@ __device__ __forceinline__ void copy_slots(const PoolView& v, int to, int from, 
 // LANES threads per (entry, head, slab of kSlab slots): the slab's scores, and the
 // tokens of its pages that were not shared. A head's slots of a page are
 // contiguous, so a partial page is one run of bytes per head.
-constexpr int kSlab = 256;
+constexpr int kSlab = 1024;
 
 template <int LANES>
 __global__ void __launch_bounds__(256)
@@ -440,8 +440,12 @@ __device__ __forceinline__ unsigned score_key(float x) {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectKeys = 48 * 1024;  // scores whose keys are held in shared memory
+constexpr int kSelectKeys = 44 * 1024;  // scores whose keys are held in shared memory
 constexpr int kDigit = 11;              // bits of a radix step: 3 steps
+// Copies of the histogram, by lane: scores crowd in few exponents, and a warp's
+// additions to one word run one after the other (78 us for 128 rows of 32768 with
+// steps of 8 bits from global memory, 33 us with all this).
+constexpr int kHists = 4;
 
 // Blocks (head, entry, layer) select; the block with head == heads of entry 0
 // plans its layer: plan of an entry = {first fresh page or -1, -, -, -}. The
@@ -451,7 +455,7 @@ constexpr int kDigit = 11;              // bits of a radix step: 3 steps
 // MSB-first radix select over keys held in shared memory (a row of up to kSelectKeys
 // scores is read from HBM once); then a warp counts, and in a second pass places,
 // the kept ones of its contiguous part by votes.
-__global__ void __launch_bounds__(kSelectThreads)
+__global__ void __launch_bounds__(kSelectThreads, 2)
     compact_select_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs, int h, int r,
                           int32_t* fresh_all, int fresh_stride, int32_t* plan_all,
                           int32_t* __restrict__ where, float* __restrict__ kept, int held) {
@@ -473,7 +477,8 @@ __global__ void __launch_bounds__(kSelectThreads)
     if (tid < n) plan[tid * kPlanInts] = seq >= 0 ? first : -1;
     return;
   }
-  __shared__ unsigned hist[1 << kDigit];
+  __shared__ uint4 hist4[1 << kDigit];  // kHists counts a bin
+  unsigned* hist = reinterpret_cast<unsigned*>(hist4);
   __shared__ unsigned s_prefix;
   __shared__ int s_rank;
   const int head = blockIdx.x, e = blockIdx.y, seq = seqs[e];
@@ -484,13 +489,22 @@ __global__ void __launch_bounds__(kSelectThreads)
   const int n_cand = T - r;
   const bool local = n_cand <= held;
   if (local && h > 0) {
-    int p = 4 * tid;
-    for (; p + 3 < n_cand; p += 4 * kSelectThreads) {
-      const float4 x = *reinterpret_cast<const float4*>(cs + p);
-      *reinterpret_cast<uint4*>(keys + p) =
-          make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
+    // four loads in flight per thread: the compiler keeps loads behind shared stores
+    for (int p0 = 0; p0 < n_cand; p0 += 16 * kSelectThreads) {
+      float4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = p0 + 4 * (tid + kSelectThreads * i);  // rows are whole pages: 16-byte loads stay inside
+        x[i] = p < n_cand ? *reinterpret_cast<const float4*>(cs + p) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = p0 + 4 * (tid + kSelectThreads * i);
+        if (p < n_cand)
+          *reinterpret_cast<uint4*>(keys + p) =
+              make_uint4(score_key(x[i].x), score_key(x[i].y), score_key(x[i].z), score_key(x[i].w));
+      }
     }
-    for (; p < n_cand; ++p) keys[p] = score_key(cs[p]);
   }
   auto key = [&](int p) { return local ? keys[p] : score_key(cs[p]); };
   // Keep candidate p iff its key is above tau, or equals tau and p is not
@@ -503,15 +517,18 @@ __global__ void __launch_bounds__(kSelectThreads)
     for (int shift = 32 - kDigit; mask != 0xffffffffu; shift -= kDigit) {
       const int s = max(shift, 0), bits = shift < 0 ? kDigit + shift : kDigit;
       const unsigned low = (1u << bits) - 1;
-      for (int i = tid; i < 1 << kDigit; i += kSelectThreads) hist[i] = 0;
+      for (int i = tid; i < 1 << kDigit; i += kSelectThreads) hist4[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
+      // (one addition for all lanes of a bin, found by a match, took 10 us longer)
+#pragma unroll 4
       for (int p = tid; p < n_cand; p += kSelectThreads) {
         const unsigned u = key(p);
-        if ((u & mask) == prefix) atomicAdd(&hist[(u >> s) & low], 1u);
+        if ((u & mask) == prefix) atomicAdd(&hist[((u >> s) & low) * kHists + (lane & (kHists - 1))], 1u);
       }
       __syncthreads();
       // the bin of the rank-th key: two bins a thread, one block scan
-      const int a = static_cast<int>(hist[2 * tid]), b = static_cast<int>(hist[2 * tid + 1]);
+      const uint4 x = hist4[2 * tid], y = hist4[2 * tid + 1];
+      const int a = static_cast<int>(x.x + x.y + x.z + x.w), b = static_cast<int>(y.x + y.y + y.z + y.w);
       int total;
       const int before = block_exclusive_scan(a + b, wsum, &total);
       if (before <= rank && rank < before + a + b) {
@@ -531,6 +548,7 @@ __global__ void __launch_bounds__(kSelectThreads)
   const int groups = (T + 31) / 32, per = (groups + kSelectWarps - 1) / kSelectWarps;
   const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
   int above = 0, equal = 0;  // above: kept whatever the ties are
+#pragma unroll 4
   for (int g = g0; g < g1; ++g) {
     const int p = 32 * g + lane;
     const bool cand = p < n_cand && h > 0;
@@ -545,21 +563,37 @@ __global__ void __launch_bounds__(kSelectThreads)
   const size_t out = ((static_cast<size_t>(blockIdx.z) * n + e) * v.heads + head) * k;
   const unsigned below = (1u << lane) - 1;
   int eq = eq0;
-  for (int g = g0; g < g1; ++g) {
-    const int p = 32 * g + lane;
-    const bool cand = p < n_cand && h > 0;
-    const unsigned u = cand ? key(p) : 0u;
-    const unsigned same = __ballot_sync(0xffffffffu, cand && u == tau);
-    const bool keep = cand ? u > tau || (u == tau && eq + __popc(same & below) >= skip)
-                           : p >= n_cand && p < T;
-    const unsigned all = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      const int s = at + __popc(all & below), page = held_page(v, seq, p >> v.shift);
-      where[out + s] = page < 0 ? -1 : (page << v.shift) + (p & (v.page - 1));
-      kept[out + s] = cs[p];
+  for (int g = g0; g < g1; g += 4) {  // four groups at a time, their loads in flight together
+    int slot[4], page[4];
+    float value[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 32 * (g + i) + lane;
+      const bool in = g + i < g1, cand = in && p < n_cand && h > 0;
+      const unsigned u = cand ? key(p) : 0u;
+      const unsigned same = __ballot_sync(0xffffffffu, cand && u == tau);
+      const bool keep = cand ? u > tau || (u == tau && eq + __popc(same & below) >= skip)
+                             : in && p >= n_cand && p < T;
+      const unsigned all = __ballot_sync(0xffffffffu, keep);
+      slot[i] = keep ? at + __popc(all & below) : -1;
+      at += __popc(all);
+      eq += __popc(same);
     }
-    at += __popc(all);
-    eq += __popc(same);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 32 * (g + i) + lane;
+      page[i] = slot[i] < 0 ? 0 : v.table[static_cast<size_t>(seq) * v.width + (p >> v.shift)];
+      value[i] = slot[i] < 0 ? 0.f : cs[p];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = 32 * (g + i) + lane;
+      if (slot[i] < 0) continue;
+      const bool held_one = page[i] >= 0 && page[i] < v.pages;
+      if (!held_one) atomicOr(v.err, kErrBadState);
+      where[out + slot[i]] = held_one ? (page[i] << v.shift) + (p & (v.page - 1)) : -1;
+      kept[out + slot[i]] = value[i];
+    }
   }
 }
 
@@ -641,10 +675,11 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
                                                         share ? n : n * v.width, plan);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a warp per task where the tasks fill the GPU, else a block (32 heads x 4
-  // entries, 50 tokens each: 19.4 us by warps, see the design notes for blocks)
+  // a warp per task where the tasks fill the GPU, else a block: 32 heads x 4
+  // entries of some 50 tokens take 7.6 us by blocks, 19.4 us by warps; scores of
+  // 128 heads x 32768 tokens (4096 tasks) 33 us by blocks of 256 slots, 18 us by warps
   const int tasks = n * v.heads, slabs = (v.cap + kSlab - 1) / kSlab;
-  const bool many = static_cast<long>(tasks) * layers >= 8192;
+  const bool many = static_cast<long>(tasks) * slabs * layers >= 4096;
   const int per_block = many ? 8 : 1;
   const dim3 grid((tasks + per_block - 1) / per_block, slabs, layers);
   return launch_after(many ? fork_copy_kernel<32> : fork_copy_kernel<256>, grid, 256, 0, stream, v, n,
