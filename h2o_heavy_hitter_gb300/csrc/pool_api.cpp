@@ -70,16 +70,22 @@ int check_list(const h2o_pool* p, int layer, bool all, int n, const void* list) 
 
 bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
 
-// Runs f(), turning exceptions (the allocator's) into H2O_ENOMEM.
+// Runs f(), the part of a call that allocates or asks PyTorch for its stream:
+// no exception leaves a C entry point.
 template <typename F>
-int with_scratch(F&& f) {
+int guarded(F&& f) {
   try {
     return f();
   } catch (const std::exception& ex) {
-    return fail(H2O_ENOMEM, std::string("scratch allocation failed: ") + ex.what());
+    return fail(H2O_ENOMEM, std::string("allocation failed: ") + ex.what());
   } catch (...) {
-    return fail(H2O_ENOMEM, "scratch allocation failed");
+    return fail(H2O_ENOMEM, "allocation failed");
   }
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
 }
 
 int launch_status(cudaError_t e, const char* what) {
@@ -91,7 +97,7 @@ int fork_or_copy(h2o_pool* p, int layer, int n, const int32_t* src, const int32_
   if (int rc = check_list(p, layer, true, n, src)) return rc;
   if (n > 0 && !dst) return fail(H2O_EINVAL, "null sequence list");
   if (n == 0) return H2O_OK;
-  return with_scratch([&] {
+  return guarded([&] {
     const h2o::PoolView v = layer_view(p, layer < 0 ? 0 : layer);
     const size_t L = layer < 0 ? p->layers : 1, N = n;
     const size_t fresh = L * N * (share ? 1 : v.width), plan = L * N * h2o::kPlanInts;
@@ -124,6 +130,11 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
     return fail(H2O_EINVAL, "pages * heads * page_size must be below 2^31 (slots of a layer)");
   if (static_cast<int64_t>(max_pages) * page_size > H2O_MAX_T)
     return fail(H2O_EINVAL, "max_pages * page_size exceeds H2O_MAX_T");
+  // what the sizes below are made of; 2^56 bytes are more than any device has
+  const double want = static_cast<double>(layers) *
+                      (static_cast<double>(pages) * heads * page_size * (4 * head_dim + 12) +
+                       static_cast<double>(sequences) * max_pages * (4.0 * heads * page_size + 4));
+  if (want > 7e16) return fail(H2O_ENOMEM, "pool too large");
   auto* p = new (std::nothrow) h2o_pool();
   if (!p) return fail(H2O_ENOMEM, "out of host memory");
   try {
@@ -153,8 +164,9 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
   const size_t meta = align_up(L * sequences * 8, 256);
   const size_t ref = align_up(L * pages * 4, 256);
   const size_t total = 2 * kv + per_slot + 2 * scale + score + table + meta + ref + 256;
-  cudaStream_t s = current_stream();
+  cudaStream_t s = nullptr;
   try {
+    s = current_stream();
     p->base = device_alloc(total, s);
   } catch (const std::exception& ex) {
     delete p;
@@ -237,7 +249,7 @@ int h2o_pool_write(h2o_pool* p, int layer, int n, const int32_t* seqs, const voi
   if (n == 0 || T == 0) return H2O_OK;
   if (!K || !V) return fail(H2O_EINVAL, "null K or V");
   if (!aligned16(K) || !aligned16(V)) return fail(H2O_EINVAL, "K and V must be 16-byte aligned");
-  return with_scratch([&] {
+  return guarded([&] {
     const h2o::PoolView v = layer_view(p, layer);
     const size_t fresh = static_cast<size_t>(n) * ((T + v.page - 1) / v.page);
     const size_t plan = static_cast<size_t>(n) * h2o::kPlanInts;
@@ -259,9 +271,11 @@ int h2o_pool_copy(h2o_pool* p, int layer, int n, const int32_t* src, const int32
 
 int h2o_pool_free(h2o_pool* p, int layer, int n, const int32_t* seqs) {
   if (int rc = check_list(p, layer, true, n, seqs)) return rc;
-  return launch_status(h2o::pool_free(layer_view(p, layer < 0 ? 0 : layer),
-                                      layer < 0 ? p->layers : 1, n, seqs, current_stream()),
-                       "pool free launch");
+  return guarded([&] {
+    return launch_status(h2o::pool_free(layer_view(p, layer < 0 ? 0 : layer),
+                                        layer < 0 ? p->layers : 1, n, seqs, current_stream()),
+                         "pool free launch");
+  });
 }
 
 int h2o_pool_compact(h2o_pool* p, int layer, int n, const int32_t* seqs, int h, int r) {
@@ -269,7 +283,7 @@ int h2o_pool_compact(h2o_pool* p, int layer, int n, const int32_t* seqs, int h, 
   if (h < 0 || r < 0 || h > H2O_MAX_K || r > H2O_MAX_K || h + r < 1 || h + r > H2O_MAX_K)
     return fail(H2O_EINVAL, "need h >= 0, r >= 0 and 1 <= h + r <= H2O_MAX_K");
   if (n == 0 || h + r >= p->v.cap) return H2O_OK;  // no sequence is longer than the budget
-  return with_scratch([&] {
+  return guarded([&] {
     const h2o::PoolView v = layer_view(p, layer < 0 ? 0 : layer);
     const size_t L = layer < 0 ? p->layers : 1, N = n, k = h + r;
     const size_t fresh = L * N * ((k + v.page - 1) / v.page), plan = L * N * h2o::kPlanInts;
@@ -294,7 +308,12 @@ int h2o_pool_attend(h2o_pool* p, int layer, int n, const int32_t* seqs, int pref
   if (n == 0) return H2O_OK;
   if (!q || !out) return fail(H2O_EINVAL, "null q or out");
   if (!aligned16(q) || !aligned16(out)) return fail(H2O_EINVAL, "q and out must be 16-byte aligned");
-  return with_scratch([&] {
+  const size_t bytes = static_cast<size_t>(n) * q_heads * p->v.d * 2;
+  const size_t lse_bytes = lse ? static_cast<size_t>(n) * q_heads * sizeof(float) : 0;
+  if (overlap(q, bytes, out, bytes) || overlap(lse, lse_bytes, q, bytes) ||
+      overlap(lse, lse_bytes, out, bytes))
+    return fail(H2O_EINVAL, "q, out and lse must not overlap");
+  return guarded([&] {
     h2o::AttendArgs a{};
     a.v = layer_view(p, layer);
     a.seqs = seqs;
@@ -315,7 +334,7 @@ int h2o_pool_attend(h2o_pool* p, int layer, int n, const int32_t* seqs, int pref
 
 int h2o_pool_sync_check(h2o_pool* p) {
   if (int rc = check_pool(p)) return rc;
-  return check_error_word(p->v.err, current_stream());
+  return guarded([&] { return check_error_word(p->v.err, current_stream()); });
 }
 
 }  // extern "C"

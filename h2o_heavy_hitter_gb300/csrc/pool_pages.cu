@@ -412,8 +412,18 @@ __global__ void __launch_bounds__(256)
       float f[EPL];
 #pragma unroll
       for (int j = 0; j < NV; ++j) bf16x8_to_f32(raw[kv][j], f + 8 * j);
+      // a NaN or an infinity has no code: the vector becomes NaN by its scale
+      bool wild = false;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) wild |= !(fabsf(f[j]) < INFINITY);
+      wild = __ballot_sync(gmask, wild) & gmask;
+      if (wild) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) f[j] = 0.f;
+      }
       uint32_t pairs[EPL / 2];
-      const float sc = quantize_e4m3<EPL>(f, gmask, LPT, pairs, kTinyVector);
+      float sc = quantize_e4m3<EPL>(f, gmask, LPT, pairs, kTinyVector);
+      if (wild) sc = __int_as_float(0x7fc00000);
       if constexpr (EPL == 16)
         *reinterpret_cast<uint4*>(dst + l * EPL) =
             make_uint4(pairs[0] | (pairs[1] << 16), pairs[2] | (pairs[3] << 16),

@@ -524,7 +524,7 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  * -infinity. Rows of skipped entries keep what they held.
  *
  * q: device bf16 [n][q_heads][d]; out: device bf16 [n][q_heads][d]; lse: device
- * fp32 [n][q_heads]; q and out 16-byte aligned. q_heads is a multiple of H, at
+ * fp32 [n][q_heads]; q and out 16-byte aligned; the three must not overlap. q_heads is a multiple of H, at
  * most H2O_POOL_MAX_GROUP times. `prefix` in `seqs` is a bad entry.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */

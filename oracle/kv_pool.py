@@ -22,12 +22,16 @@ BAD_STATE, BAD_LENGTH, NO_PAGE, BAD_LIST = 2, 4, 8, 16
 
 
 def quantise(x):
-    """kv_fp8.quantize_vector of every vector [..., d], those of magnitude up to 2^-119 as zero."""
+    """kv_fp8.quantize_vector of every vector [..., d], those of magnitude up to 2^-119 as zero;
+    one with a NaN or an infinity has zero codes and a NaN for its scale."""
+    wild = ~np.isfinite(x).all(-1)
+    x = np.where(wild[..., None], 0.0, x)
     amax = np.max(np.abs(x), -1).astype(np.float32)
     zero = amax <= 2.0 ** -119
     inv = np.float32(kv_fp8.E4M3_MAX) / np.where(zero, np.float32(1), amax)
     y = np.where(zero[..., None], np.float32(0), x.astype(np.float32) * inv[..., None])
-    return kv_fp8.e4m3_encode(y), np.where(zero, np.float32(0), amax / np.float32(kv_fp8.E4M3_MAX))
+    scale = np.where(zero, np.float32(0), amax / np.float32(kv_fp8.E4M3_MAX))
+    return kv_fp8.e4m3_encode(y), np.where(wild, np.float32(np.nan), scale)
 
 
 class Pool:

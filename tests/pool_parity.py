@@ -108,9 +108,9 @@ class Both:
         for name in "KV":
             if self.kv == "fp8":
                 assert np.array_equal(v[name].numpy(), o.codes[name]), name
-                assert np.array_equal(v[name.lower() + "scale"].numpy(), o.scale[name]), name
+                assert np.array_equal(v[name.lower() + "scale"].numpy(), o.scale[name], equal_nan=True), name
             else:
-                assert np.array_equal(v[name].double().numpy(), getattr(o, name)), name
+                assert np.array_equal(v[name].double().numpy(), getattr(o, name), equal_nan=True), name
         # a probability's error is that of its logit (up to 2^-14, see attend); the sums add fp32
         # roundings of values up to the score itself
         np.testing.assert_allclose(v["score"].double().numpy(), o.score, rtol=2e-4, atol=1e-6)

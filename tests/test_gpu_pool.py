@@ -203,6 +203,89 @@ def test_attend_ignores_what_lies_behind_a_sequence():
     b.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("what", ["key", "value", "query"])
+def test_a_nan_reaches_the_rows_that_attend_to_it_and_no_others(kv, what):
+    heads, d = 2, 64
+    b = Both(pages=30, page=16, heads=heads, d=d, sequences=3, max_pages=12, kv=kv)
+    K, V = b.tokens(3, 150), b.tokens(3, 150)
+    q = b.queries(2, 4)
+    if what == "query":
+        q[0, 1, 5] = np.nan
+    else:
+        (K if what == "key" else V)[0, 1, 70, 3] = np.nan if kv == "bf16" else np.inf
+    b.write([0, 1, 2], 150, [150, 140, 20], K=K, V=V)
+    b.check()
+    _, qt = bf16(q)
+    out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints([0, 1]), qt, prefix=2)
+    nan = out.isnan().cpu().numpy()  # [2, 4, d]
+    if what == "query":
+        assert nan[0, 1].all() and not nan[0, [0, 2, 3]].any() and not nan[1].any()
+    else:  # key head 1 of sequence 0 serves the query heads 2 and 3
+        assert not nan[1].any() and not nan[0, :2].any()
+        assert nan[0, 2:].all() if what == "key" or kv == "fp8" else nan[0, 2:, 3].all()
+    b.close()
+
+
+def test_every_e4m3_value_is_attended_to_exactly():
+    """A token that alone has weight returns its stored value: all 254 codes, both signs, as
+    values; as keys, a logit of each."""
+    d = 128
+    b = Both(pages=40, page=16, heads=1, d=d, sequences=1, max_pages=40, kv="fp8")
+    b.write([0], 600)
+    from oracle import kv_fp8
+    codes = np.array([c for c in range(256) if c & 0x7f != 0x7f], np.uint8)
+    v = np.resize(codes, (2, d))
+    v[1] = codes[-d:]
+    slot = [(int(b.oracle.table[0, t // 16]), t % 16) for t in (300, 301)]
+    for (p, o), row in zip(slot, v):
+        b.view["V"][p, 0, o] = torch.from_numpy(row).cuda()
+        b.view["vscale"][p, 0, o] = 0.5
+        b.view["K"][p, 0, o] = 0
+        b.view["kscale"][p, 0, o] = 1.0
+    for (p, o), row in zip(slot, v):
+        b.view["K"][p, 0, o, 0] = 0x7e  # 448 * 4 / sqrt(128): above every other logit by 100
+        q = np.zeros((1, 1, d))
+        q[..., 0] = 4.0
+        out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints([0]), bf16(q)[1], accumulate=False)
+        b.view["K"][p, 0, o, 0] = 0
+        want = torch.from_numpy(kv_fp8.e4m3_decode(row) * 0.5).to(torch.bfloat16)
+        assert torch.equal(out[0, 0].cpu(), want)
+    # one code a key, the query a unit vector of each value: s = code / sqrt(d)
+    b.view["K"].zero_()
+    b.view["kscale"].fill_(1.0)
+    for i, c in enumerate(codes):
+        b.view["K"][int(b.oracle.table[0, i // 16]), 0, i % 16, 5] = int(c)
+    b.view["score"].zero_()
+    q = np.zeros((1, 1, d))
+    q[..., 5] = 0.109375  # 7 / 64: two codes hold it
+    out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints([0]), bf16(q)[1])
+    x = np.zeros(600)
+    x[:len(codes)] = kv_fp8.e4m3_decode(codes) * 0.109375 / np.sqrt(d)
+    p = np.exp(x)
+    np.testing.assert_allclose(b.view["score"][0, 0, :600].double().cpu().numpy(), p / p.sum(), rtol=1e-5)
+    b.close()
+
+
+@pytest.mark.parametrize("magnitude", [2.0 ** -130, 2.0 ** -40, 1.0, 2.0 ** 60])
+def test_queries_of_any_magnitude_on_codes(magnitude):
+    """An E4M3 pool splits a query into two codes a value: no magnitude loses bits."""
+    d = 64
+    b = Both(pages=64, page=16, heads=2, d=d, sequences=41, max_pages=40, kv="fp8")
+    b.write([40], 333, K=b.tokens(1, 333) / magnitude if magnitude > 1 else None)
+    for n in (3, 40):  # few and many rows
+        q64, q = bf16(b.queries(n, 2) * magnitude * np.exp2(-np.arange(d) / 4))
+        b.write(range(n), 1, score=False, K=b.tokens(n, 1) / max(1.0, magnitude))
+        out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints(range(n)), q, prefix=40)
+        want, want_lse = b.oracle.attend(range(n), q64, 40)
+        # logits up to 32; a value is off by 2^-17 of the row's largest at most
+        assert np.abs(lse.double().cpu().numpy() - want_lse).max() <= 2e-4
+        assert np.abs(out.double().cpu().numpy() - want).max() <= 2.0 ** -7 * np.abs(b.oracle.V).max()
+        b.check()
+        b.free(range(n))
+    b.close()
+
+
 def test_attend_large_and_equal_logits():
     b = Both(pages=24, page=16, heads=1, d=64, sequences=2, max_pages=20)
     x = np.zeros((1, 1, 300, 64))
@@ -440,6 +523,7 @@ def test_refusals():
                 lambda: h2o.h2o_pool_compact(pool, 0, one, 2 ** 31 - 1, 1),
                 lambda: h2o.h2o_pool_free(pool, -2, one),
                 lambda: h2o.h2o_pool_free(pool, 0, ints([-1] * 1025)),
+                lambda: h2o.h2o_pool_attend(pool, 0, one, q, out=q),
                 lambda: h2o.h2o_pool_create(1, 8, 24, 2, 64, 3, 4),
                 lambda: h2o.h2o_pool_create(1, 1 << 24, 128, 1, 64, 3, 4)):
         with pytest.raises(h2o.H2OError) as e:

@@ -40,6 +40,13 @@ def test_create_checks_its_arguments(lib, args, word):
     assert word in lib.h2o_last_error() and out.value is None
 
 
+def test_a_pool_beyond_any_device_is_refused(lib):
+    """Sizes whose product passes 64 bits must not wrap to a small allocation."""
+    out = P(1)
+    assert lib.h2o_pool_create(65535, 8, 16, 1024, 64, 1 << 20, 65536, 0, ctypes.byref(out)) == -3
+    assert b"too large" in lib.h2o_last_error() and out.value is None
+
+
 def test_null_pools_are_refused(lib):
     fake = 0x10000  # never dereferenced
     for name, types, args in (
