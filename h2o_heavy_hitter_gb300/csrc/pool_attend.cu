@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ joining the pieces
-constexpr int kFinishWarps = 4;
+constexpr int kFinishWarps = 4, kFinishThreads = 32 * kFinishWarps;
 
 // Where the records of a (entry, key head) unit's rows are: `prefix` of the
 // prefix, then `own` of the own tokens. Record i of row g is at base + i * step + g.
@@ -740,16 +740,17 @@ struct Records {
 };
 
 // Warp-wide: the four divisions that place the pieces run in as many lanes.
-__device__ __forceinline__ Records records_of(const AttendParams& p, int b, int h, int plen, int lane) {
+__device__ __forceinline__ Records records_of(const AttendParams& p, int b, int h, int plen,
+                                              const int (&cum)[3], int lane) {
   Records x{};
-  const int pt = p.a.prefix >= 0 ? key_tiles(plen) : 0, tiles = p.w.cum[b + 1] - p.w.cum[b];
-  const int64_t own = static_cast<int64_t>(p.w.cum[p.s.n]) * p.s.heads;
+  const int pt = p.a.prefix >= 0 ? key_tiles(plen) : 0, tiles = cum[1] - cum[0];
+  const int64_t own = static_cast<int64_t>(cum[2]) * p.s.heads;
   const int64_t pre = static_cast<int64_t>(p.s.heads) * (p.s.few ? 1 : p.s.blocks) * pt;
   const int64_t ototal = own + (p.s.few ? pre : 0), ptotal = p.s.few ? ototal : pre;
   const int qt = b / p.s.per_tile, r0 = (b - qt * p.s.per_tile) * p.s.group;
   const int u = p.s.few ? h : h * p.s.blocks + (qt >> 1);
   const int64_t pa = static_cast<int64_t>(u) * pt;
-  const int64_t oa = (p.s.few ? pre : 0) + static_cast<int64_t>(p.w.cum[b]) * p.s.heads + static_cast<int64_t>(h) * tiles;
+  const int64_t oa = (p.s.few ? pre : 0) + static_cast<int64_t>(cum[0]) * p.s.heads + static_cast<int64_t>(h) * tiles;
   // first and last tile of the prefix unit, of the own one
   const int64_t at = lane < 2 ? pa + (lane ? pt - 1 : 0) : oa + (lane == 2 ? 0 : tiles - 1);
   const int64_t total = lane < 2 ? ptotal : ototal;
@@ -778,73 +779,133 @@ __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int 
   return x;
 }
 
+// Index of record i of row g in its array (the prefix's for i < x.prefix), and its {max, sum}.
+__device__ __forceinline__ size_t record(const AttendParams& p, const Records& x, int i, int g) {
+  return (i < x.prefix ? x.pbase + i * x.pstep
+                       : x.obase + static_cast<size_t>(i - x.prefix) * p.s.group) + g;
+}
+__device__ __forceinline__ float2 record_ml(const AttendParams& p, const Records& x, int i, int g) {
+  return (i < x.prefix ? p.w.pml : p.w.tml)[record(p, x, i, g)];
+}
+
+// A warp's lse (base 2) of row g, the same bits wherever it is computed; `first`:
+// the maximum of record `lane`.
+__device__ __forceinline__ float row_lse(const AttendParams& p, const Records& x, int g, int lane,
+                                         float& first) {
+  const int all = x.prefix + x.own;
+  float m = -INFINITY, l = 0.f;
+  first = -INFINITY;
+  for (int i = lane; i < all; i += 32) {
+    const float2 y = record_ml(p, x, i, g);
+    if (i < 32) first = y.x;
+    const float top = fmaxf(m, y.x);
+    if (top != -INFINITY) {
+      l = l * ex2(m - top) + y.y * ex2(y.x - top);
+      m = top;
+    } else {
+      l += y.y;  // a NaN sum stays one
+    }
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
+    const float top = fmaxf(m, mo);
+    if (top != -INFINITY)
+      l = l * ex2(m - top) + lo * ex2(mo - top);
+    else
+      l += lo;
+    m = top;
+  }
+  return __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
+}
+
+// Scores of a prefix with few rows, from their logits, rows in order: a block per
+// head and 4 kFinishThreads keys. It computes the lse's of all rows itself, which
+// takes less than another launch would.
+__device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
+  const PoolView& v = p.a.v;
+  const int per_head = (v.cap + 4 * kFinishThreads - 1) / (4 * kFinishThreads);
+  const int h = block / per_head, j = ((block - h * per_head) * kFinishThreads + threadIdx.x) * 4;
+  const int plen = max(0, checked_length(v, p.a.prefix, false));
+  if ((block - h * per_head) * kFinishThreads * 4 >= plen) return;
+  const int rows = p.s.n * p.s.group, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < rows; i += kFinishWarps) {
+    const int b = i / p.s.group;
+    const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
+    float first;
+    // +inf: not counted, whatever its logits are
+    const float x = p.w.seq[b] < 0
+                        ? INFINITY
+                        : row_lse(p, records_of(p, b, h, plen, cum, lane), i - b * p.s.group, lane, first);
+    if (lane == 0) s_lse[i] = x;
+  }
+  __syncthreads();
+  if (j >= plen) return;
+  const float* L = p.w.plogits + static_cast<size_t>(h) * rows * v.cap + j;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < rows; ++i) {
+    const float n = s_lse[i];
+    const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(i) * v.cap);
+    if (n == INFINITY) continue;
+    a[0] += ex2(y.x - n);
+    a[1] += ex2(y.y - n);
+    a[2] += ex2(y.z - n);
+    a[3] += ex2(y.w - n);
+  }
+  float* score = v.score + (static_cast<size_t>(p.a.prefix) * v.heads + h) * v.cap + j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i < plen) score[i] += a[i];
+}
+
 // Per (entry, key head) and chunk of keys, one to four warps by the size of the
 // group: join the rows, a warp each, in the order of the pieces, and add the
 // probabilities of the own tokens to their scores. Every chunk computes the lse's
-// it needs, chunk 0 writes.
+// it needs, chunk 0 writes. `blocks` * `chunks` such blocks, then those of the prefix's scores.
 template <int D>
-__global__ void __launch_bounds__(32 * kFinishWarps)
-    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps) {
+__global__ void __launch_bounds__(kFinishThreads)
+    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps, int blocks, int chunks) {
   grid_dependency_wait();
   grid_launch_dependents();
   __shared__ float s_lse[kFinishWarps][kFewRows];
+  if (static_cast<int>(blockIdx.x) >= blocks * chunks) {
+    prefix_scores(p, blockIdx.x - blocks * chunks, s_lse[0]);
+    return;
+  }
   const PoolView& v = p.a.v;
   const int group = p.s.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = blockIdx.x / blocks, block = blockIdx.x - chunk * blocks;
   const int local = warp / unit_warps, sub = warp - local * unit_warps;
-  const int unit = blockIdx.x * (kFinishWarps / unit_warps) + local;
+  const int unit = block * (kFinishWarps / unit_warps) + local;
   const bool in = unit < p.s.n * p.s.heads;
   const int b = in ? unit / p.s.heads : 0, h = in ? unit - b * p.s.heads : 0;
+  const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
   const int seq = in ? p.w.seq[b] : -1;
-  float* nlse = nullptr;  // for the scores of the prefix
-  if (in && p.w.nlse && blockIdx.y == 0)
+  const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
+  float* nlse = nullptr;  // for the scores of a prefix with many rows
+  if (in && p.w.nlse && chunk == 0)
     nlse = p.w.nlse + (static_cast<size_t>(h) * p.s.nq + b / p.s.per_tile) * TILE_ROWS +
            b % p.s.per_tile * group;
   int len = 0;
   if (seq >= 0) {
-    const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
     len = v.meta[2 * seq];
-    const Records x = records_of(p, b, h, plen, lane);
+    const Records x = records_of(p, b, h, plen, cum, lane);
     const int all = x.prefix + x.own;
     for (int g = sub; g < group; g += unit_warps) {
-      auto record = [&](int i) -> size_t {
-        return (i < x.prefix ? x.pbase + i * x.pstep : x.obase + static_cast<size_t>(i - x.prefix) * group) + g;
-      };
-      auto ml = [&](int i) -> float2 { return (i < x.prefix ? p.w.pml : p.w.tml)[record(i)]; };
-      float m = -INFINITY, l = 0.f;
-      float2 first = make_float2(-INFINITY, 0.f);  // of record `lane`
-      for (int i = lane; i < all; i += 32) {
-        const float2 y = ml(i);
-        if (i < 32) first = y;
-        const float top = fmaxf(m, y.x);
-        if (top != -INFINITY) {
-          l = l * ex2(m - top) + y.y * ex2(y.x - top);
-          m = top;
-        } else {
-          l += y.y;  // a NaN sum stays one
-        }
-      }
-#pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
-        const float top = fmaxf(m, mo);
-        if (top != -INFINITY)
-          l = l * ex2(m - top) + lo * ex2(mo - top);
-        else
-          l += lo;
-        m = top;
-      }
-      const float lse = __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
+      float first;
+      const float lse = row_lse(p, x, g, lane, first);
       if (lane == 0) s_lse[local][g] = lse;
-      if (blockIdx.y) continue;
+      if (chunk) continue;
       float acc[D / 32] = {};
       for (int i0 = 0; i0 < all; i0 += 32) {
-        const float mine = i0 == 0 ? first.x : i0 + lane < all ? ml(i0 + lane).x : -INFINITY;
+        const float mine = i0 == 0 ? first : i0 + lane < all ? record_ml(p, x, i0 + lane, g).x : -INFINITY;
         const float wgt = all ? ex2(mine - lse) : 0.f;
         const int n = min(32, all - i0);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
           const float wi = __shfl_sync(0xffffffffu, wgt, i);
-          const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(i0 + i) * D + lane * (D / 32);
+          const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(p, x, i0 + i, g) * D + lane * (D / 32);
           float part[D / 32];
           if constexpr (D == 128) {
             const float4 y = *reinterpret_cast<const float4*>(o);
@@ -874,8 +935,8 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
   if (seq < 0) return;
   const float* L = p.w.logits + static_cast<size_t>(unit) * group * v.cap;
   float* score = v.score + (static_cast<size_t>(seq) * v.heads + h) * v.cap;
-  const int step = gridDim.y * unit_warps * 128;
-  for (int j = ((blockIdx.y * unit_warps + sub) * 32 + lane) * 4; j < len; j += step) {
+  const int step = chunks * unit_warps * 128;
+  for (int j = ((chunk * unit_warps + sub) * 32 + lane) * 4; j < len; j += step) {
     // four slots a lane: a sequence's rows end at a multiple of its page
     float4 sum = *reinterpret_cast<float4*>(score + j);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
@@ -894,35 +955,6 @@ __global__ void __launch_bounds__(32 * kFinishWarps)
     if (j + 3 < len) sum.w += a[3];
     *reinterpret_cast<float4*>(score + j) = sum;
   }
-}
-
-// Scores of a prefix with few rows, from their logits: block (head; keys), rows in order.
-constexpr int kSumThreads = 128;
-
-__global__ void __launch_bounds__(kSumThreads)
-    pool_prefix_sum_kernel(const __grid_constant__ AttendParams p) {
-  const PoolView& v = p.a.v;
-  const int plen = max(0, checked_length(v, p.a.prefix, false));
-  const int h = blockIdx.x, rows = p.s.n * p.s.group, j = (blockIdx.y * kSumThreads + threadIdx.x) * 4;
-  grid_dependency_wait();
-  if (j >= plen) return;
-  const float* L = p.w.plogits + static_cast<size_t>(h) * rows * v.cap + j;
-  const float* nlse = p.w.nlse + static_cast<size_t>(h) * TILE_ROWS;
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i < rows; ++i) {
-    const float n = nlse[i];
-    const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(i) * v.cap);
-    if (n == -INFINITY) continue;  // not counted, whatever its logits are
-    a[0] += ex2(y.x + n);
-    a[1] += ex2(y.y + n);
-    a[2] += ex2(y.z + n);
-    a[3] += ex2(y.w + n);
-  }
-  float* score = v.score + (static_cast<size_t>(p.a.prefix) * v.heads + h) * v.cap + j;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (j + i < plen) score[i] += a[i];
 }
 
 // ------------------------------------------------------------------ host side
@@ -957,7 +989,7 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, bool codes, void
   w.seq = reinterpret_cast<int*>(take(s.n * sizeof(int)));
   w.cum = reinterpret_cast<int*>(take((s.n + 1) * sizeof(int)));
   w.nlse = reinterpret_cast<float*>(
-      take(s.blocks && accumulate ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
+      take(s.blocks && !s.few && accumulate ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
   w.pml = reinterpret_cast<float2*>(take(prow * sizeof(float2)));
   w.tml = reinterpret_cast<float2*>(take(trow * sizeof(float2)));
   w.po = reinterpret_cast<float*>(take(prow * s.d * sizeof(float)));
@@ -1015,14 +1047,11 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
   const int chunks = p.a.accumulate
                          ? std::max(1, std::min(8 * p.s.grid / blocks, (p.a.v.cap + 511) / 512))
                          : 1;
-  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks, chunks), 32 * kFinishWarps, 0, stream, p,
-                        unit_warps)) != cudaSuccess)
+  const int sums = p.w.plogits ? p.s.heads * ((p.a.v.cap + 4 * kFinishThreads - 1) / (4 * kFinishThreads)) : 0;
+  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks * chunks + sums), kFinishThreads, 0, stream,
+                        p, unit_warps, blocks, chunks)) != cudaSuccess)
     return e;
-  if (!p.a.accumulate || p.a.prefix < 0) return cudaSuccess;
-  if (many) return pool_prefix_score(p, stream);
-  return launch_after(pool_prefix_sum_kernel,
-                      dim3(p.s.heads, (p.a.v.cap + 4 * kSumThreads - 1) / (4 * kSumThreads)),
-                      kSumThreads, 0, stream, p);
+  return many && p.a.accumulate ? pool_prefix_score(p, stream) : cudaSuccess;
 }
 
 }  // namespace
