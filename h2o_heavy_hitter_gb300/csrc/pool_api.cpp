@@ -219,8 +219,14 @@ void h2o_pool_destroy(h2o_pool* p) {
     int cur = -1;
     const bool other = cudaGetDevice(&cur) == cudaSuccess && cur != p->device;
     if (other) cudaSetDevice(p->device);
-    cudaDeviceSynchronize();  // whichever streams its calls ran on
-    device_free(p->base);
+    guarded([&] {
+      // whichever streams its calls ran on; a synchronisation would spoil a capture
+      cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+      cudaStreamIsCapturing(current_stream(), &capture);
+      if (capture == cudaStreamCaptureStatusNone) cudaDeviceSynchronize();
+      device_free(p->base);
+      return H2O_OK;
+    });
     if (other) cudaSetDevice(cur);
   }
   delete p;

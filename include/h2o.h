@@ -453,7 +453,8 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
                     int max_pages, int kv_format, h2o_pool** out);
 
 /* h2o_pool_destroy - wait for the device's work, then free the pool. NULL is
- * accepted. Not during a stream capture. */
+ * accepted. While the current stream is captured nothing is waited for: the
+ * pool's work on other streams must then have finished. */
 void h2o_pool_destroy(h2o_pool* pool);
 
 /* h2o_pool_view - device addresses of one layer's arrays; the layers of an

@@ -429,6 +429,90 @@ def test_calls_on_another_stream_and_in_a_graph():
     b.close()
 
 
+def test_two_graphs_and_eager_calls_on_streams_of_their_own():
+    """Layers are independent: graphs of two layers and eager calls on a third run at once and
+    leave what they leave one after the other."""
+    import h2o_heavy_hitter_gb300 as h2o
+    heads, d, page, L = 4, 64, 16, 3
+    gen = torch.Generator("cuda").manual_seed(5)
+    pool = h2o.h2o_pool_create(L, 120, page, heads, d, 12, 30)
+    k = torch.randn(2, 12, heads, 400, d, generator=gen, device="cuda").to(torch.bfloat16)
+    q = torch.randn(L, 11, 2 * heads, d, generator=gen, device="cuda").to(torch.bfloat16)
+    one = torch.randn(11, heads, 1, d, generator=gen, device="cuda").to(torch.bfloat16)
+    lens, all_, batch = ints([50 + 7 * i for i in range(11)] + [400]), ints(range(12)), ints(range(11))
+    for layer in range(L):
+        h2o.h2o_pool_write(pool, layer, all_, k[0], k[1], lens)
+    view = h2o.h2o_pool_view(pool)
+    start = {n: x.clone() for n, x in view.items()}
+
+    def step(layer):
+        h2o.h2o_pool_write(pool, layer, batch, one, one)
+        return h2o.h2o_pool_attend(pool, layer, batch, q[layer], prefix=11)
+
+    def reset():
+        for n, x in start.items():
+            view[n].copy_(x)
+
+    want = []
+    for layer in range(L):
+        for _ in range(6):
+            out = step(layer)
+        want.append([x.clone() for x in out])
+    scores = view["score"].clone()
+    reset()
+    streams = [torch.cuda.Stream() for _ in range(L)]
+    graphs, outs = [], []
+    for layer in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[layer]):
+            outs.append(step(layer))
+    reset()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for layer in range(2):
+            with torch.cuda.stream(streams[layer]):
+                graphs[layer].replay()
+        with torch.cuda.stream(streams[2]):
+            eager = step(2)
+    torch.cuda.synchronize()
+    for got, ref in zip(outs + [eager], want):
+        assert all(torch.equal(x, y) for x, y in zip(got, ref))
+    assert torch.equal(view["score"], scores)
+    h2o.h2o_pool_sync_check(pool)
+    pool.close()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_the_longest_list(kv):
+    """1024 entries, the most of one call: every operator."""
+    n = 1024
+    b = Both(pages=2 * n + 60, page=16, heads=1, d=64, sequences=2 * n + 1, max_pages=8, kv=kv)
+    lens = [int(x) for x in b.rng.integers(0, 4, n)]
+    b.write(range(n), 3, lens)
+    b.write([2 * n], 100)
+    b.attend(range(n), 2, prefix=2 * n)
+    b.check()
+    b.fork(range(n), range(n, 2 * n))
+    b.compact(range(n, 2 * n), 1, 1)
+    b.write(range(n), 1)
+    b.free(range(n - 1, -1, -1))
+    b.check()
+    b.attend([-1, 0] * 2 + list(range(n + 4, 2 * n)), 1, prefix=2 * n)
+    b.check(errors=16)  # sequence 0 twice
+    b.close()
+
+
+@pytest.mark.parametrize("kept_in_shared", [45056, 45057, 70000])
+def test_compact_rows_around_what_shared_memory_holds(kept_in_shared):
+    r, h = 40, 1000
+    n = kept_in_shared + r
+    b = Both(pages=1 + -(-n // 128) + 10, page=128, heads=1, d=64, sequences=1, max_pages=560, seed=1)
+    b.write([0], n)
+    b.compact([0], h, r)
+    b.check()
+    b.close()
+
+
 def test_views_keep_their_pool():
     import gc
     import h2o_heavy_hitter_gb300 as h2o
