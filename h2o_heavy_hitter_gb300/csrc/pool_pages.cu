@@ -372,8 +372,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-// One block per (entry, head, kWriteTokens tokens); eight lanes per token, each
-// D / 8 values of its key and of its value.
+// kWriteTokens tokens per block, of one (entry, head) or, where calls write few
+// tokens (a step's), of several: 1 << span tokens of each. Eight lanes per token,
+// each D / 8 values of its key and of its value.
 constexpr int kWriteTokens = 32;
 // 448 / amax overflows below 448 / FLT_MAX (just above 2^-120): such vectors are stored as zero.
 constexpr float kTinyVector = 0x1p-119f;
@@ -382,15 +383,17 @@ template <int D, bool F8>
 __global__ void __launch_bounds__(256)
     write_kernel(PoolView v, int n, const int32_t* __restrict__ seqs,
                  const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V, int T,
-                 const float* __restrict__ score, const int32_t* plan) {
+                 int span, const float* __restrict__ score, const int32_t* plan) {
   constexpr int LPT = 8, EPL = D / LPT, NV = EPL / 8;
-  const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
-  const int t = blockIdx.y * kWriteTokens + threadIdx.x / LPT, l = threadIdx.x % LPT;
+  const int token = threadIdx.x / LPT, l = threadIdx.x % LPT;
+  const int unit = (blockIdx.x * kWriteTokens >> span) + (token >> span);  // (entry, head)
+  const int t = blockIdx.y * kWriteTokens + (token & ((1 << span) - 1));
+  const int e = unit / v.heads, head = unit - e * v.heads;
   grid_dependency_wait();
-  if (t >= plan[e * kPlanInts]) return;  // whole groups of eight lanes leave together
+  if (e >= n || t >= plan[e * kPlanInts]) return;  // whole groups of eight lanes leave together
   const unsigned gmask = 0xffu << (threadIdx.x & 31 & ~(LPT - 1));
   const int seq = seqs[e], slot = plan[e * kPlanInts + 1] + t;
-  const size_t src = (static_cast<size_t>(blockIdx.x) * T + t) * D + l * EPL;
+  const size_t src = (static_cast<size_t>(unit) * T + t) * D + l * EPL;
   uint4 raw[2][NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(256)
   if (l == 0) {
     v.pos[to] = plan[e * kPlanInts + 2] + t;
     v.score[(static_cast<size_t>(seq) * v.heads + head) * v.cap + slot] =
-        score ? score[static_cast<size_t>(blockIdx.x) * T + t] : 0.f;
+        score ? score[static_cast<size_t>(unit) * T + t] : 0.f;
   }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
@@ -710,12 +713,15 @@ cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void
   write_plan_kernel<<<1, kPlanThreads, 0, stream>>>(v, n, seqs, T, lens, fresh, plan);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid(n * v.heads, (T + kWriteTokens - 1) / kWriteTokens);
+  int span = 0;
+  while (1 << span < kWriteTokens && 1 << span < T) ++span;
+  const int units = kWriteTokens >> span;  // per block
+  const dim3 grid((n * v.heads + units - 1) / units, (T + kWriteTokens - 1) / kWriteTokens);
   auto kk = static_cast<const __nv_bfloat16*>(K);
   auto vv = static_cast<const __nv_bfloat16*>(V);
   auto kern = v.d == 128 ? (v.kscale ? write_kernel<128, true> : write_kernel<128, false>)
                          : (v.kscale ? write_kernel<64, true> : write_kernel<64, false>);
-  return launch_after(kern, grid, 256, 0, stream, v, n, seqs, kk, vv, T, score,
+  return launch_after(kern, grid, 256, 0, stream, v, n, seqs, kk, vv, T, span, score,
                       static_cast<const int32_t*>(plan));
 }
 
