@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     // one overlaps the product of the next. An S^T buffer and a P buffer are those
     // of the warpgroup's tile before the last, whose O^T is issued by then; the
     // MMAs of one thread complete in order.
-    if (lane == 0) {
+    {
       const uint64_t dk0 = F8 ? desc_codes<D>(sK) : desc_kmajor<D>(sK, 0);
       const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : smem_desc(sQ, 16, 1024);
       const uint64_t dp0 = smem_desc(sP, 16, 1024);
@@ -460,14 +460,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       } pv;
       auto issue_pv = [&]() -> bool {
         const uint32_t st = pv.g % RV, buf = pv.c & 1;
-        if (!pool_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
-            !pool_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err) ||
-            (pv.first && pv.e >= 2 && !pool_wait(&bars->o_free[pv.t], ((pv.e >> 1) - 1) & 1, v.err)))
+        if (!pool_warp_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
+            !pool_warp_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err) ||
+            (pv.first && pv.e >= 2 && !pool_warp_wait(&bars->o_free[pv.t], ((pv.e >> 1) - 1) & 1, v.err)))
           return false;
         tc_fence_after();
         const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
         const uint64_t pb = dp0 + static_cast<uint64_t>((pv.t * 2 + buf) * (C::P >> 4));
         const uint32_t o = tmem + C::O_COL + pv.t * 32;
+        if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
           umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
@@ -475,16 +476,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         umma_commit(&bars->values.empty[st]);
         umma_commit(&bars->pv_done[pv.t][buf]);
         if (pv.last) umma_commit(&bars->o_last[pv.t]);
+        }
+        __syncwarp();
         return true;
       };
       while (ok && w.next()) {
         const int t = e & 1, qb = e & 1;
         const int cols = w.rows() <= 16 ? 16 : 32;
         const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0), idesc8 = idesc_e4m3(TILE_KEYS, cols);
-        if (!pool_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
+        if (!pool_warp_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
           const uint32_t st = g % RK, buf = c[t] & 1;
-          if (!pool_wait(&bars->keys.full[st], (g / RK) & 1, v.err)) {
+          if (!pool_warp_wait(&bars->keys.full[st], (g / RK) & 1, v.err)) {
             ok = false;
             break;
           }
@@ -492,6 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::Q >> 4));
           const uint32_t d_tm = tmem + t * 64 + buf * 32;
+          if (elect_one()) {
           if constexpr (F8) {
 #pragma unroll
             for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
@@ -506,6 +510,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           umma_commit(&bars->s_full[t][buf]);
           umma_commit(&bars->keys.empty[st]);
           if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
+          }
+          __syncwarp();
           if (pv.live && !issue_pv()) {
             ok = false;
             break;
