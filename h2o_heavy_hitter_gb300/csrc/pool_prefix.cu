@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     // ---------------------------------------------------------------- MMA issuer
     // S j is followed by the P V of S j - 1, so the softmax of one S overlaps the
     // product of the next; the S buffer of j is that of j - 2, whose P V is issued.
-    if (lane == 0) {
+    {
       constexpr uint32_t idesc_qk = idesc_bf16(TILE_ROWS, TILE_KEYS, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(TILE_ROWS, D, 0, 1);
       const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : desc_kmajor<D>(sQ, 0);
@@ -222,17 +222,18 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       } pv;
       auto issue_pv = [&]() -> bool {
         const uint32_t st = pv.g % RV, buf = pv.j & 1;
-        if (!pool_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
-            !pool_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err))
+        if (!pool_warp_wait(&bars->p_ready[buf], (pv.j >> 1) & 1, v.err) ||
+            !pool_warp_wait(&bars->values.full[st], (pv.g / RV) & 1, v.err))
           return false;
         if (pv.first && pv.e > 0) {
           for (int t = 0; t < 2; ++t)
-            if ((!pv.two || t == pv.t) && !pool_wait(&bars->o_free[t], (pv.e - 1) & 1, v.err))
+            if ((!pv.two || t == pv.t) && !pool_warp_wait(&bars->o_free[t], (pv.e - 1) & 1, v.err))
               return false;
         }
         tc_fence_after();
         const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
         const uint32_t s_tm = tmem + buf * 128;
+        if (elect_one()) {
         // B = V tile, MN-major: 16 keys = two 8-row swizzle atoms (2048 bytes)
 #pragma unroll
         for (int kk = 0; kk < TILE_KEYS / 16; ++kk) {
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         if (pv.last)
           for (int t = 0; t < 2; ++t)
             if (!pv.two || t == pv.t) umma_commit(&bars->o_last[t]);
+        }
+        __syncwarp();
         return true;
       };
       while (ok && w.next()) {
@@ -255,8 +258,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const uint32_t st = g % RK;
           for (int t = 0; ok && t < nt; ++t, ++j) {
             const uint32_t qb = (qn + t) & 1;
-            if ((kt == w.kt0 && !pool_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
-                (t == 0 && !pool_wait(&bars->keys.full[st], (g / RK) & 1, v.err))) {
+            if ((kt == w.kt0 && !pool_warp_wait(&bars->q_full[qb], ((qn + t) >> 1) & 1, v.err)) ||
+                (t == 0 && !pool_warp_wait(&bars->keys.full[st], (g / RK) & 1, v.err))) {
               ok = false;
               break;
             }
@@ -264,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
             const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
             const uint32_t d_tm = tmem + (j & 1) * 128;
+            if (elect_one()) {
             if constexpr (F8) {
 #pragma unroll
               for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
@@ -279,6 +283,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             umma_commit(&bars->s_full[j & 1]);
             if (t == nt - 1) umma_commit(&bars->keys.empty[st]);
             if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
+            }
+            __syncwarp();
             if (pv.live && !issue_pv()) {
               ok = false;
               break;
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
       }
     }
   } else if (warp == kWarpMMA) {
-    if (lane == 0) {
+    {
       const uint64_t dq0 = F8 ? desc_codes<D>(sQ) : desc_kmajor<D>(sQ, 0);
       const uint64_t dk0 = F8 ? desc_codes<D>(ring) : desc_kmajor<D>(ring, 0);
       uint32_t f0 = 0, cnt[2] = {0, 0};  // f0: fill of the head's (or tile's) row tile 0
@@ -619,11 +625,11 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         const bool done = !stay || k.last_of_head();  // the row tiles' last use
         const uint32_t st = g % R;
         const int t = g & 1;
-        if (!pool_wait(&bars->keys.full[st], (g / R) & 1, v.err)) break;
+        if (!pool_warp_wait(&bars->keys.full[st], (g / R) & 1, v.err)) break;
         for (int qt = 0; qt < nq; ++qt) {
           const uint32_t f = f0 + qt, qb = f & 1, buf = 2 * t + (cnt[t] & 1);
-          if ((fresh && !pool_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
-              (cnt[t] >= 2 && !pool_wait(&bars->s_free[buf], ((cnt[t] >> 1) - 1) & 1, v.err))) {
+          if ((fresh && !pool_warp_wait(&bars->q_full[qb], (f >> 1) & 1, v.err)) ||
+              (cnt[t] >= 2 && !pool_warp_wait(&bars->s_free[buf], ((cnt[t] >> 1) - 1) & 1, v.err))) {
             ok = false;
             break;
           }
@@ -633,6 +639,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           const uint64_t kb = dk0 + static_cast<uint64_t>(st * (C::KTILE >> 4));
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
           const uint32_t d_tm = tmem + buf * 128;
+          if (elect_one()) {
           if constexpr (F8) {
             const uint32_t idesc = idesc_e4m3(TILE_KEYS, cols);
 #pragma unroll
@@ -650,6 +657,8 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           umma_commit(&bars->s_full[buf]);
           if (done) umma_commit(&bars->q_empty[qb]);
           if (qt == nq - 1) umma_commit(&bars->keys.empty[st]);
+          }
+          __syncwarp();
           ++cnt[t];
         }
       }
