@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         for (int kk = 0; kk < TILE_KEYS / 16; ++kk) {
           const int half = kk >> 2;
           const uint32_t o = tmem + C::O_COL + (pv.two ? pv.t : half) * 128;
-          const uint32_t a = s_tm + (pv.two ? kk * 8 : half * 64 + (kk & 3) * 8);
+          const uint32_t a = s_tm + half * 64 + (kk & 3) * 8;
           const bool fresh = pv.first && (pv.two ? kk == 0 : (kk & 3) == 0);
           umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
         }
@@ -388,9 +388,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t sc2 = f2_pack(qscale, qscale), nm2 = f2_pack(-ref, -ref);
           uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-          for (int c = 0; c < chunks; ++c) {
+          for (int c = chunks - 1; c >= 0; --c) {  // the last chunk is still in registers
             const int first = col0 + 64 * c;
-            if (chunks > 1) load(s, first);
+            if (c < chunks - 1) load(s, first);
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
               uint32_t pk[8];
@@ -410,8 +410,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                   pk[x] = pack_bf16x2(p0, p1);
                 }
               }
-              // P over S columns already read: this half's, or (two chunks) the first 64
-              tmem_st8(s_tm + (w.two ? 32 * c : col0) + cc * 8, pk);
+              tmem_st8(s_tm + first + cc * 8, pk);  // P over the S columns it came from
             }
           }
           float r0, r1, r2, r3;
