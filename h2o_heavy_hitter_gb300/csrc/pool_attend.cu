@@ -198,23 +198,6 @@ constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpV = 3, kWarpRows = 4, kWarpCodes = 
 constexpr int kCodeThreads = 256;
 constexpr int kQBox = kFewRows * 128;  // rows x 64 channels (or keys) of an operand with few rows
 
-template <int D, bool F8>
-struct Cfg {
-  static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
-  static constexpr int TILE = TILE_KEYS * D * 2;
-  static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;  // keys are used as they are stored
-  static constexpr int RK = (F8 ? 3 : 2) * (128 / D), RV = (F8 ? 2 : 3) * (128 / D);
-  static constexpr int S = F8 ? 2 * (128 / D) : 1;  // slots of value codes
-  static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
-  static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
-  static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
-  static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(RK) * KTILE + RV * TILE + 2 * Q + 4 * P + CODES + SCALES +
-                                 sizeof(List) + 3072 + 1024;
-  // TMEM: S^T of warpgroup t in columns 64 t + 32 (0, 1), its O^T at 128 + 32 t
-  static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
-};
-
 template <int RK, int RV, int S>
 struct Bars {
   RingBars<RK> keys;
@@ -229,6 +212,23 @@ struct Bars {
   uint32_t tmem;
   int wsum[33];
   float xmax[2][2][4][kFewRows];   // [warpgroup][use & 1][quadrant][row]
+};
+
+template <int D, bool F8>
+struct Cfg {
+  static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
+  static constexpr int TILE = TILE_KEYS * D * 2;
+  static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;  // keys are used as they are stored
+  static constexpr int RK = (F8 ? 3 : 2) * (128 / D), RV = (F8 ? 2 : 3) * (128 / D);
+  static constexpr int S = F8 ? 2 * (128 / D) : 1;  // slots of value codes
+  static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
+  static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
+  static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
+  static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
+  static constexpr size_t SMEM = static_cast<size_t>(RK) * KTILE + RV * TILE + 2 * Q + 4 * P + CODES +
+                                 SCALES + sizeof(List) + sizeof(Bars<RK, RV, S>) + 1024;
+  // TMEM: S^T of warpgroup t in columns 64 t + 32 (0, 1), its O^T at 128 + 32 t
+  static constexpr uint32_t O_COL = 128, TMEM_COLS = 256;
 };
 
 // Fp32 values as integers of the same order, for the integer maximum of a warp.
@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   float* vscales = cscales + C::S * TILE_KEYS;                  // [kScaleTiles][128]
   List& list = *reinterpret_cast<List*>(reinterpret_cast<uint8_t*>(kscales) + C::SCALES);
   auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(&list + 1);
-  static_assert(sizeof(Bars<RK, RV, C::S>) <= 3072, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -470,12 +469,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         const uint32_t o = tmem + C::O_COL + pv.t * 32;
         if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
-          umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
-                  pv.idesc | (1u << 15), (!pv.first || kk > 0) ? 1u : 0u);
-        umma_commit(&bars->values.empty[st]);
-        umma_commit(&bars->pv_done[pv.t][buf]);
-        if (pv.last) umma_commit(&bars->o_last[pv.t]);
+          for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
+            umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
+                    pv.idesc | (1u << 15), (!pv.first || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->values.empty[st]);
+          umma_commit(&bars->pv_done[pv.t][buf]);
+          if (pv.last) umma_commit(&bars->o_last[pv.t]);
         }
         __syncwarp();
         return true;
@@ -496,20 +495,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::Q >> 4));
           const uint32_t d_tm = tmem + t * 64 + buf * 32;
           if (elect_one()) {
-          if constexpr (F8) {
+            if constexpr (F8) {
 #pragma unroll
-            for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
-              umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
-                           qd + kk / (D / 32) * (kFewRows * D >> 4) + kk % (D / 32) * 2, idesc8, kk > 0);
-          } else {
+              for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
+                umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
+                             qd + kk / (D / 32) * (kFewRows * D >> 4) + kk % (D / 32) * 2, idesc8, kk > 0);
+            } else {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(d_tm, kb + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
-                      qd + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
-          }
-          umma_commit(&bars->s_full[t][buf]);
-          umma_commit(&bars->keys.empty[st]);
-          if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss(d_tm, kb + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
+                        qd + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            }
+            umma_commit(&bars->s_full[t][buf]);
+            umma_commit(&bars->keys.empty[st]);
+            if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
           }
           __syncwarp();
           if (pv.live && !issue_pv()) {
@@ -738,60 +737,16 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ joining the pieces
 constexpr int kFinishWarps = 4, kFinishThreads = 32 * kFinishWarps;
 
-// Where the records of a (entry, key head) unit's rows are: `prefix` of the
-// prefix, then `own` of the own tokens. Record i of row g is at base + i * step + g.
-struct Records {
-  int prefix, own;
-  size_t pbase, pstep, obase;
-};
-
-// Warp-wide: the four divisions that place the pieces run in as many lanes.
+// place_records by a warp: the four divisions run in as many lanes.
 __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int h, int plen,
                                               const int (&cum)[3], int lane) {
-  Records x{};
-  const int pt = p.a.prefix >= 0 ? key_tiles(plen) : 0, tiles = cum[1] - cum[0];
-  const int64_t own = static_cast<int64_t>(cum[2]) * p.s.heads;
-  const int64_t pre = static_cast<int64_t>(p.s.heads) * (p.s.few ? 1 : p.s.blocks) * pt;
-  const int64_t ototal = own + (p.s.few ? pre : 0), ptotal = p.s.few ? ototal : pre;
-  const int qt = b / p.s.per_tile, r0 = (b - qt * p.s.per_tile) * p.s.group;
-  const int u = p.s.few ? h : h * p.s.blocks + (qt >> 1);
-  const int64_t pa = static_cast<int64_t>(u) * pt;
-  const int64_t oa = (p.s.few ? pre : 0) + static_cast<int64_t>(cum[0]) * p.s.heads + static_cast<int64_t>(h) * tiles;
-  // first and last tile of the prefix unit, of the own one
-  const int64_t at = lane < 2 ? pa + (lane ? pt - 1 : 0) : oa + (lane == 2 ? 0 : tiles - 1);
-  const int64_t total = lane < 2 ? ptotal : ototal;
-  const int c = total > 0 ? owner(at, total, p.s.grid) : 0;
-  const int p0 = __shfl_sync(0xffffffffu, c, 0), p1 = __shfl_sync(0xffffffffu, c, 1);
-  const int o0 = __shfl_sync(0xffffffffu, c, 2), o1 = __shfl_sync(0xffffffffu, c, 3);
-  if (pt) {
-    x.prefix = p1 - p0 + 1;
-    const size_t piece = u + p0;
-    if (p.s.few) {
-      x.pbase = piece * kFewRows + r0;
-      x.pstep = kFewRows;
-    } else if ((qt | 1) < p.s.nq) {  // a block of two row tiles: a record per tile
-      x.pbase = (piece * 2 + (qt & 1)) * TILE_ROWS + r0;
-      x.pstep = 2 * TILE_ROWS;
-    } else {                         // one row tile: a record per half of the keys
-      x.pbase = piece * 2 * TILE_ROWS + r0;
-      x.pstep = TILE_ROWS;
-      x.prefix *= 2;
-    }
-  }
-  if (tiles) {
-    x.own = o1 - o0 + 1;
-    x.obase = static_cast<size_t>(b * p.s.heads + h + o0) * p.s.group;
-  }
-  return x;
-}
-
-// Index of record i of row g in its array (the prefix's for i < x.prefix), and its {max, sum}.
-__device__ __forceinline__ size_t record(const AttendParams& p, const Records& x, int i, int g) {
-  return (i < x.prefix ? x.pbase + i * x.pstep
-                       : x.obase + static_cast<size_t>(i - x.prefix) * p.s.group) + g;
-}
-__device__ __forceinline__ float2 record_ml(const AttendParams& p, const Records& x, int i, int g) {
-  return (i < x.prefix ? p.w.pml : p.w.tml)[record(p, x, i, g)];
+  return place_records(p, b, h, plen, cum, [&](const int64_t (&at)[4], const int64_t (&total)[2], int (&c)[4]) {
+    const int64_t x = lane == 0 ? at[0] : lane == 1 ? at[1] : lane == 2 ? at[2] : at[3];
+    const int64_t n = lane < 2 ? total[0] : total[1];
+    const int mine = n > 0 ? owner(x, n, p.s.grid) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __shfl_sync(0xffffffffu, mine, i);
+  });
 }
 
 // A warp's lse (base 2) of row g, the same bits wherever it is computed; `first`:
@@ -804,23 +759,12 @@ __device__ __forceinline__ float row_lse(const AttendParams& p, const Records& x
   for (int i = lane; i < all; i += 32) {
     const float2 y = record_ml(p, x, i, g);
     if (i < 32) first = y.x;
-    const float top = fmaxf(m, y.x);
-    if (top != -INFINITY) {
-      l = l * ex2(m - top) + y.y * ex2(y.x - top);
-      m = top;
-    } else {
-      l += y.y;  // a NaN sum stays one
-    }
+    join(m, l, y.x, y.y);
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
     const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
-    const float top = fmaxf(m, mo);
-    if (top != -INFINITY)
-      l = l * ex2(m - top) + lo * ex2(mo - top);
-    else
-      l += lo;
-    m = top;
+    join(m, l, mo, lo);
   }
   return __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
 }
@@ -870,15 +814,8 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
 // probabilities of the own tokens to their scores. Every chunk computes the lse's
 // it needs, chunk 0 writes. `blocks` * `chunks` such blocks, then those of the prefix's scores.
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
-    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps, int blocks, int chunks) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  __shared__ float s_lse[kFinishWarps][kFewRows];
-  if (static_cast<int>(blockIdx.x) >= blocks * chunks) {
-    prefix_scores(p, blockIdx.x - blocks * chunks, s_lse[0]);
-    return;
-  }
+__device__ __forceinline__ void finish_block(const AttendParams& p, int unit_warps, int blocks, int chunks,
+                                             float (&s_lse)[kFinishWarps][kFewRows]) {
   const PoolView& v = p.a.v;
   const int group = p.s.group, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x / blocks, block = blockIdx.x - chunk * blocks;
@@ -905,13 +842,15 @@ __global__ void __launch_bounds__(kFinishThreads)
       if (chunk) continue;
       float acc[D / 32] = {};
       for (int i0 = 0; i0 < all; i0 += 32) {
-        const float mine = i0 == 0 ? first : i0 + lane < all ? record_ml(p, x, i0 + lane, g).x : -INFINITY;
+        const float mine =
+            i0 == 0 ? first : i0 + lane < all ? record_ml(p, x, i0 + lane, g).x : -INFINITY;
         const float wgt = all ? ex2(mine - lse) : 0.f;
         const int n = min(32, all - i0);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
           const float wi = __shfl_sync(0xffffffffu, wgt, i);
-          const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) + record(p, x, i0 + i, g) * D + lane * (D / 32);
+          const float* o = (i0 + i < x.prefix ? p.w.po : p.w.to) +
+                           record(p, x, i0 + i, g) * D + lane * (D / 32);
           float part[D / 32];
           if constexpr (D == 128) {
             const float4 y = *reinterpret_cast<const float4*>(o);
@@ -963,6 +902,23 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
 }
 
+// `beside`: launched behind pool_prefix_score_kernel, which lets it start once the
+// kernels before both have completed. It reads nothing of that kernel, so only
+// its own end waits: what follows this kernel follows both.
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps, int blocks, int chunks,
+                       bool beside) {
+  __shared__ float s_lse[kFinishWarps][kFewRows];
+  if (!beside) grid_dependency_wait();
+  grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= blocks * chunks)
+    prefix_scores(p, blockIdx.x - blocks * chunks, s_lse[0]);
+  else
+    finish_block<D>(p, unit_warps, blocks, chunks, s_lse);
+  if (beside && blockIdx.x == 0) grid_dependency_wait();
+}
+
 // ------------------------------------------------------------------ host side
 Shape shape_of(const AttendArgs& a, int sms) {
   Shape s{};
@@ -994,8 +950,9 @@ size_t scratch_layout(const Shape& s, int cap, bool accumulate, bool codes, void
   AttendScratch w{};
   w.seq = reinterpret_cast<int*>(take(s.n * sizeof(int)));
   w.cum = reinterpret_cast<int*>(take((s.n + 1) * sizeof(int)));
+  const bool nlse = s.blocks && !s.few && accumulate && !score_joins(s);
   w.nlse = reinterpret_cast<float*>(
-      take(s.blocks && !s.few && accumulate ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
+      take(nlse ? static_cast<size_t>(s.heads) * s.nq * TILE_ROWS * sizeof(float) : 0));
   w.pml = reinterpret_cast<float2*>(take(prow * sizeof(float2)));
   w.tml = reinterpret_cast<float2*>(take(trow * sizeof(float2)));
   w.po = reinterpret_cast<float*>(take(prow * s.d * sizeof(float)));
@@ -1053,11 +1010,14 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
   const int chunks = p.a.accumulate
                          ? std::max(1, std::min(8 * p.s.grid / blocks, (p.a.v.cap + 511) / 512))
                          : 1;
-  const int sums = p.w.plogits ? p.s.heads * ((p.a.v.cap + 4 * kFinishThreads - 1) / (4 * kFinishThreads)) : 0;
+  const int per_block = 4 * kFinishThreads;  // keys of prefix_scores
+  const int sums = p.w.plogits ? p.s.heads * ((p.a.v.cap + per_block - 1) / per_block) : 0;
+  const bool scores = many && p.a.accumulate, beside = scores && score_joins(p.s);
+  if (beside && (e = pool_prefix_score(p, stream)) != cudaSuccess) return e;
   if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks * chunks + sums), kFinishThreads, 0, stream,
-                        p, unit_warps, blocks, chunks)) != cudaSuccess)
+                        p, unit_warps, blocks, chunks, beside)) != cudaSuccess)
     return e;
-  return many && p.a.accumulate ? pool_prefix_score(p, stream) : cudaSuccess;
+  return scores && !beside ? pool_prefix_score(p, stream) : cudaSuccess;
 }
 
 }  // namespace

@@ -36,6 +36,17 @@ __device__ __forceinline__ void store_32b(float* dst, const uint32_t* v) {
 constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpV = 3, kWarpSoftmax = 4, kWarpCodes = 12;
 constexpr int kCodeThreads = 128;
 
+template <int RK, int RV, int S>
+struct Bars {
+  RingBars<RK> keys;
+  RingBars<RV> values;
+  RingBars<S> codes;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
+  uint64_t o_last[2], o_free[2];               // one phase per unit
+  uint32_t tmem;
+};
+
 template <int D, bool F8>
 struct Cfg {
   static constexpr int THREADS = 32 * kWarpCodes + (F8 ? kCodeThreads : 0);
@@ -46,18 +57,8 @@ struct Cfg {
   static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
   static constexpr uint32_t O_COL = 256;  // S buffers at columns 0 and 128, O of half t at 256 + 128 t
   static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2 + RV) * TILE + RK * KTILE + CODES + SCALES + 1024 + 1024;
-};
-
-template <int RK, int RV, int S>
-struct Bars {
-  RingBars<RK> keys;
-  RingBars<RV> values;
-  RingBars<S> codes;
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
-  uint64_t o_last[2], o_free[2];               // one phase per unit
-  uint32_t tmem;
+  static constexpr size_t SMEM = static_cast<size_t>(2 + RV) * TILE + RK * KTILE + CODES + SCALES +
+                                 sizeof(Bars<RK, RV, S>) + 1024;
 };
 
 // A walk along one CTA's share of the units.
@@ -124,7 +125,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   float* cscales = kscales + RK * TILE_KEYS;                    // [S][128], of value codes
   float* vscales = cscales + C::S * TILE_KEYS;                  // [kScaleTiles][128]
   auto* bars = reinterpret_cast<Bars<RK, RV, C::S>*>(reinterpret_cast<uint8_t*>(kscales) + C::SCALES);
-  static_assert(sizeof(Bars<RK, RV, C::S>) <= 1024, "Bars must fit the space reserved in Cfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -234,20 +234,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
         const uint32_t s_tm = tmem + buf * 128;
         if (elect_one()) {
-        // B = V tile, MN-major: 16 keys = two 8-row swizzle atoms (2048 bytes)
+          // B = V tile, MN-major: 16 keys = two 8-row swizzle atoms (2048 bytes)
 #pragma unroll
-        for (int kk = 0; kk < TILE_KEYS / 16; ++kk) {
-          const int half = kk >> 2;
-          const uint32_t o = tmem + C::O_COL + (pv.two ? pv.t : half) * 128;
-          const uint32_t a = s_tm + half * 64 + (kk & 3) * 8;
-          const bool fresh = pv.first && (pv.two ? kk == 0 : (kk & 3) == 0);
-          umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
-        }
-        umma_commit(&bars->pv_done[buf]);
-        if (pv.frees) umma_commit(&bars->values.empty[st]);
-        if (pv.last)
-          for (int t = 0; t < 2; ++t)
-            if (!pv.two || t == pv.t) umma_commit(&bars->o_last[t]);
+          for (int kk = 0; kk < TILE_KEYS / 16; ++kk) {
+            const int half = kk >> 2;
+            const uint32_t o = tmem + C::O_COL + (pv.two ? pv.t : half) * 128;
+            const uint32_t a = s_tm + half * 64 + (kk & 3) * 8;
+            const bool fresh = pv.first && (pv.two ? kk == 0 : (kk & 3) == 0);
+            umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
+          }
+          umma_commit(&bars->pv_done[buf]);
+          if (pv.frees) umma_commit(&bars->values.empty[st]);
+          if (pv.last)
+            for (int t = 0; t < 2; ++t)
+              if (!pv.two || t == pv.t) umma_commit(&bars->o_last[t]);
         }
         __syncwarp();
         return true;
@@ -268,21 +268,21 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
             const uint32_t d_tm = tmem + (j & 1) * 128;
             if (elect_one()) {
-            if constexpr (F8) {
+              if constexpr (F8) {
 #pragma unroll
-              for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
-                umma_ss_8bit(d_tm, qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2,
-                             kb + kk % (D / 32) * 2, idesc_e4m3(TILE_ROWS, TILE_KEYS), kk > 0);
-            } else {
+                for (int kk = 0; kk < 2 * (D / 32); ++kk)  // the queries' first codes, then their second
+                  umma_ss_8bit(d_tm, qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2,
+                               kb + kk % (D / 32) * 2, idesc_e4m3(TILE_ROWS, TILE_KEYS), kk > 0);
+              } else {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-                umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+                  umma_ss(d_tm, qd + off, kb + off, idesc_qk, kk > 0);
+                }
               }
-            }
-            umma_commit(&bars->s_full[j & 1]);
-            if (t == nt - 1) umma_commit(&bars->keys.empty[st]);
-            if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
+              umma_commit(&bars->s_full[j & 1]);
+              if (t == nt - 1) umma_commit(&bars->keys.empty[st]);
+              if (kt == w.kt1 - 1) umma_commit(&bars->q_empty[qb]);
             }
             __syncwarp();
             if (pv.live && !issue_pv()) {
@@ -492,6 +492,16 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ scores of the prefix
+template <int R>
+struct ScoreBars {
+  RingBars<R> keys;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
+  uint64_t joined;                // a phase per head of the share
+  uint32_t tmem;
+  float nlse[2][2 * TILE_ROWS];   // [heads & 1] of a head's rows (score_joins)
+};
+
 // Warps as above, 4..7 even key tiles, 8..11 odd ones.
 template <int D, bool F8>
 struct ScoreCfg {
@@ -500,15 +510,8 @@ struct ScoreCfg {
   static constexpr int KTILE = F8 ? TILE_KEYS * D : TILE;
   static constexpr int R = (F8 ? 8 : 4) * (128 / D);
   static constexpr int SCALES = F8 ? R * TILE_KEYS * 4 : 0;
-  static constexpr size_t SMEM = static_cast<size_t>(2) * TILE + R * KTILE + SCALES + 1024 + 1024;
-};
-
-template <int R>
-struct ScoreBars {
-  RingBars<R> keys;
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
-  uint32_t tmem;
+  static constexpr size_t SMEM =
+      static_cast<size_t>(2) * TILE + R * KTILE + SCALES + sizeof(ScoreBars<R>) + 1024;
 };
 
 // One CTA's share of the (head, key tile) list.
@@ -531,6 +534,35 @@ struct KeyCursor {
   __device__ bool last_of_head() const { return it + 1 >= end || kt + 1 == tiles; }
 };
 
+// -lse (base 2) of row r of a head's row tile qt, -inf for one that is not counted.
+__device__ __noinline__ float joined_row(const AttendParams& p, int qt, int r, int h, int len) {
+  const int b = qt * p.s.per_tile + r / p.s.group, g = r % p.s.group;
+  if (r >= p.s.per_tile * p.s.group || b >= p.s.n || p.w.seq[b] < 0) return -INFINITY;
+  const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
+  auto owners = [&](const int64_t (&at)[4], const int64_t (&total)[2], int (&c)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = total[i / 2] > 0 ? owner(at[i], total[i / 2], p.s.grid) : 0;
+  };
+  const Records x = place_records(p, b, h, len, cum, owners);
+  const int all = x.prefix + x.own;
+  float m = -INFINITY, l = 0.f;
+  for (int i0 = 0; i0 < all; i0 += 8) {  // eight loads in flight
+    float2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = i0 + i < all ? record_ml(p, x, i0 + i, g) : make_float2(-INFINITY, 0.f);
+    float top = m, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;  // (no logit but -inf: sums of zero, or a NaN)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += y[i].y * ex2(y[i].x - ref);
+    l = l * ex2(m - ref) + sum;
+    m = top;
+  }
+  return -(m + log2f(l));
+}
+
 // The row tiles of a head stay in shared memory when there are at most two; more
 // are fetched again for every key tile. A fill is one load of a row tile: fill f
 // lies in buffer f & 1.
@@ -548,7 +580,6 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   uint8_t* ring = smem + 2 * C::TILE;
   float* scales = reinterpret_cast<float*>(ring + R * C::KTILE);  // [R][128]
   auto* bars = reinterpret_cast<ScoreBars<R>*>(reinterpret_cast<uint8_t*>(scales) + C::SCALES);
-  static_assert(sizeof(ScoreBars<R>) <= 1024, "Bars must fit the space reserved in ScoreCfg::SMEM");
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -560,6 +591,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_empty[i], 1);
     }
+    mbar_init(&bars->joined, 8);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], 4);
@@ -580,7 +612,7 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
   const uint32_t tmem = bars->tmem;
   const int len = max(0, checked_length(v, p.a.prefix, false));
   const int nq = p.s.nq, group = p.s.group;
-  const bool stay = nq <= 2;
+  const bool stay = score_joins(p.s);
   KeyCursor k(p, len, blockIdx.x);
 
   if (warp == 0) {
@@ -639,23 +671,23 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
           const uint64_t qd = dq0 + static_cast<uint64_t>(qb * (C::TILE >> 4));
           const uint32_t d_tm = tmem + buf * 128;
           if (elect_one()) {
-          if constexpr (F8) {
-            const uint32_t idesc = idesc_e4m3(TILE_KEYS, cols);
+            if constexpr (F8) {
+              const uint32_t idesc = idesc_e4m3(TILE_KEYS, cols);
 #pragma unroll
-            for (int kk = 0; kk < 2 * (D / 32); ++kk)
-              umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
-                           qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2, idesc, kk > 0);
-          } else {
-            const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0);
+              for (int kk = 0; kk < 2 * (D / 32); ++kk)
+                umma_ss_8bit(d_tm, kb + kk % (D / 32) * 2,
+                             qd + kk / (D / 32) * (C::KTILE >> 4) + kk % (D / 32) * 2, idesc, kk > 0);
+            } else {
+              const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-              umma_ss(d_tm, kb + off, qd + off, idesc, kk > 0);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+                umma_ss(d_tm, kb + off, qd + off, idesc, kk > 0);
+              }
             }
-          }
-          umma_commit(&bars->s_full[buf]);
-          if (done) umma_commit(&bars->q_empty[qb]);
-          if (qt == nq - 1) umma_commit(&bars->keys.empty[st]);
+            umma_commit(&bars->s_full[buf]);
+            if (done) umma_commit(&bars->q_empty[qb]);
+            if (qt == nq - 1) umma_commit(&bars->keys.empty[st]);
           }
           __syncwarp();
           ++cnt[t];
@@ -667,14 +699,27 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t cnt = 0;
     bool ok = true;
-    grid_dependency_wait();  // the lse's, by the kernel before
+    grid_dependency_wait();    // the pieces, or the lse's, by the kernels before
+    grid_launch_dependents();  // the finish kernel, when it comes behind this one
+    int last = -1;
+    uint32_t heads = 0;        // of the share so far
     for (uint32_t g = 0; ok && k.step(); ++g) {
+      if (stay && last != k.h) {  // half t joins the rows of row tile t, both use them
+        // (two buffers: the one written was last read before the other's phase)
+        if (t < nq) bars->nlse[heads & 1][t * TILE_ROWS + r] = joined_row(p, t, r, k.h, len);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->joined);
+        if (!pool_warp_wait(&bars->joined, heads & 1, v.err)) break;
+        ++heads;
+        last = k.h;
+      }
       if ((g & 1) != static_cast<uint32_t>(t)) continue;
       float acc = 0.f, ks = p.qscale;
       for (int qt = 0; qt < nq; ++qt, ++cnt) {
         const uint32_t buf = 2 * t + (cnt & 1);
         const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
-        const float* nl = p.w.nlse + (static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS;
+        const float* nl = stay ? bars->nlse[(heads - 1) & 1] + qt * TILE_ROWS
+                               : p.w.nlse + (static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS;
         if (!pool_warp_wait(&bars->s_full[buf], (cnt >> 1) & 1, v.err)) {
           ok = false;
           break;

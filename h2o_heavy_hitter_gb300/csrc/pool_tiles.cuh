@@ -33,7 +33,8 @@ struct Shape {
 struct AttendScratch {
   int* seq;        // [n] sequence of an entry, -1 skipped
   int* cum;        // [n + 1] own tiles of the entries before
-  float* nlse;     // [heads][nq][128] -lse (base 2) of a prefix row, -inf: not counted (accumulate only)
+  float* nlse;     // [heads][nq][128] -lse (base 2) of a prefix row, -inf: not counted
+                   // (accumulate, unless score_joins)
   float2* pml;     // prefix pieces {max, sum}: many rows [heads * blocks + grid][2][128],
                    // few rows [heads + grid][kFewRows]
   float2* tml;     // own pieces [n * heads + grid][group]
@@ -51,6 +52,12 @@ struct AttendParams {
   AttendScratch w;
   float qscale;  // log2(e) / sqrt(d)
 };
+
+// The prefix's score kernel joins the sums of its rows itself, and runs beside the
+// finish kernel, where two row tiles hold them. Beyond, every CTA would do that for
+// all rows of a head and keep them; it follows the finish kernel, which leaves them
+// in AttendScratch::nlse.
+inline __host__ __device__ bool score_joins(const Shape& s) { return s.nq <= 2; }
 
 // Launchers of the kernels for a prefix with many rows (pool_prefix.cu). The
 // first leaves pieces, the second adds the prefix's scores.
@@ -245,6 +252,72 @@ __device__ void convert_values(const PoolView& v, const uint8_t* codes, const fl
 template <int D>
 __device__ __forceinline__ uint64_t desc_codes(const uint8_t* tile) {
   return D == 128 ? smem_desc(tile, 16, 1024) : smem_desc_64(tile, 16, 512);
+}
+// ------------------------------------------------------------------ records
+// Where the records of a (entry, key head) unit's rows are: `prefix` of the
+// prefix, then `own` of the own tokens. Record i of row g is at base + i * step + g.
+struct Records {
+  int prefix, own;
+  size_t pbase, pstep, obase;
+};
+
+// owners(at, total, c): the CTAs c[4] that had tiles at[4] of lists of total[2] tiles:
+// the first and last tile of the prefix unit that holds the rows (list 0), then
+// of the own unit (list 1). cum: own tiles before the entry, before the next, of all.
+template <typename Owners>
+__device__ __forceinline__ Records place_records(const AttendParams& p, int b, int h, int plen,
+                                                 const int (&cum)[3], Owners&& owners) {
+  Records x{};
+  const int pt = p.a.prefix >= 0 ? key_tiles(plen) : 0, tiles = cum[1] - cum[0];
+  const int64_t own = static_cast<int64_t>(cum[2]) * p.s.heads;
+  const int64_t pre = static_cast<int64_t>(p.s.heads) * (p.s.few ? 1 : p.s.blocks) * pt;
+  const int64_t ototal = own + (p.s.few ? pre : 0), ptotal = p.s.few ? ototal : pre;
+  const int qt = b / p.s.per_tile, r0 = (b - qt * p.s.per_tile) * p.s.group;
+  const int u = p.s.few ? h : h * p.s.blocks + (qt >> 1);
+  const int64_t pa = static_cast<int64_t>(u) * pt;
+  const int64_t oa = (p.s.few ? pre : 0) + static_cast<int64_t>(cum[0]) * p.s.heads +
+                     static_cast<int64_t>(h) * tiles;
+  int c[4];
+  owners({pa, pa + pt - 1, oa, oa + tiles - 1}, {ptotal, ototal}, c);
+  if (pt) {
+    x.prefix = c[1] - c[0] + 1;
+    const size_t piece = u + c[0];
+    if (p.s.few) {
+      x.pbase = piece * kFewRows + r0;
+      x.pstep = kFewRows;
+    } else if ((qt | 1) < p.s.nq) {  // a block of two row tiles: a record per tile
+      x.pbase = (piece * 2 + (qt & 1)) * TILE_ROWS + r0;
+      x.pstep = 2 * TILE_ROWS;
+    } else {                         // one row tile: a record per half of the keys
+      x.pbase = piece * 2 * TILE_ROWS + r0;
+      x.pstep = TILE_ROWS;
+      x.prefix *= 2;
+    }
+  }
+  if (tiles) {
+    x.own = c[3] - c[2] + 1;
+    x.obase = static_cast<size_t>(b * p.s.heads + h + c[2]) * p.s.group;
+  }
+  return x;
+}
+
+// Index of record i of row g in its array (the prefix's for i < x.prefix), and its {max, sum}.
+__device__ __forceinline__ size_t record(const AttendParams& p, const Records& x, int i, int g) {
+  return (i < x.prefix ? x.pbase + i * x.pstep
+                       : x.obase + static_cast<size_t>(i - x.prefix) * p.s.group) + g;
+}
+__device__ __forceinline__ float2 record_ml(const AttendParams& p, const Records& x, int i, int g) {
+  return (i < x.prefix ? p.w.pml : p.w.tml)[record(p, x, i, g)];
+}
+
+// Adds a record to {m, l}.
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2);
+  if (top != -INFINITY)
+    l = l * ex2(m - top) + l2 * ex2(m2 - top);
+  else
+    l += l2;  // a NaN sum stays one
+  m = top;
 }
 #endif  // __CUDACC__
 
