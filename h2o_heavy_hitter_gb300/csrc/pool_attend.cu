@@ -737,7 +737,8 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ joining the pieces
 constexpr int kFinishWarps = 4, kFinishThreads = 32 * kFinishWarps;
 
-// place_records by a warp: the four divisions run in as many lanes.
+// place_records by L adjacent lanes: the four divisions run in as many of them.
+template <int L>
 __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int h, int plen,
                                               const int (&cum)[3], int lane) {
   return place_records(p, b, h, plen, cum, [&](const int64_t (&at)[4], const int64_t (&total)[2], int (&c)[4]) {
@@ -745,28 +746,30 @@ __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int 
     const int64_t n = lane < 2 ? total[0] : total[1];
     const int mine = n > 0 ? owner(x, n, p.s.grid) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __shfl_sync(0xffffffffu, mine, i);
+    for (int i = 0; i < 4; ++i) c[i] = __shfl_sync(0xffffffffu, mine, i, L);
   });
 }
 
-// A warp's lse (base 2) of row g, the same bits wherever it is computed; `first`:
-// the maximum of record `lane`.
+// The lse (base 2) of row g by L adjacent lanes (all groups of a warp at once), the
+// same bits in every block; `first`: the maximum of record `lane`.
+template <int L>
 __device__ __forceinline__ float row_lse(const AttendParams& p, const Records& x, int g, int lane,
                                          float& first) {
   const int all = x.prefix + x.own;
   float m = -INFINITY, l = 0.f;
   first = -INFINITY;
-  for (int i = lane; i < all; i += 32) {
+#pragma unroll 2
+  for (int i = lane; i < all; i += L) {
     const float2 y = record_ml(p, x, i, g);
-    if (i < 32) first = y.x;
+    if (i < L) first = y.x;
     join(m, l, y.x, y.y);
   }
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
+  for (int off = L / 2; off; off >>= 1) {
     const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
     join(m, l, mo, lo);
   }
-  return __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0);
+  return __shfl_sync(0xffffffffu, all ? m + log2f(l) : -INFINITY, 0, L);
 }
 
 // Scores of a prefix with few rows, from their logits, rows in order: a block per
@@ -778,16 +781,16 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
   const int h = block / per_head, j = ((block - h * per_head) * kFinishThreads + threadIdx.x) * 4;
   const int plen = max(0, checked_length(v, p.a.prefix, false));
   if ((block - h * per_head) * kFinishThreads * 4 >= plen) return;
-  const int rows = p.s.n * p.s.group, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < rows; i += kFinishWarps) {
-    const int b = i / p.s.group;
+  // eight lanes a row (a warp a row, of 16 rows, took 6 us longer over 32 heads of 32768 keys)
+  const int rows = p.s.n * p.s.group, lane = threadIdx.x & 7;
+  for (int i0 = 0; i0 < rows; i0 += kFinishThreads / 8) {
+    const int i = i0 + (threadIdx.x >> 3), b = min(i, rows - 1) / p.s.group;
     const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
     float first;
+    const float x = row_lse<8>(p, records_of<8>(p, b, h, plen, cum, lane), min(i, rows - 1) - b * p.s.group,
+                               lane, first);
     // +inf: not counted, whatever its logits are
-    const float x = p.w.seq[b] < 0
-                        ? INFINITY
-                        : row_lse(p, records_of(p, b, h, plen, cum, lane), i - b * p.s.group, lane, first);
-    if (lane == 0) s_lse[i] = x;
+    if (lane == 0 && i < rows) s_lse[i] = p.w.seq[b] < 0 ? INFINITY : x;
   }
   __syncthreads();
   if (j >= plen) return;
@@ -833,11 +836,11 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
   int len = 0;
   if (seq >= 0) {
     len = v.meta[2 * seq];
-    const Records x = records_of(p, b, h, plen, cum, lane);
+    const Records x = records_of<32>(p, b, h, plen, cum, lane);
     const int all = x.prefix + x.own;
     for (int g = sub; g < group; g += unit_warps) {
       float first;
-      const float lse = row_lse(p, x, g, lane, first);
+      const float lse = row_lse<32>(p, x, g, lane, first);
       if (lane == 0) s_lse[local][g] = lse;
       if (chunk) continue;
       float acc[D / 32] = {};
