@@ -411,14 +411,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 
   if (warp == 0) {
     if constexpr (F8)
-      produce_codes<D>(v, &tk, v.kscale, sK, kscales, bars->keys, TileCursor(w));
+      produce_codes<D, true>(v, &tk, v.kscale, sK, kscales, bars->keys, TileCursor(w));
     else
-      produce_tma<D>(v, &tk, sK, bars->keys, TileCursor(w));
+      produce_tma<D, true>(v, &tk, sK, bars->keys, TileCursor(w));
   } else if (warp == kWarpV) {
     if constexpr (F8)
-      produce_codes<D>(v, &tv, v.vscale, codes, cscales, bars->codes, TileCursor(w));
+      produce_codes<D, true>(v, &tv, v.vscale, codes, cscales, bars->codes, TileCursor(w));
     else
-      produce_tma<D>(v, &tv, sV, bars->values, TileCursor(w));
+      produce_tma<D, true>(v, &tv, sV, bars->values, TileCursor(w));
   } else if (F8 && warp >= kWarpCodes) {
     convert_values<D, RV, C::S, kCodeThreads>(v, codes, cscales, bars->codes, sV, bars->values, vscales,
                                               TileCursor(w), threadIdx.x - 32 * kWarpCodes);
