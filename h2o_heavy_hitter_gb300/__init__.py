@@ -424,8 +424,8 @@ def _list_ptr(pool: H2OPool, seqs, name: str = "seqs", n: int | None = None) -> 
 
 def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
     """Zero-copy torch views of a pool's arrays (library-owned memory, which they keep until
-    the pool is closed): of one layer, or of all with a leading dimension of layers. K and V are bf16, or uint8 E4M3 codes
-    with "kscale" and "vscale" in an "fp8" pool."""
+    the pool is closed): of one layer, or of all with a leading dimension of layers. K and V
+    are bf16, or uint8 E4M3 codes with "kscale" and "vscale" in an "fp8" pool."""
     ptrs = [ctypes.c_void_p() for _ in range(9)]
     _check(load_library().h2o_pool_view(pool.handle, layer or 0, *[ctypes.byref(p) for p in ptrs]))
     lead = (pool.layers,) if layer is None else ()
@@ -466,15 +466,17 @@ def h2o_pool_write(pool: H2OPool, layer: int, seqs, K, V, lens=None, score=None)
 def h2o_pool_fork(pool: H2OPool, layer: int, src, dst) -> None:
     """Makes the empty sequences dst continuations of src that share their whole pages
     (layer -1: in every layer)."""
+    a = _list_ptr(pool, src, "src")
     n = len(src)
-    a, b = _list_ptr(pool, src, "src"), _list_ptr(pool, dst, "dst", n)
+    b = _list_ptr(pool, dst, "dst", n)
     _check(load_library().h2o_pool_fork(pool.handle, layer, n, a, b))
 
 
 def h2o_pool_copy(pool: H2OPool, layer: int, src, dst) -> None:
     """h2o_pool_fork that copies every page instead of sharing the whole ones."""
+    a = _list_ptr(pool, src, "src")
     n = len(src)
-    a, b = _list_ptr(pool, src, "src"), _list_ptr(pool, dst, "dst", n)
+    b = _list_ptr(pool, dst, "dst", n)
     _check(load_library().h2o_pool_copy(pool.handle, layer, n, a, b))
 
 

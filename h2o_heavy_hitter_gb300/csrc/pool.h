@@ -31,9 +31,9 @@ struct PoolView {
 constexpr int kPoolMaxList = 1024;  // longest list of sequences of one call: one thread each
 constexpr int kPoolMaxGroup = 32;   // query heads per key head: the own rows of a sequence fit one warp
 
-// Fresh pages are found and the sequences' tables changed by one block per
-// layer ("plan"); a second kernel then moves the tokens. `fresh` (scratch) has
-// room for every page the call can ask for, per layer; `plan` (scratch) for
+// Fresh pages are found by one block per layer ("plan"), which fork, copy and write
+// let change the tables too; a second kernel then moves the tokens. `fresh` (scratch)
+// has room for every page the call can ask for, per layer; `plan` (scratch) for
 // kPlanInts ints per layer and list entry.
 constexpr int kPlanInts = 4;
 
@@ -43,7 +43,7 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
                       bool share, int32_t* fresh, int32_t* plan, cudaStream_t stream);
 cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
                       cudaStream_t stream);
-// Appends lens[i] (or T) tokens to sequence seqs[i] of one layer. fresh: n * pages of T tokens + 1.
+// Appends lens[i] (or T) tokens to sequence seqs[i] of one layer. fresh: n * ceil(T / page).
 cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void* K, const void* V,
                        int T, const int32_t* lens, const float* score, int32_t* fresh,
                        int32_t* plan, cudaStream_t stream);

@@ -20,13 +20,24 @@
 //   thread per channel. (With rows as the wide side, 128 lanes of which 1 to 8
 //   were used, the issue of both products and the read-out of the accumulator
 //   took 2.9 us a tile against 1.5 us for its bytes.) Units alternate between two
-//   warpgroups, so the end of one overlaps the beginning of the next.
+//   warpgroups, so the end of one overlaps the beginning of the next. 256
+//   sequences of 300 to 410 tokens, 32 heads of 128: 1.56 GB in 233 us (6.7 TB/s);
+//   16 rows a head over 32768 tokens and the own ones: 0.70 GB in 120 us.
 // pool_prefix_kernel, pool_prefix_score_kernel (pool_prefix.cu) take a prefix with
 //   more rows.
 // pool_finish_kernel joins the pieces of each row in fixed order and adds the
 //   probabilities to the scores, from the logits that the first kernel left (4
 //   bytes per key and row, against 4 d of keys and values).
-// P is rounded to bf16, the operand type of the second product; logits, sums and
+//
+// E4M3 pools: the codes of keys are matrix operands as they are, against queries
+// split into two codes a value (pool_split_queries_kernel), with the key's and the
+// row's scale applied to the logit; converting keys to bf16 too took 115 us where
+// this took 110. Codes of values become bf16 in shared memory, by eight warps of
+// their own, and their scales go into P. Bound by the work on a tile, not by its
+// bytes: 64 sequences of up to 1000 tokens, 8 heads, 4 query heads each: 74 MB in 35 us.
+//
+// P is rounded to bf16, the operand type of the second product, whose exponent
+// reaches as far as fp32's (a value's scale is in it); logits, sums and
 // accumulators are fp32. What lies behind a sequence's end in its last page is
 // not trusted: its probabilities are set to zero, and its values in shared
 // memory too, since 0 times a NaN is not 0.
@@ -813,9 +824,11 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
 }
 
 // Per (entry, key head) and chunk of keys, one to four warps by the size of the
-// group: join the rows, a warp each, in the order of the pieces, and add the
-// probabilities of the own tokens to their scores. Every chunk computes the lse's
-// it needs, chunk 0 writes. `blocks` * `chunks` such blocks, then those of the prefix's scores.
+// group (unit_warps; a row each at a time): join the rows, a warp each, in the order of
+// the pieces, and add the probabilities of the own tokens to their scores. Every
+// chunk computes the lse's it needs, chunk 0 writes. `blocks` * `chunks` such blocks,
+// then those of the prefix's scores. Latency-bound: the lengths, the records, then
+// the outputs are loads behind one another; 8192 rows take 20 us, 4 rows 6.
 template <int D>
 __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_warps, int blocks, int chunks,
                                              float (&s_lse)[kFinishWarps][kFewRows]) {

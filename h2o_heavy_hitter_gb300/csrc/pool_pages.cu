@@ -249,7 +249,9 @@ __device__ __forceinline__ void copy_slots(const PoolView& v, int to, int from, 
 
 // LANES threads per (entry, head, slab of kSlab slots): the slab's scores, and the
 // tokens of its pages that were not shared. A head's slots of a page are
-// contiguous, so a partial page is one run of bytes per head.
+// contiguous, so a partial page is one run of bytes per head. Bound by the writes: 56
+// forks of 8 prompts of 200 tokens, 48 layers of 56 heads, 1.1 GB in 207 us, each
+// source read from HBM once. (Stores that leave L2 first made that 250 us.)
 constexpr int kSlab = 1024;
 
 template <int LANES>
@@ -374,7 +376,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // kWriteTokens tokens per block, of one (entry, head) or, where calls write few
 // tokens (a step's), of several: 1 << span tokens of each. Eight lanes per token,
-// each D / 8 values of its key and of its value.
+// each D / 8 values of its key and of its value. Bound by HBM: 8 prompts of up to 2048
+// tokens, 32 heads of 128, 0.47 GB in 69 us. (A step of 256 sequences x 32 heads: 14.3
+// us with its plan, 22.5 with a block per entry and head.)
 constexpr int kWriteTokens = 32;
 // 448 / amax overflows below 448 / FLT_MAX (just above 2^-120): such vectors are stored as zero.
 constexpr float kTinyVector = 0x1p-119f;
@@ -457,7 +461,8 @@ constexpr int kSelectKeys = 44 * 1024;  // scores whose keys are held in shared 
 constexpr int kDigit = 11;              // bits of a radix step: 3 steps
 // Copies of the histogram, by lane: scores crowd in few exponents, and a warp's
 // additions to one word run one after the other (78 us for 128 rows of 32768 with
-// steps of 8 bits from global memory, 33 us with all this).
+// steps of 8 bits from global memory, 33 us with all this). Bound by these steps and
+// the block's barriers between them, not by the row's 4 bytes a token.
 constexpr int kHists = 4;
 
 // Blocks (head, entry, layer) select; the block with head == heads of entry 0
@@ -611,8 +616,9 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
 }
 
 // One warp per kGather kept slots of a head: all loads of a lane are in flight
-// before its stores. The first block of an entry also puts the new pages in the table
-// and drops the old ones, which the gather does not read again.
+// before its stores. Bound by HBM: 4096 of 32768 tokens of 128 heads, 0.54 GB in 86
+// us. The first block of an entry also puts the new pages in the table and drops the
+// old ones, which the gather does not read again.
 constexpr int kGather = 4;
 
 template <int ROW>

@@ -10,11 +10,14 @@
 //   and no maximum is exchanged; with two, the halves take a row tile each and
 //   share the key and value tiles. S is double-buffered: the product of the next
 //   tile runs under the softmax of this one. Bound by HBM up to some 128 rows,
-//   beyond by the exponentials and the products of 256 rows a tile.
-// pool_prefix_score_kernel: the prefix's scores once every row's lse is known: S^T
-//   = K Q^T again, a thread per key, p = 2^(s - lse) summed over all rows in
-//   order. It reads K once more (2 d bytes a key and head); keeping the logits of
-//   more than 32 rows would move 8 bytes a key and row.
+//   beyond by the exponentials and the products of 256 rows a tile: 512 rows a
+//   head, 8 heads, 32768 keys take 94 us with the joining (730 TFLOP/s). At 1024
+//   keys a CTA has two tiles, and 17 us are its start and the read-out.
+// pool_prefix_score_kernel: the prefix's scores once the pieces are there: S^T = K
+//   Q^T again, a thread per key, p = 2^(s - lse) summed over all rows in order. It
+//   reads K once more (2 d bytes a key and head); keeping the logits of more than
+//   32 rows would move 8 bytes a key and row. For up to 256 rows it joins the rows'
+//   sums itself and runs beside the finish kernel (256 sequences: 290 -> 286 us in all).
 #include "device_state.h"
 #include "pool_tiles.cuh"
 

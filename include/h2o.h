@@ -525,8 +525,11 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  * -infinity. Rows of skipped entries keep what they held.
  *
  * q: device bf16 [n][q_heads][d]; out: device bf16 [n][q_heads][d]; lse: device
- * fp32 [n][q_heads]; q and out 16-byte aligned; the three must not overlap. q_heads is a multiple of H, at
- * most H2O_POOL_MAX_GROUP times. `prefix` in `seqs` is a bad entry.
+ * fp32 [n][q_heads]; q and out 16-byte aligned; the three must not overlap.
+ * q_heads is a multiple of H, at most H2O_POOL_MAX_GROUP times. `prefix` in `seqs`
+ * is a bad entry. With accumulate the call's scratch holds 4 bytes per query row
+ * and slot of a longest sequence, 4 n q_heads C (twice that for a prefix with at
+ * most 32 rows a head).
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
 int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int prefix,
