@@ -188,6 +188,19 @@ def test_attend_many_tiles(heads, group, d, page, batch, longest, prefix, kv):
     b.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads,group,batch,prefix", [(700, 1, 36, 100), (330, 3, 47, 70)])
+def test_attend_many_heads_to_a_share(heads, group, batch, prefix, kv):
+    """More heads than SMs: a share of the prefix's tiles passes through several heads."""
+    lens = [(7 * i) % 23 for i in range(batch)] + [prefix]
+    b = Both(batch + 8, 32, heads, 64, batch + 1, 4, kv, seed=heads)
+    b.write(range(batch + 1), prefix, lens)
+    for _ in range(2):
+        b.attend(range(batch), heads * group, prefix=batch)
+        b.check()
+    b.close()
+
+
 def test_attend_ignores_what_lies_behind_a_sequence():
     """NaN and infinities in the slots behind the last token, of the prefix too."""
     b = Both(pages=12, page=32, heads=2, d=64, sequences=3, max_pages=4)
