@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
+  // beside the prefix kernel, which waited for what came before it, this one waits at its end
+  if (p.a.prefix < 0 || p.s.few) grid_dependency_wait();
   if (threadIdx.x == 0) {
     for (int i = 0; i < RK; ++i) {
       mbar_init(&bars->keys.full[i], 1);
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         (w.prefix ? p.w.pml : p.w.tml)[rec + lane] = make_float2(m, l);
     }
   }
-  // a kernel for a prefix with many rows may still run: what follows waits for both
+  // the prefix kernel may still run: what follows waits for both
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
@@ -702,6 +704,8 @@ __global__ void __launch_bounds__(256)
     pool_split_queries_kernel(const __nv_bfloat16* __restrict__ q, int rows, uint8_t* q8, float* qfac) {
   constexpr int N = D / 32;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (row >= rows) return;
   uint32_t raw[N / 2];
   if constexpr (N == 4)
@@ -988,9 +992,9 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
   cudaError_t e;
   if (F8) {
     const int rows = p.s.n * p.s.heads * p.s.group;
-    pool_split_queries_kernel<D><<<(rows + 7) / 8, 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(p.a.q), rows, p.w.q8, p.w.qfac);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(pool_split_queries_kernel<D>, dim3((rows + 7) / 8), 256, 0, stream,
+                          static_cast<const __nv_bfloat16*>(p.a.q), rows, p.w.q8, p.w.qfac)) != cudaSuccess)
+      return e;
     if ((e = query_code_map(&t1, p, 0, 1)) != cudaSuccess) return e;
     if ((e = query_code_map(&t2, p, 1, 1)) != cudaSuccess) return e;
   } else {
@@ -1011,15 +1015,9 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(pool_rows_kernel<D, F8>), C::SMEM,
                             opted_in)) != cudaSuccess)
     return e;
-  if (many) {
-    e = launch_after(pool_rows_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream, tq, t1,
-                     tq2, t2, tk, tv, p);
-  } else {
-    pool_rows_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, t1, tq2, t2, tk, tv,
-                                                                            p);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess) return e;
+  if ((e = launch_after(pool_rows_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream, tq, t1, tq2,
+                        t2, tk, tv, p)) != cudaSuccess)
+    return e;
   const int unit_warps = p.s.group >= 4 ? 4 : p.s.group >= 2 ? 2 : 1, units = p.s.n * p.s.heads;
   const int blocks = (units * unit_warps + kFinishWarps - 1) / kFinishWarps;
   // enough chunks of keys for the scores of few long rows

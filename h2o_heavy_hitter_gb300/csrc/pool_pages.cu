@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.x) * fresh_stride;
   int32_t* plan = plan_all + static_cast<size_t>(blockIdx.x) * n * kPlanInts;
   const int i = threadIdx.x;
+  grid_dependency_wait();
   grid_launch_dependents();
   int to = list_entry(v, dst, n, s_list);
   const int from = i < n ? src[i] : -1;
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(256)
   const int task = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const int e = task / v.heads, head = task % v.heads;
   grid_dependency_wait();
+  grid_launch_dependents();
   if (e >= n || !plan[e * kPlanInts]) return;
   const int len = plan[e * kPlanInts + 1], lo = blockIdx.y * kSlab, hi = min(len, lo + kSlab);
   if (lo >= hi) return;
@@ -283,6 +285,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     free_kernel(PoolView v0, int n, const int32_t* __restrict__ seqs) {
   __shared__ int s_list[kPlanThreads], s_len[kPlanThreads];
   const PoolView v = at_layer(v0, blockIdx.x);
+  grid_dependency_wait();
+  grid_launch_dependents();
   int seq = list_entry(v, seqs, n, s_list), len = 0;
   if (seq >= 0 && (len = seq_length(v, seq)) < 0) seq = -1;
   __syncthreads();  // every thread has compared the list
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       s_first[kPlanThreads];
   __shared__ int wsum[33];
   const int i = threadIdx.x;
+  grid_dependency_wait();
   grid_launch_dependents();
   int seq = list_entry(v, seqs, n, s_list);
   __syncthreads();
@@ -394,6 +399,7 @@ __global__ void __launch_bounds__(256)
   const int t = blockIdx.y * kWriteTokens + (token & ((1 << span) - 1));
   const int e = unit / v.heads, head = unit - e * v.heads;
   grid_dependency_wait();
+  grid_launch_dependents();
   if (e >= n || t >= plan[e * kPlanInts]) return;  // whole groups of eight lanes leave together
   const unsigned gmask = 0xffu << (threadIdx.x & 31 & ~(LPT - 1));
   const int seq = seqs[e], slot = plan[e * kPlanInts + 1] + t;
@@ -481,6 +487,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   const PoolView v = at_layer(v0, blockIdx.z);
   const int k = h + r, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int wsum[33];
+  grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == static_cast<unsigned>(v.heads)) {
     if (blockIdx.y) return;
@@ -633,6 +640,7 @@ __global__ void __launch_bounds__(256)
   const PoolView v = at_layer(v0, blockIdx.z);
   const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
   grid_dependency_wait();
+  grid_launch_dependents();
   const int first = plan_all[(static_cast<size_t>(blockIdx.z) * n + e) * kPlanInts];
   if (first < 0) return;
   const int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.z) * fresh_stride + first;
@@ -690,9 +698,8 @@ __global__ void __launch_bounds__(256)
 cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, const int32_t* dst,
                       bool share, int32_t* fresh, int32_t* plan, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
-  fork_plan_kernel<<<layers, kPlanThreads, 0, stream>>>(v, n, src, dst, share, fresh,
-                                                        share ? n : n * v.width, plan);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(fork_plan_kernel, dim3(layers), kPlanThreads, 0, stream, v, n, src, dst,
+                               share, fresh, share ? n : n * v.width, plan);
   if (e != cudaSuccess) return e;
   // a warp per task where the tasks fill the GPU, else a block: 32 heads x 4
   // entries of some 50 tokens take 7.6 us by blocks, 19.4 us by warps; scores of
@@ -708,16 +715,15 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
 cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
                       cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
-  free_kernel<<<layers, kPlanThreads, 0, stream>>>(v, n, seqs);
-  return cudaGetLastError();
+  return launch_after(free_kernel, dim3(layers), kPlanThreads, 0, stream, v, n, seqs);
 }
 
 cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void* K, const void* V,
                        int T, const int32_t* lens, const float* score, int32_t* fresh,
                        int32_t* plan, cudaStream_t stream) {
   if (n == 0 || T == 0) return cudaSuccess;
-  write_plan_kernel<<<1, kPlanThreads, 0, stream>>>(v, n, seqs, T, lens, fresh, plan);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      launch_after(write_plan_kernel, dim3(1), kPlanThreads, 0, stream, v, n, seqs, T, lens, fresh, plan);
   if (e != cudaSuccess) return e;
   int span = 0;
   while (1 << span < kWriteTokens && 1 << span < T) ++span;
@@ -743,9 +749,9 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(compact_select_kernel),
                                    kSelectKeys * sizeof(unsigned), opted_in);
   if (e != cudaSuccess) return e;
-  compact_select_kernel<<<dim3(v.heads + 1, n, layers), kSelectThreads, held * sizeof(unsigned),
-                          stream>>>(v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(compact_select_kernel, dim3(v.heads + 1, n, layers), kSelectThreads,
+                   held * sizeof(unsigned), stream, v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
+  if (e != cudaSuccess) return e;
   const dim3 grid(n * v.heads, (k + 8 * kGather - 1) / (8 * kGather), layers);
   auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>
               : v.row_bytes == 128 ? compact_gather_kernel<128> : compact_gather_kernel<64>;

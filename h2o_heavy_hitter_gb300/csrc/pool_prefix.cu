@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
+  grid_dependency_wait();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
@@ -789,8 +790,8 @@ cudaError_t prefix_t(const AttendParams& p, cudaStream_t stream) {
   if ((e = raise_smem_limit(reinterpret_cast<const void*>(pool_prefix_kernel<D, F8>), C::SMEM,
                             opted_in)) != cudaSuccess)
     return e;
-  pool_prefix_kernel<D, F8><<<p.s.grid, C::THREADS, C::SMEM, stream>>>(tq, tq2, tk, tv, p);
-  return cudaGetLastError();
+  return launch_after(pool_prefix_kernel<D, F8>, dim3(p.s.grid), C::THREADS, C::SMEM, stream, tq, tq2, tk,
+                      tv, p);
 }
 
 template <int D, bool F8>
