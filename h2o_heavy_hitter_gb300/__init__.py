@@ -416,10 +416,14 @@ def _ptr(pool: H2OPool, t, dtype: torch.dtype, shape: tuple, name: str) -> int:
     return _dev_ptr(t, dtype, shape, name)
 
 
-def _list_ptr(pool: H2OPool, seqs, name: str = "seqs", n: int | None = None) -> int:
-    if isinstance(seqs, torch.Tensor) and seqs.dim() != 1:
-        raise ValueError(f"{name} must have one dimension, got {tuple(seqs.shape)}")
-    return _ptr(pool, seqs, torch.int32, (len(seqs) if n is None else n,), name)
+def _list_ptr(pool: H2OPool, seqs, name: str = "seqs") -> tuple[int, int]:
+    """Address and length of a sequence list."""
+    if not isinstance(seqs, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = seqs.shape
+    if len(shape) != 1:
+        raise ValueError(f"{name} must have one dimension, got {tuple(shape)}")
+    return _ptr(pool, seqs, torch.int32, shape, name), shape[0]
 
 
 def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
@@ -451,10 +455,10 @@ def h2o_pool_view(pool: H2OPool, layer: int | None = None) -> dict:
 def h2o_pool_write(pool: H2OPool, layer: int, seqs, K, V, lens=None, score=None) -> None:
     """Appends tokens to sequences: bf16 K, V [n, H, T, d], the first lens[i] (CUDA int32 [n];
     default T) of entry i, with initial scores fp32 [n, H, T] (default 0)."""
-    ps = _list_ptr(pool, seqs)
+    ps, n = _list_ptr(pool, seqs)
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
         raise ValueError("K must be a tensor [n, heads, T, head_dim]")
-    n, T = len(seqs), K.shape[2]
+    T = K.shape[2]
     shape = (n, pool.heads, T, pool.head_dim)
     pk = _ptr(pool, K, torch.bfloat16, shape, "K")
     pv = _ptr(pool, V, torch.bfloat16, shape, "V")
@@ -466,31 +470,29 @@ def h2o_pool_write(pool: H2OPool, layer: int, seqs, K, V, lens=None, score=None)
 def h2o_pool_fork(pool: H2OPool, layer: int, src, dst) -> None:
     """Makes the empty sequences dst continuations of src that share their whole pages
     (layer -1: in every layer)."""
-    a = _list_ptr(pool, src, "src")
-    n = len(src)
-    b = _list_ptr(pool, dst, "dst", n)
+    a, n = _list_ptr(pool, src, "src")
+    b = _ptr(pool, dst, torch.int32, (n,), "dst")
     _check(load_library().h2o_pool_fork(pool.handle, layer, n, a, b))
 
 
 def h2o_pool_copy(pool: H2OPool, layer: int, src, dst) -> None:
     """h2o_pool_fork that copies every page instead of sharing the whole ones."""
-    a = _list_ptr(pool, src, "src")
-    n = len(src)
-    b = _list_ptr(pool, dst, "dst", n)
+    a, n = _list_ptr(pool, src, "src")
+    b = _ptr(pool, dst, torch.int32, (n,), "dst")
     _check(load_library().h2o_pool_copy(pool.handle, layer, n, a, b))
 
 
 def h2o_pool_free(pool: H2OPool, layer: int, seqs) -> None:
     """Empties sequences (layer -1: in every layer); pages that nobody holds are free again."""
-    ps = _list_ptr(pool, seqs)
-    _check(load_library().h2o_pool_free(pool.handle, layer, len(seqs), ps))
+    ps, n = _list_ptr(pool, seqs)
+    _check(load_library().h2o_pool_free(pool.handle, layer, n, ps))
 
 
 def h2o_pool_compact(pool: H2OPool, layer: int, seqs, h: int, r: int) -> None:
     """Keeps the r last tokens and the h others of largest score of every head of each
     sequence longer than h + r (layer -1: in every layer)."""
-    ps = _list_ptr(pool, seqs)
-    _check(load_library().h2o_pool_compact(pool.handle, layer, len(seqs), ps, h, r))
+    ps, n = _list_ptr(pool, seqs)
+    _check(load_library().h2o_pool_compact(pool.handle, layer, n, ps, h, r))
 
 
 def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=None, lse=None,
@@ -499,10 +501,10 @@ def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=No
     ``prefix`` (shared by the batch; -1: none) and each sequence's own. Returns (out bf16
     [n, q_heads, d], lse fp32 [n, q_heads]); with ``accumulate`` the probabilities are added to
     the accumulated scores. Rows of -1 entries are not written."""
-    ps = _list_ptr(pool, seqs)
+    ps, n = _list_ptr(pool, seqs)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [n, q_heads, head_dim]")
-    n, heads = len(seqs), q.shape[1]
+    heads = q.shape[1]
     shape = (n, heads, pool.head_dim)
     pq = _ptr(pool, q, torch.bfloat16, shape, "q")
     if out is None:
