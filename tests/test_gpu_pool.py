@@ -442,6 +442,73 @@ def test_calls_on_another_stream_and_in_a_graph():
     b.close()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("batch", [3, 40, 90])  # narrow rows, one row tile of the prefix, three
+def test_a_captured_step_behind_copies_and_joined_streams(kv, batch):
+    """Every call of a captured graph behind a copy, a fill and a join of two streams."""
+    import h2o_heavy_hitter_gb300 as h2o
+    heads, group = 3, 3
+    b = Both(pages=5 * batch + 30, page=16, heads=heads, d=128, sequences=batch + 2, max_pages=20, kv=kv, seed=batch)
+    b.write(range(batch + 1), 290, [(13 * i) % 37 for i in range(batch)] + [290])
+    k64, k = bf16(b.tokens(batch, 1))
+    v64, v = bf16(b.tokens(batch, 1))
+    q64, q = bf16(b.queries(batch, heads * group))
+    k_in, v_in, q_in = torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(q)
+    seqs, some, sink = ints(range(batch)), ints([batch]), ints([batch + 1])
+    out = torch.zeros_like(q)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        k_in.copy_(k)
+        v_in.copy_(v)
+        h2o.h2o_pool_write(b.pool, 0, seqs, k_in, v_in)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q_in.copy_(q)
+            lse.fill_(3.0)
+        out.zero_()
+        main.wait_stream(side)
+        h2o.h2o_pool_attend(b.pool, 0, seqs, q_in, prefix=batch, out=out, lse=lse)
+        h2o.h2o_pool_free(b.pool, 0, sink)
+        h2o.h2o_pool_fork(b.pool, 0, some, sink)
+        k_in.zero_()
+        v_in.zero_()
+        h2o.h2o_pool_compact(b.pool, 0, sink, 30, 9)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q_in.zero_()
+        main.wait_stream(side)
+
+    def oracle_step():
+        b.oracle.write(range(batch), k64, v64)
+        want = b.oracle.attend(range(batch), q64, batch)
+        b.oracle.free([batch + 1])
+        b.oracle.fork([batch], [batch + 1])
+        b.oracle.compact([batch + 1], 30, 9)
+        return want
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    oracle_step()
+    b.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        graph.replay()
+        want, want_lse = oracle_step()
+        size = np.abs(b.oracle.V).max()  # the tolerances of Both.attend
+        assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * (size + np.abs(want)) + 1e-3 * size)
+        assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= 1e-4)
+    b.check()
+    b.close()
+
+
 def test_two_graphs_and_eager_calls_on_streams_of_their_own():
     """Layers are independent: graphs of two layers and eager calls on a third run at once and
     leave what they leave one after the other."""
