@@ -622,11 +622,11 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   }
 }
 
-// One warp per kGather kept slots of a head: all loads of a lane are in flight
+// One warp per 1 KB of keys of a head's kept slots: all loads of a lane are in flight
 // before its stores. Bound by HBM: 4096 of 32768 tokens of 128 heads, 0.54 GB in 86
 // us. The first block of an entry also puts the new pages in the table and drops the
 // old ones, which the gather does not read again.
-constexpr int kGather = 4;
+constexpr int gather_slots(int row) { return 1024 / row; }
 
 template <int ROW>
 __global__ void __launch_bounds__(256)
@@ -634,9 +634,10 @@ __global__ void __launch_bounds__(256)
                           const int32_t* fresh_all, int fresh_stride,
                           const int32_t* plan_all, const int32_t* where,
                           const float* kept) {
+  constexpr int SLOTS = gather_slots(ROW);
   constexpr int CH = ROW / 16;                     // 16-byte chunks of a vector
   constexpr int PER = 2 * CH;                      // chunks of a slot: key, then value
-  constexpr int NC = (PER * kGather + 31) / 32;    // chunks per lane
+  constexpr int NC = (PER * SLOTS + 31) / 32;    // chunks per lane
   const PoolView v = at_layer(v0, blockIdx.z);
   const int e = blockIdx.x / v.heads, head = blockIdx.x % v.heads;
   grid_dependency_wait();
@@ -658,14 +659,14 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0) v.meta[2 * seq] = k;
   }
   const size_t in = ((static_cast<size_t>(blockIdx.z) * n + e) * v.heads + head) * k;
-  const int slot0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kGather;
+  const int slot0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * SLOTS;
   uint4 x[NC];
   uint8_t* dst[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = lane + 32 * i, slot = slot0 + c / PER;
     dst[i] = nullptr;
-    if (c >= PER * kGather || slot >= k) continue;
+    if (c >= PER * SLOTS || slot >= k) continue;
     const int w = where[in + slot];
     if (w < 0) continue;
     const int at = c % PER, kv = at >= CH, byte = (kv ? at - CH : at) * 16;
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < NC; ++i)
     if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = x[i];
   const int slot = slot0 + lane;
-  if (lane < kGather && slot < k) {
+  if (lane < SLOTS && slot < k) {
     v.score[(static_cast<size_t>(seq) * v.heads + head) * v.cap + slot] = kept[in + slot];
     const int w = where[in + slot];
     if (w >= 0) {
@@ -752,7 +753,8 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
   e = launch_after(compact_select_kernel, dim3(v.heads + 1, n, layers), kSelectThreads,
                    held * sizeof(unsigned), stream, v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
   if (e != cudaSuccess) return e;
-  const dim3 grid(n * v.heads, (k + 8 * kGather - 1) / (8 * kGather), layers);
+  const int slots = 8 * gather_slots(v.row_bytes);  // per block
+  const dim3 grid(n * v.heads, (k + slots - 1) / slots, layers);
   auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>
               : v.row_bytes == 128 ? compact_gather_kernel<128> : compact_gather_kernel<64>;
   return launch_after(kern, grid, 256, 0, stream, v, n, seqs, k, static_cast<const int32_t*>(fresh),
