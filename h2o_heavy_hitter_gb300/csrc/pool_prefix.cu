@@ -503,7 +503,10 @@ struct ScoreBars {
   uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
   uint64_t joined;                // a phase per head of the share
   uint32_t tmem;
-  float nlse[2][2 * TILE_ROWS];   // [heads & 1] of a head's rows (score_joins)
+  // -lse [0] and the scale of the codes [1] of rows, which all lanes read at once: of a head's
+  // rows, by heads & 1 (score_joins), or of the 32 rows that a warp has at hand
+  alignas(16) float rows[2][2][2 * TILE_ROWS];
+  alignas(16) float some[2][8][32];
 };
 
 // Warps as above, 4..7 even key tiles, 8..11 odd ones.
@@ -538,6 +541,11 @@ struct KeyCursor {
   __device__ bool last_of_head() const { return it + 1 >= end || kt + 1 == tiles; }
 };
 
+// E4M3: what the codes of an entry's query row are to be multiplied by.
+__device__ __forceinline__ float row_factor(const AttendParams& p, int entry, int h, int g) {
+  return p.w.qfac[(static_cast<size_t>(entry) * p.s.heads + h) * p.s.group + g];
+}
+
 // -lse (base 2) of row r of a head's row tile qt, -inf for one that is not counted.
 __device__ __noinline__ float joined_row(const AttendParams& p, int qt, int r, int h, int len) {
   const int b = qt * p.s.per_tile + r / p.s.group, g = r % p.s.group;
@@ -567,11 +575,16 @@ __device__ __noinline__ float joined_row(const AttendParams& p, int qt, int r, i
   return -(m + log2f(l));
 }
 
+// Fewer registers than THREADS threads could have (112 at most), so that three blocks of
+// the finish kernel fit beside a CTA: grouped E4M3 heads 75.9 us a call, with 162 registers
+// 84.4, with 80 and spills 77.9.
+constexpr int kScoreBound = 576;
+
 // The row tiles of a head stay in shared memory when there are at most two; more
 // are fetched again for every key tile. A fill is one load of a row tile: fill f
 // lies in buffer f & 1.
 template <int D, bool F8>
-__global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
+__global__ void __launch_bounds__(kScoreBound, 1)
     pool_prefix_score_kernel(const __grid_constant__ CUtensorMap tq,
                              const __grid_constant__ CUtensorMap tq2,
                              const __grid_constant__ CUtensorMap tk,
@@ -710,7 +723,12 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
     for (uint32_t g = 0; ok && k.step(); ++g) {
       if (stay && last != k.h) {  // half t joins the rows of row tile t, both use them
         // (two buffers: the one written was last read before the other's phase)
-        if (t < nq) bars->nlse[heads & 1][t * TILE_ROWS + r] = joined_row(p, t, r, k.h, len);
+        if (t < nq) {
+          const int entry = t * p.s.per_tile + r / group;
+          const int at = t * TILE_ROWS + r;
+          if (F8) bars->rows[1][heads & 1][at] = entry < p.s.n ? row_factor(p, entry, k.h, r % group) : 1.f;
+          bars->rows[0][heads & 1][at] = joined_row(p, t, r, k.h, len);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->joined);
         if (!pool_warp_wait(&bars->joined, heads & 1, v.err)) break;
@@ -722,8 +740,6 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
       for (int qt = 0; qt < nq; ++qt, ++cnt) {
         const uint32_t buf = 2 * t + (cnt & 1);
         const int rows = min(p.s.per_tile, p.s.n - qt * p.s.per_tile) * group;
-        const float* nl = stay ? bars->nlse[(heads - 1) & 1] + qt * TILE_ROWS
-                               : p.w.nlse + (static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS;
         if (!pool_warp_wait(&bars->s_full[buf], (cnt >> 1) & 1, v.err)) {
           ok = false;
           break;
@@ -740,22 +756,37 @@ __global__ void __launch_bounds__(ScoreCfg<D, F8>::THREADS, 1)
         }
         float part[4] = {0.f, 0.f, 0.f, 0.f};
         for (int c = 0; c < rows; c += 32) {
-          const int row = c + lane;
-          const float mine = row < rows ? nl[row] : -INFINITY;
-          float fac = 1.f;
-          if (F8 && row < rows)
-            fac = p.w.qfac[(static_cast<size_t>(qt * p.s.per_tile + row / group) * p.s.heads + k.h) * group +
-                           row % group];
+          const float* nl = bars->rows[0][(heads - 1) & 1] + qt * TILE_ROWS + c;
+          const float* fac = bars->rows[1][(heads - 1) & 1] + qt * TILE_ROWS + c;
+          if (!stay) {
+            nl = bars->some[0][warp - kWarpSoftmax];
+            fac = bars->some[1][warp - kWarpSoftmax];
+            const int at = c + lane;
+            const bool in = at < rows;
+            const float mine =
+                in ? p.w.nlse[(static_cast<size_t>(k.h) * nq + qt) * TILE_ROWS + at] : -INFINITY;
+            const float mf =
+                F8 && in ? row_factor(p, qt * p.s.per_tile + at / group, k.h, at % group) : 1.f;
+            __syncwarp();
+            bars->some[0][warp - kWarpSoftmax][lane] = mine;
+            if (F8) bars->some[1][warp - kWarpSoftmax][lane] = mf;
+            __syncwarp();
+          }
           uint32_t s[32];
           tmem_ld32(tmem + lane_off + buf * 128 + c, s);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const float n = __shfl_sync(0xffffffffu, mine, x);
-            // rows that are not counted, and columns that are none, may hold anything
-            const float f = F8 ? ks * __shfl_sync(0xffffffffu, fac, x) : ks;
-            const float e = ex2(fmaf(__uint_as_float(s[x]), f, n));
-            part[x & 3] += n == -INFINITY ? 0.f : e;
+          for (int x = 0; x < 32; x += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + x);
+            const float4 f4 =
+                F8 ? *reinterpret_cast<const float4*>(fac + x) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float n[4] = {n4.x, n4.y, n4.z, n4.w}, f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              // rows that are not counted, and columns that are none, may hold anything
+              const float e = ex2(fmaf(__uint_as_float(s[x + y]), F8 ? ks * f[y] : ks, n[y]));
+              part[y] += n[y] == -INFINITY ? 0.f : e;
+            }
           }
         }
         acc += (part[0] + part[1]) + (part[2] + part[3]);
