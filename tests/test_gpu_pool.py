@@ -443,6 +443,53 @@ def test_calls_on_another_stream_and_in_a_graph():
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("batch,heads,group", [(6, 32, 2), (64, 16, 1), (120, 8, 2), (70, 8, 5)])
+def test_calls_back_to_back_equal_synchronised_ones(batch, heads, group, kv):
+    """Launches that begin while the one before drains read nothing too early and overwrite nothing
+    too early: the same calls with a synchronisation behind each give the same bits."""
+    import h2o_heavy_hitter_gb300 as h2o
+    rng = torch.Generator(device="cuda").manual_seed(batch)
+    rand = lambda *shape: torch.randn(*shape, generator=rng, device="cuda").to(torch.bfloat16)
+    prefix, steps = 2500, 6
+    K, V = rand(batch + 1, heads, prefix, 128), rand(batch + 1, heads, prefix, 128)
+    lens = ints([(37 * i) % 300 for i in range(batch)] + [prefix])
+    k, v = rand(steps, batch, heads, 1, 128), rand(steps, batch, heads, 1, 128)
+    q = rand(steps, 2, batch, heads * group, 128)
+    everyone, seqs, one, sink = ints(range(batch + 1)), ints(range(batch)), ints([batch]), ints([batch + 1])
+
+    def run(wait):
+        pool = h2o.h2o_pool_create(1, 14 * batch + 100, 32, heads, 128, batch + 2, 80, kv)
+        outs = torch.zeros(steps, 2, batch, heads * group, 128, dtype=torch.bfloat16, device="cuda")
+        lses = torch.zeros(steps, 2, batch, heads * group, device="cuda")
+        calls = [lambda: h2o.h2o_pool_write(pool, 0, everyone, K, V, lens=lens)]
+        for t in range(steps):
+            attend = lambda t, i: h2o.h2o_pool_attend(pool, 0, seqs, q[t, i], prefix=batch if i == 0 or t % 2 else -1,
+                                                      out=outs[t, i], lse=lses[t, i], accumulate=t != 3)
+            calls += [lambda t=t: h2o.h2o_pool_write(pool, 0, seqs, k[t], v[t]),
+                      lambda t=t: attend(t, 0), lambda t=t: attend(t, 1),
+                      lambda: h2o.h2o_pool_free(pool, 0, sink),
+                      lambda: h2o.h2o_pool_fork(pool, 0, one, sink),
+                      lambda: h2o.h2o_pool_compact(pool, 0, sink, 100, 60),
+                      lambda: h2o.h2o_pool_compact(pool, 0, seqs, 150, 50)]
+        torch.cuda.synchronize()
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        h2o.h2o_pool_sync_check(pool)
+        state = {name: x.clone() for name, x in h2o.h2o_pool_view(pool, 0).items()}
+        torch.cuda.synchronize()
+        pool.close()
+        return state | {"out": outs, "lse": lses}
+
+    want = run(True)
+    for _ in range(3):
+        got = run(False)
+        for name, x in want.items():
+            assert torch.equal(x.view(torch.uint8), got[name].view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("batch", [3, 40, 90])  # narrow rows, one row tile of the prefix, three
 def test_a_captured_step_behind_copies_and_joined_streams(kv, batch):
     """Every call of a captured graph behind a copy, a fill and a join of two streams."""
