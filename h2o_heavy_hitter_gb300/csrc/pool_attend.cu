@@ -36,9 +36,11 @@
 // their own, and their scales go into P. Bound by the work on a tile, not by its
 // bytes: 64 sequences of up to 1000 tokens, 8 heads, 4 query heads each: 74 MB in 35 us.
 //
-// P is rounded to bf16, the operand type of the second product, whose exponent
-// reaches as far as fp32's (a value's scale is in it); logits, sums and
-// accumulators are fp32. What lies behind a sequence's end in its last page is
+// The second product takes P as two bf16 terms, p rounded and what is left of it
+// rounded: 16 significant bits, with an exponent that reaches as far as fp32's (a
+// value's scale is in it). Logits, sums and accumulators are fp32. (One term, 8
+// bits, would be the largest error of an output before its own rounding.)
+// What lies behind a sequence's end in its last page is
 // not trusted: its probabilities are set to zero, and its values in shared
 // memory too, since 0 times a NaN is not 0.
 #include <algorithm>
@@ -208,6 +210,7 @@ struct TileCursor {
 constexpr int kWarpMMA = 1, kWarpQ = 2, kWarpV = 3, kWarpRows = 4, kWarpCodes = 12;
 constexpr int kCodeThreads = 256;
 constexpr int kQBox = kFewRows * 128;  // rows x 64 channels (or keys) of an operand with few rows
+constexpr int kSplitRows = 16;         // rows up to which one P operand holds both terms
 
 template <int RK, int RV, int S>
 struct Bars {
@@ -234,7 +237,10 @@ struct Cfg {
   static constexpr int S = F8 ? 2 * (128 / D) : 1;  // slots of value codes
   static constexpr int CODES = F8 ? S * TILE_KEYS * D : 0;
   static constexpr int Q = kQBox * (D / 64);  // a unit's queries; two buffers
-  static constexpr int P = kQBox * 2;         // a tile's probabilities; two buffers per warpgroup
+  // A tile's probabilities, 128 keys x 32 columns: up to 16 rows' first terms and, kSplitRows
+  // further, their second, two buffers per warpgroup; or, of more rows, the first terms in one
+  // buffer and the second in the other.
+  static constexpr int P = kQBox * 2;
   static constexpr int SCALES = F8 ? (RK + S + kScaleTiles) * TILE_KEYS * 4 : 0;
   static constexpr size_t SMEM = static_cast<size_t>(RK) * KTILE + RV * TILE + 2 * Q + 4 * P + CODES +
                                  SCALES + sizeof(List) + sizeof(Bars<RK, RV, S>) + 1024;
@@ -282,6 +288,7 @@ struct TileRows {
   float fac;      // E4M3: scale of row `lane`'s logits
   bool live;      // the key lies before the sequence's end
   uint8_t* p;     // row 0 of the P operand at this key's place in a 16-byte chunk
+  int second;     // bytes from a row's first term to its second
   int chunk;      // that chunk
   float* logits;  // row 0's logit of this key, or null
   int cap, rows;
@@ -337,8 +344,11 @@ __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float&
       pr[i] = a.live ? ex2(fmaf(__uint_as_float(s[i]), k, -n)) : 0.f;
       // K-major, 128-byte swizzle: 16-byte chunk (key / 8) of a row at chunk ^ (row & 7)
       const int row = r0 + i;
-      *reinterpret_cast<__nv_bfloat16*>(a.p + row * 128 + ((a.chunk ^ (row & 7)) << 4)) =
-          __float2bfloat16(a.live ? pr[i] * a.vs : 0.f);
+      uint8_t* at = a.p + row * 128 + ((a.chunk ^ (row & 7)) << 4);
+      const float x = a.live ? pr[i] * a.vs : 0.f;
+      const __nv_bfloat16 first = __float2bfloat16(x);
+      *reinterpret_cast<__nv_bfloat16*>(at) = first;
+      *reinterpret_cast<__nv_bfloat16*>(at + a.second) = __float2bfloat16(x - __bfloat162float(first));
     }
     const float x = __shfl_sync(0xffffffffu, warp_sums<CH>(pr, lane), (lane - r0) & 31);
     if (lane >= r0 && lane < r0 + CH) sum = x;
@@ -466,10 +476,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       int e = 0;
       bool ok = true;
       struct {
-        bool live = false, first, last;
+        bool live = false, first, last, wide;
         int t, e;
-        uint32_t c, g, idesc;
+        uint32_t c, g;
       } pv;
+      constexpr uint32_t idesc_pv = idesc_bf16(TILE_KEYS, kFewRows, 0, 0) | (1u << 15);
       auto issue_pv = [&]() -> bool {
         const uint32_t st = pv.g % RV, buf = pv.c & 1;
         if (!pool_warp_wait(&bars->p_ready[pv.t][buf], (pv.c >> 1) & 1, v.err) ||
@@ -478,13 +489,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           return false;
         tc_fence_after();
         const uint64_t vb = dv0 + static_cast<uint64_t>(st * (C::TILE >> 4));
-        const uint64_t pb = dp0 + static_cast<uint64_t>((pv.t * 2 + buf) * (C::P >> 4));
+        const uint64_t pb = dp0 + static_cast<uint64_t>((pv.t * 2 + (pv.wide ? 0 : buf)) * (C::P >> 4));
         const uint32_t o = tmem + C::O_COL + pv.t * 32;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
-            umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
-                    pv.idesc | (1u << 15), (!pv.first || kk > 0) ? 1u : 0u);
+            umma_ss(o, vb + kk * (2048 >> 4), pb + (((kk >> 2) * kQBox + (kk & 3) * 32) >> 4), idesc_pv,
+                    (!pv.first || kk > 0) ? 1u : 0u);
+          if (pv.wide) {
+#pragma unroll
+            for (int kk = 0; kk < TILE_KEYS / 16; ++kk)
+              umma_ss(o, vb + kk * (2048 >> 4), pb + ((C::P + (kk >> 2) * kQBox + (kk & 3) * 32) >> 4),
+                      idesc_pv, 1u);
+          }
           umma_commit(&bars->values.empty[st]);
           umma_commit(&bars->pv_done[pv.t][buf]);
           if (pv.last) umma_commit(&bars->o_last[pv.t]);
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       };
       while (ok && w.next()) {
         const int t = e & 1, qb = e & 1;
-        const int cols = w.rows() <= 16 ? 16 : 32;
+        const int cols = w.rows() <= kSplitRows ? kSplitRows : kFewRows;
         const uint32_t idesc = idesc_bf16(TILE_KEYS, cols, 0, 0), idesc8 = idesc_e4m3(TILE_KEYS, cols);
         if (!pool_warp_wait(&bars->q_full[qb], (e >> 1) & 1, v.err)) break;
         for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
@@ -535,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           pv.e = e;
           pv.c = c[t]++;
           pv.g = g;
-          pv.idesc = idesc;
+          pv.wide = w.rows() > kSplitRows;
         }
         ++e;
       }
@@ -574,6 +591,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       } else if (p.w.logits) {
         logits = p.w.logits + (static_cast<size_t>(w.b) * p.s.heads + w.h) * rows * v.cap;
       }
+      const bool wide = rows > kSplitRows;
       float m = -INFINITY, l = 0.f;  // of row `lane`
       float fac = 1.f;               // E4M3: of row `lane`'s codes
       if (F8 && lane < rows)
@@ -620,11 +638,19 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         float alpha = 1.f, sum;
         bool rescale = false;
         const TileRows tr{s_tm, ks, vs, fac, live,
-                          sP + (t * 2 + buf) * C::P + (r >> 6) * kQBox + (r & 7) * 2, (r & 63) >> 3,
+                          sP + (t * 2 + (wide ? 0 : buf)) * C::P + (r >> 6) * kQBox + (r & 7) * 2,
+                          wide ? C::P : kSplitRows * 128, (r & 63) >> 3,
                           logits ? logits + kt * TILE_KEYS + r : nullptr, v.cap, rows};
+        // many rows have one P buffer, which the O^T before this one must have read: it is
+        // waited for behind the maximum
+        auto maximum = [&](float mine, float (&all)[4]) -> bool {
+          return exchange(mine, all) &&
+                 (!wide || kt == w.kt0 ||
+                  pool_warp_wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1, v.err));
+        };
         const bool done = rows == 1   ? tile_softmax<1, F8>(tr, m, alpha, rescale, sum, exchange)
                           : rows <= 4 ? tile_softmax<4, F8>(tr, m, alpha, rescale, sum, exchange)
-                                      : tile_softmax<8, F8>(tr, m, alpha, rescale, sum, exchange);
+                                      : tile_softmax<8, F8>(tr, m, alpha, rescale, sum, maximum);
         if (!done) {
           ok = false;
           break;
@@ -638,13 +664,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           }
           tc_fence_after();
           for (int r0 = 0; r0 < rows; r0 += 8) {
-            uint32_t o[8];
-            tmem_ld8(o_tm + r0, o);
-            tmem_wait_ld();
+            for (int term = 0; term < (wide ? 1 : 2); ++term) {
+              uint32_t o[8];
+              tmem_ld8(o_tm + term * kSplitRows + r0, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, alpha, (r0 + i) & 31));
-            tmem_st8(o_tm + r0, o);
+              for (int i = 0; i < 8; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, alpha, (r0 + i) & 31));
+              tmem_st8(o_tm + term * kSplitRows + r0, o);
+            }
           }
           tmem_wait_st();
         }
@@ -663,14 +691,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       const size_t rec = static_cast<size_t>(w.piece) * (w.prefix ? kFewRows : p.s.group);
       float* out = (w.prefix ? p.w.po : p.w.to) + rec * D;
       for (int r0 = 0; r0 < rows; r0 += 8) {
-        uint32_t o[8];
+        uint32_t o[8], o2[8];
         tmem_ld8(o_tm + r0, o);
+        if (!wide) tmem_ld8(o_tm + kSplitRows + r0, o2);
         tmem_wait_ld();
         if (r < D) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (r0 + i >= rows) break;
-            out[(r0 + i) * D + r] = __uint_as_float(o[i]);
+            out[(r0 + i) * D + r] = __uint_as_float(o[i]) + (wide ? 0.f : __uint_as_float(o2[i]));
           }
         }
       }

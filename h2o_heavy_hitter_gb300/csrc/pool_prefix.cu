@@ -9,7 +9,8 @@
 //   an accumulator of their own, so that two short softmax chains run side by side
 //   and no maximum is exchanged; with two, the halves take a row tile each and
 //   share the key and value tiles. S is double-buffered: the product of the next
-//   tile runs under the softmax of this one. Bound by HBM up to some 128 rows,
+//   tile runs under the softmax of this one. P is two bf16 terms (pool_attend.cu), side
+//   by side in the columns that S held. Bound by HBM up to some 128 rows,
 //   beyond by the exponentials and the products of 256 rows a tile: 512 rows a
 //   head, 8 heads, 32768 keys take 94 us with the joining (730 TFLOP/s). At 1024
 //   keys a CTA has two tiles, and 17 us are its start and the read-out.
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             const uint32_t a = s_tm + half * 64 + (kk & 3) * 8;
             const bool fresh = pv.first && (pv.two ? kk == 0 : (kk & 3) == 0);
             umma_ts(o, a, vb + kk * (2048 >> 4), idesc_pv, fresh ? 0u : 1u);
+            umma_ts(o, a + 32, vb + kk * (2048 >> 4), idesc_pv, 1u);  // the second term
           }
           umma_commit(&bars->pv_done[buf]);
           if (pv.frees) umma_commit(&bars->values.empty[st]);
@@ -390,31 +392,37 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
             m = mx;
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t sc2 = f2_pack(qscale, qscale), nm2 = f2_pack(-ref, -ref);
+          const uint64_t sc2 = f2_pack(qscale, qscale), nm2 = f2_pack(-ref, -ref), minus = f2_pack(-1.f, -1.f);
           uint64_t rs2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
           for (int c = chunks - 1; c >= 0; --c) {  // the last chunk is still in registers
             const int first = col0 + 64 * c;
             if (c < chunks - 1) load(s, first);
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              uint32_t pk[8];
+            for (int cc = 0; cc < 8; ++cc) {
+              uint32_t pk[4], pk2[4];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                float a, b;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[cc * 16 + 2 * x]),
-                                         __uint_as_float(s[cc * 16 + 2 * x + 1])),
-                                 sc2, nm2),
-                          a, b);
-                const float p0 = ex2(a), p1 = ex2(b);
+              for (int x = 0; x < 4; ++x) {
+                const int y = cc * 4 + x;
+                float p0, p1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), sc2, nm2),
+                          p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
                 rs2[x & 1] = f2_add(rs2[x & 1], f2_pack(p0, p1));
                 if (F8) {
-                  const float2 v2 = reinterpret_cast<const float2*>(vs)[first / 2 + cc * 8 + x];
-                  pk[x] = pack_bf16x2(p0 * v2.x, p1 * v2.y);
-                } else {
-                  pk[x] = pack_bf16x2(p0, p1);
+                  const float2 v2 = reinterpret_cast<const float2*>(vs)[first / 2 + y];
+                  p0 *= v2.x;
+                  p1 *= v2.y;
                 }
+                pk[x] = pack_bf16x2(p0, p1);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(pk[x] << 16), __uint_as_float(pk[x] & 0xffff0000u)),
+                                 minus, f2_pack(p0, p1)),
+                          p0, p1);
+                pk2[x] = pack_bf16x2(p0, p1);
               }
-              tmem_st8(s_tm + first + cc * 8, pk);  // P over the S columns it came from
+              // P over the S columns it came from: 32 of first terms, 32 of second
+              tmem_st4(s_tm + first + cc * 4, pk);
+              tmem_st4(s_tm + first + 32 + cc * 4, pk2);
             }
           }
           float r0, r1, r2, r3;

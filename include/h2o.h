@@ -516,7 +516,9 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  *
  * For row (i, query head hq), key head hq / (q_heads / H): p = softmax(q . k /
  * sqrt(d)) over both token lists, out = sum_j p_j v_j (bf16, rounded once from
- * fp32), lse = the natural log of the softmax's normaliser (fp32; may be NULL).
+ * an fp32 sum; p_j, in an H2O_KV_FP8 pool times v_j's scale, enters it with 16
+ * significant bits, as two bf16 terms), lse = the natural log of the softmax's
+ * normaliser (fp32; may be NULL).
  * With accumulate, every probability is added to its slot's accumulated score:
  * to the sequence's for its own tokens (summed over the head's query group), to
  * the prefix's, summed over group and batch, for the prefix: the statistic by
