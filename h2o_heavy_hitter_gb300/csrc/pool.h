@@ -43,14 +43,16 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
                       bool share, int32_t* fresh, int32_t* plan, cudaStream_t stream);
 cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
                       cudaStream_t stream);
-// Appends lens[i] (or T) tokens to sequence seqs[i] of one layer. fresh: n * ceil(T / page).
+// Appends lens[i] (or T) tokens to sequence seqs[i] of one layer (T = 0: the list is checked
+// alone). fresh: n * ceil(T / page).
 cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void* K, const void* V,
                        int T, const int32_t* lens, const float* score, int32_t* fresh,
                        int32_t* plan, cudaStream_t stream);
 
 // Keeps the r last tokens and the h others of largest (score, slot) of every
 // head of each sequence longer than h + r. fresh: n * ceil(k / page) per layer;
-// where / kept: layers * n * heads * k.
+// where / kept: layers * n * heads * k. With h + r >= cap (none of the three is then
+// needed) it checks the list alone.
 cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* seqs, int h, int r,
                          int32_t* fresh, int32_t* plan, int32_t* where, float* kept,
                          cudaStream_t stream);

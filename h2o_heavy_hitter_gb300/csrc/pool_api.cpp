@@ -252,8 +252,8 @@ int h2o_pool_write(h2o_pool* p, int layer, int n, const int32_t* seqs, const voi
                    const void* V, int T, const int32_t* lens, const float* score) {
   if (int rc = check_list(p, layer, false, n, seqs)) return rc;
   if (T < 0 || T > H2O_MAX_T) return fail(H2O_EINVAL, "T out of range");
-  if (n == 0 || T == 0) return H2O_OK;
-  if (!K || !V) return fail(H2O_EINVAL, "null K or V");
+  if (n == 0) return H2O_OK;
+  if (T > 0 && (!K || !V)) return fail(H2O_EINVAL, "null K or V");
   if (!aligned16(K) || !aligned16(V)) return fail(H2O_EINVAL, "K and V must be 16-byte aligned");
   return guarded([&] {
     const h2o::PoolView v = layer_view(p, layer);
@@ -288,10 +288,11 @@ int h2o_pool_compact(h2o_pool* p, int layer, int n, const int32_t* seqs, int h, 
   if (int rc = check_list(p, layer, true, n, seqs)) return rc;
   if (h < 0 || r < 0 || h > H2O_MAX_K || r > H2O_MAX_K || h + r < 1 || h + r > H2O_MAX_K)
     return fail(H2O_EINVAL, "need h >= 0, r >= 0 and 1 <= h + r <= H2O_MAX_K");
-  if (n == 0 || h + r >= p->v.cap) return H2O_OK;  // no sequence is longer than the budget
+  if (n == 0) return H2O_OK;
   return guarded([&] {
     const h2o::PoolView v = layer_view(p, layer < 0 ? 0 : layer);
-    const size_t L = layer < 0 ? p->layers : 1, N = n, k = h + r;
+    // where no sequence can be longer than the budget nothing is kept; the list is checked all the same
+    const size_t L = layer < 0 ? p->layers : 1, N = n, k = h + r < v.cap ? h + r : 0;
     const size_t fresh = L * N * ((k + v.page - 1) / v.page), plan = L * N * h2o::kPlanInts;
     const size_t kept = L * N * v.heads * k;
     cudaStream_t s = current_stream();

@@ -724,10 +724,10 @@ cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
 cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void* K, const void* V,
                        int T, const int32_t* lens, const float* score, int32_t* fresh,
                        int32_t* plan, cudaStream_t stream) {
-  if (n == 0 || T == 0) return cudaSuccess;
+  if (n == 0) return cudaSuccess;
   cudaError_t e =
       launch_after(write_plan_kernel, dim3(1), kPlanThreads, 0, stream, v, n, seqs, T, lens, fresh, plan);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || T == 0) return e;
   int span = 0;
   while (1 << span < kWriteTokens && 1 << span < T) ++span;
   const int units = kWriteTokens >> span;  // per block
@@ -744,7 +744,7 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
                          int32_t* fresh, int32_t* plan, int32_t* where, float* kept,
                          cudaStream_t stream) {
   const int k = h + r;
-  if (n == 0 || k >= v.cap) return cudaSuccess;  // no sequence can be longer than h + r
+  if (n == 0) return cudaSuccess;
   const int stride = n * ((k + v.page - 1) >> v.shift);
   // the keys of a row in shared memory, where rows can be that long
   const int held = std::min(v.cap, kSelectKeys);
@@ -754,7 +754,7 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
   if (e != cudaSuccess) return e;
   e = launch_after(compact_select_kernel, dim3(v.heads + 1, n, layers), kSelectThreads,
                    held * sizeof(unsigned), stream, v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || k >= v.cap) return e;  // (no sequence can be longer than h + r)
   const int slots = 8 * gather_slots(v.row_bytes);  // per block
   const dim3 grid(n * v.heads, (k + slots - 1) / slots, layers);
   auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>

@@ -470,7 +470,8 @@ int h2o_pool_view(h2o_pool* pool, int layer, void** K, void** V, float** k_scale
  * a length outside [0, T] is clamped and sets bit 4) from K, V, device bf16
  * [n][H][T][d], 16-byte aligned, with initial scores score, device fp32
  * [n][H][T] (a prompt's column sums from h2o_prefill_attention; NULL: zeros).
- * They take the sequence's next positions. An entry that would grow beyond
+ * They take the sequence's next positions. With T = 0 K and V may be NULL: the
+ * lists are checked alone. An entry that would grow beyond
  * max_pages is refused, unchanged, with bit 8.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
