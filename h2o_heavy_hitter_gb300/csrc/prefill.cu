@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -914,7 +915,7 @@ cudaError_t prefill_colsum(const void* Q, const void* K, const float* lse2, int 
 }
 
 // ------------------------------------------------------------------ per-device state
-// Kernel attributes and looked-up symbol addresses are kept for devices
+// Kernel attributes and looked-up device symbols are kept for devices
 // 0 .. kMaxDevices - 1 under one mutex. forget_device_state() starts a new
 // epoch, which invalidates all of it.
 namespace {
@@ -923,16 +924,17 @@ int g_device_state_epoch = 1;
 }  // namespace
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
+  static std::atomic<void*> found{nullptr};  // a lookup that fails is made again by the next call
+  void* ptr = found.load(std::memory_order_acquire);
+  if (!ptr) {
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
-  return fn;
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(ptr, std::memory_order_release);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
 }
 
 cudaError_t raise_smem_limit(const void* kernel, size_t bytes, int (&opted_in)[kMaxDevices]) {

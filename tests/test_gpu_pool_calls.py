@@ -1,5 +1,4 @@
 """Calls of the paged cache that its documentation allows, at the edges of its rules."""
-import ctypes
 import os
 import subprocess
 import sys
@@ -43,3 +42,47 @@ def test_a_budget_beyond_the_capacity_checks_all_layers():
     with pytest.raises(h2o.H2OError, match="word 0x2 "):
         h2o.h2o_pool_sync_check(pool)
     pool.close()
+
+
+def test_a_driver_lookup_that_failed_once_is_made_again(tmp_path):
+    """A fake of the runtime call that finds the driver's tensor-map encoder fails the first time:
+    that pool is refused, the next one works."""
+    fake = tmp_path / "fake.c"
+    fake.write_text("""
+#define _GNU_SOURCE
+#include <dlfcn.h>
+#include <string.h>
+int cudaGetDriverEntryPointByVersion(const char* symbol, void** fn, unsigned version,
+                                     unsigned long long flags, int* result) {
+  static int failed = 0;
+  if (!strcmp(symbol, "cuTensorMapEncodeTiled") && !failed++) {
+    if (result) *result = 1; /* symbol not found */
+    *fn = 0;
+    return 0;
+  }
+  int (*real)(const char*, void**, unsigned, unsigned long long, int*) =
+      dlsym(RTLD_NEXT, "cudaGetDriverEntryPointByVersion");
+  return real(symbol, fn, version, flags, result);
+}
+""")
+    lib = tmp_path / "fake.so"
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", lib, fake, "-ldl"], check=True)
+    code = """
+import torch, h2o_heavy_hitter_gb300 as h2o
+make = lambda: h2o.h2o_pool_create(1, 4, 16, 1, 64, 2, 2)
+try:
+    make()
+    print("first made")
+except h2o.H2OError as e:
+    print("first refused", e.code)
+pool = make()
+x = torch.ones(1, 1, 5, 64, dtype=torch.bfloat16, device="cuda")
+one = torch.zeros(1, dtype=torch.int32, device="cuda")
+h2o.h2o_pool_write(pool, 0, one, x, x)
+out, _ = h2o.h2o_pool_attend(pool, 0, one, x[:, :, 0])
+print("second", out.eq(1).all().item())
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "LD_PRELOAD": str(lib)})
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split("\n")[:2] == ["first refused -4", "second True"], r.stdout
