@@ -100,6 +100,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// For a kernel some of whose threads read, before their grid_dependency_wait or without one,
+// what kernels before the one it follows wrote (never what that one writes): the wait alone
+// promises visibility, and only to the kernel that executes it. A thread of each block that has
+// it releases it and triggers; one of the kernel that follows acquires it for its block, for
+// copies of the TMA engine too, before a block barrier and the first read. (Fences by all
+// threads cost 1 to 4 us a call of paged attention.)
+__device__ __forceinline__ void grid_release_dependents() {
+  __threadfence();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_acquire() {
+  __threadfence();
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 // Lets the next kernel of the stream start its prologue.
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -379,8 +379,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
-  // beside the prefix kernel, which waited for what came before it, this one waits at its end
-  if (p.a.prefix < 0 || p.s.few) grid_dependency_wait();
+  // beside the prefix kernel, which waited for what came before it and released that, this one
+  // waits at its end
+  if (p.a.prefix < 0 || p.s.few) {
+    grid_dependency_wait();
+  } else {
+    if (threadIdx.x == 0) grid_acquire();
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < RK; ++i) {
       mbar_init(&bars->keys.full[i], 1);
@@ -710,8 +716,12 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         (w.prefix ? p.w.pml : p.w.tml)[rec + lane] = make_float2(m, l);
     }
   }
-  // the prefix kernel may still run: what follows waits for both
-  grid_launch_dependents();
+  // the prefix kernel may still run: what follows waits for both (pool_prefix_score_kernel
+  // begins with keys and queries, which are older than both)
+  if (p.a.prefix < 0 || p.s.few)
+    grid_launch_dependents();
+  else if (threadIdx.x == 0)
+    grid_release_dependents();
   grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
@@ -796,7 +806,7 @@ __device__ __forceinline__ Records records_of(const AttendParams& p, int b, int 
 
 // The lse (base 2) of row g by L adjacent lanes (all groups of a warp at once), the
 // same bits in every block; `first`: the maximum of record `lane`.
-template <int L>
+template <int L, bool L2>
 __device__ __forceinline__ float row_lse(const AttendParams& p, const Records& x, int g, int lane,
                                          float& first) {
   const int all = x.prefix + x.own;
@@ -804,7 +814,7 @@ __device__ __forceinline__ float row_lse(const AttendParams& p, const Records& x
   first = -INFINITY;
 #pragma unroll 2
   for (int i = lane; i < all; i += L) {
-    const float2 y = record_ml(p, x, i, g);
+    const float2 y = record_ml<L2>(p, x, i, g);
     if (i < L) first = y.x;
     join(m, l, y.x, y.y);
   }
@@ -831,7 +841,7 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
     const int i = i0 + (threadIdx.x >> 3), b = min(i, rows - 1) / p.s.group;
     const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
     float first;
-    const float x = row_lse<8>(p, records_of<8>(p, b, h, plen, cum, lane), min(i, rows - 1) - b * p.s.group,
+    const float x = row_lse<8, false>(p, records_of<8>(p, b, h, plen, cum, lane), min(i, rows - 1) - b * p.s.group,
                                lane, first);
     // +inf: not counted, whatever its logits are
     if (lane == 0 && i < rows) s_lse[i] = p.w.seq[b] < 0 ? INFINITY : x;
@@ -862,7 +872,7 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
 // chunk computes the lse's it needs, chunk 0 writes. `blocks` * `chunks` such blocks,
 // then those of the prefix's scores. Latency-bound: the lengths, the records, then
 // the outputs are loads behind one another; 8192 rows take 20 us, 4 rows 6.
-template <int D>
+template <int D, bool L2>
 __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_warps, int blocks, int chunks,
                                              float (&s_lse)[kFinishWarps][kFewRows]) {
   const PoolView& v = p.a.v;
@@ -872,8 +882,8 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
   const int unit = block * (kFinishWarps / unit_warps) + local;
   const bool in = unit < p.s.n * p.s.heads;
   const int b = in ? unit / p.s.heads : 0, h = in ? unit - b * p.s.heads : 0;
-  const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
-  const int seq = in ? p.w.seq[b] : -1;
+  const int cum[3] = {load<L2>(p.w.cum + b), load<L2>(p.w.cum + b + 1), load<L2>(p.w.cum + p.s.n)};
+  const int seq = in ? load<L2>(p.w.seq + b) : -1;
   const int plen = p.a.prefix >= 0 ? max(0, checked_length(v, p.a.prefix, false)) : 0;
   float* nlse = nullptr;  // for the scores of a prefix with many rows
   if (in && p.w.nlse && chunk == 0)
@@ -881,18 +891,18 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
            b % p.s.per_tile * group;
   int len = 0;
   if (seq >= 0) {
-    len = v.meta[2 * seq];
+    len = load<L2>(v.meta + 2 * seq);
     const Records x = records_of<32>(p, b, h, plen, cum, lane);
     const int all = x.prefix + x.own;
     for (int g = sub; g < group; g += unit_warps) {
       float first;
-      const float lse = row_lse<32>(p, x, g, lane, first);
+      const float lse = row_lse<32, L2>(p, x, g, lane, first);
       if (lane == 0) s_lse[local][g] = lse;
       if (chunk) continue;
       float acc[D / 32] = {};
       for (int i0 = 0; i0 < all; i0 += 32) {
         const float mine =
-            i0 == 0 ? first : i0 + lane < all ? record_ml(p, x, i0 + lane, g).x : -INFINITY;
+            i0 == 0 ? first : i0 + lane < all ? record_ml<L2>(p, x, i0 + lane, g).x : -INFINITY;
         const float wgt = all ? ex2(mine - lse) : 0.f;
         const int n = min(32, all - i0);
 #pragma unroll 8
@@ -902,10 +912,10 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
                            record(p, x, i0 + i, g) * D + lane * (D / 32);
           float part[D / 32];
           if constexpr (D == 128) {
-            const float4 y = *reinterpret_cast<const float4*>(o);
+            const float4 y = load<L2>(reinterpret_cast<const float4*>(o));
             part[0] = y.x, part[1] = y.y, part[2] = y.z, part[3] = y.w;
           } else {
-            const float2 y = *reinterpret_cast<const float2*>(o);
+            const float2 y = load<L2>(reinterpret_cast<const float2*>(o));
             part[0] = y.x, part[1] = y.y;
           }
 #pragma unroll
@@ -932,11 +942,11 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
   const int step = chunks * unit_warps * 128;
   for (int j = ((chunk * unit_warps + sub) * 32 + lane) * 4; j < len; j += step) {
     // four slots a lane: a sequence's rows end at a multiple of its page
-    float4 sum = *reinterpret_cast<float4*>(score + j);
+    float4 sum = load<L2>(reinterpret_cast<const float4*>(score + j));
     float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int g = 0; g < group; ++g) {
-      const float4 y = *reinterpret_cast<const float4*>(L + static_cast<size_t>(g) * v.cap + j);
+      const float4 y = load<L2>(reinterpret_cast<const float4*>(L + static_cast<size_t>(g) * v.cap + j));
       const float n = s_lse[local][g];
       a[0] += ex2(y.x - n);
       a[1] += ex2(y.y - n);
@@ -951,20 +961,24 @@ __device__ __forceinline__ void finish_block(const AttendParams& p, int unit_war
   }
 }
 
-// `beside`: launched behind pool_prefix_score_kernel, which lets it start once the
-// kernels before both have completed. It reads nothing of that kernel, so only
-// its own end waits: what follows this kernel follows both.
-template <int D>
+// `beside`: launched behind pool_prefix_score_kernel, whose trigger stands behind its wait for
+// the kernels that left the pieces. This one reads nothing of that kernel, so only its own end
+// waits: what follows this kernel follows both. Without a wait nothing is promised of this SM's
+// L1, so what others wrote is read from L2 (load<true>), where those kernels, complete, have left it.
+// (An acquire by each of the 2048 blocks of 256 sequences x 32 heads cost 3 us.)
+template <int D, bool beside>
 __global__ void __launch_bounds__(kFinishThreads)
-    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps, int blocks, int chunks,
-                       bool beside) {
+    pool_finish_kernel(const __grid_constant__ AttendParams p, int unit_warps, int blocks, int chunks) {
   __shared__ float s_lse[kFinishWarps][kFewRows];
   if (!beside) grid_dependency_wait();
-  grid_launch_dependents();
+  if (!p.w.nlse)
+    grid_launch_dependents();
+  else if (threadIdx.x == 0)  // the score kernel follows, and begins with keys and queries
+    grid_release_dependents();
   if (static_cast<int>(blockIdx.x) >= blocks * chunks)
     prefix_scores(p, blockIdx.x - blocks * chunks, s_lse[0]);
   else
-    finish_block<D>(p, unit_warps, blocks, chunks, s_lse);
+    finish_block<D, beside>(p, unit_warps, blocks, chunks, s_lse);
   if (beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
@@ -1057,8 +1071,9 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t stream) {
   const int sums = p.w.plogits ? p.s.heads * ((p.a.v.cap + per_block - 1) / per_block) : 0;
   const bool scores = many && p.a.accumulate, beside = scores && score_joins(p.s);
   if (beside && (e = pool_prefix_score(p, stream)) != cudaSuccess) return e;
-  if ((e = launch_after(pool_finish_kernel<D>, dim3(blocks * chunks + sums), kFinishThreads, 0, stream,
-                        p, unit_warps, blocks, chunks, beside)) != cudaSuccess)
+  if ((e = launch_after(beside ? pool_finish_kernel<D, true> : pool_finish_kernel<D, false>,
+                        dim3(blocks * chunks + sums), kFinishThreads, 0, stream, p, unit_warps, blocks,
+                        chunks)) != cudaSuccess)
     return e;
   return scores && !beside ? pool_prefix_score(p, stream) : cudaSuccess;
 }

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   Walk w(p, plen, cta);
-  grid_launch_dependents();  // the few-rows kernel, as SMs become free
+  if (threadIdx.x == 0) grid_release_dependents();  // the rows kernel, as SMs become free, does not wait first
 
   if (warp == 0) {
     if constexpr (F8)
@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(kScoreBound, 1)
   const PoolView& v = p.a.v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    grid_acquire();  // the prefix's length, pages and queries; the softmax warps wait for the rest
     for (int i = 0; i < R; ++i) {
       mbar_init(&bars->keys.full[i], 1);
       mbar_init(&bars->keys.empty[i], F8 ? 1 + 4 : 1);  // the products, and the readers of the scales
@@ -724,8 +725,9 @@ __global__ void __launch_bounds__(kScoreBound, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t cnt = 0;
     bool ok = true;
-    grid_dependency_wait();    // the pieces, or the lse's, by the kernels before
-    grid_launch_dependents();  // the finish kernel, when it comes behind this one
+    grid_dependency_wait();     // the pieces, or the lse's, by the kernels before
+    // the finish kernel, when it comes behind this one, reads them at once
+    if (warp == kWarpSoftmax && lane == 0) grid_release_dependents();
     int last = -1;
     uint32_t heads = 0;        // of the share so far
     for (uint32_t g = 0; ok && k.step(); ++g) {

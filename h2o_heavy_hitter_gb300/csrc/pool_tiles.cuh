@@ -89,9 +89,15 @@ __device__ __forceinline__ bool pool_warp_wait(uint64_t* bar, uint32_t parity, i
 }
 
 // ------------------------------------------------------------------ lengths, shares
+// A load, L2: past L1.
+template <bool L2, typename T>
+__device__ __forceinline__ T load(const T* at) {
+  return L2 ? __ldcg(at) : *at;
+}
+
 // A sequence's length, -1 (reported when `report`) for a state that no call leaves.
 __device__ __forceinline__ int checked_length(const PoolView& v, int seq, bool report) {
-  const int len = v.meta[2 * seq];
+  const int len = __ldcg(v.meta + 2 * seq);
   if (len >= 0 && len <= v.cap) return len;
   if (report) atomicOr(v.err, kErrBadState);
   return -1;
@@ -321,8 +327,9 @@ __device__ __forceinline__ size_t record(const AttendParams& p, const Records& x
   return (i < x.prefix ? x.pbase + i * x.pstep
                        : x.obase + static_cast<size_t>(i - x.prefix) * p.s.group) + g;
 }
+template <bool L2 = false>
 __device__ __forceinline__ float2 record_ml(const AttendParams& p, const Records& x, int i, int g) {
-  return (i < x.prefix ? p.w.pml : p.w.tml)[record(p, x, i, g)];
+  return load<L2>((i < x.prefix ? p.w.pml : p.w.tml) + record(p, x, i, g));
 }
 
 // Adds a record to {m, l}.
