@@ -62,6 +62,7 @@ struct AttendArgs {
   PoolView v;            // of the layer
   const int32_t* seqs;   // [n]
   int n;
+  int before;            // entries of the caller's list ahead of seqs, whose sequences are named already
   int prefix;            // sequence whose tokens every row attends to first, or -1
   int group;             // query heads per key head
   const void* q;         // bf16 [n][heads * group][d]

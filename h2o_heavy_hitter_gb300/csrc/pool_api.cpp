@@ -4,6 +4,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <memory>
 #include <new>
 #include <string>
 #include <vector>
@@ -334,8 +336,37 @@ int h2o_pool_attend(h2o_pool* p, int layer, int n, const int32_t* seqs, int pref
     a.kmap = &p->maps[2 * layer];
     a.vmap = &p->maps[2 * layer + 1];
     cudaStream_t s = current_stream();
-    Scratch mem(h2o::pool_attend_scratch(a), s);
-    return launch_status(h2o::pool_attend(a, mem.p, s), "pool attention launch");
+    // The scratch grows with the batch and, for the scores, with the longest sequence that the
+    // pool can hold, whatever the lengths are. Where there is not that much memory the batch
+    // goes in parts, one after the other through the same scratch, which is there before the first.
+    for (int part = n;; part = (part + 1) / 2) {
+      auto sized = [&](int entries) {
+        h2o::AttendArgs x = a;
+        x.n = entries;
+        return h2o::pool_attend_scratch(x);
+      };
+      // (a last part of few entries can need more than a full one)
+      const size_t need = std::max(sized(part), n % part ? sized(n % part) : 0);
+      std::unique_ptr<Scratch> mem;
+      try {
+        mem = std::make_unique<Scratch>(need, s);
+      } catch (const std::exception&) {
+        if (part == 1) throw;
+        continue;
+      }
+      for (int at = 0; at < n; at += part) {
+        const size_t row = static_cast<size_t>(at) * q_heads;
+        a.before = at;
+        a.n = std::min(part, n - at);
+        a.seqs = seqs + at;
+        a.q = static_cast<const uint8_t*>(q) + row * p->v.d * 2;
+        a.out = static_cast<uint8_t*>(out) + row * p->v.d * 2;
+        a.lse = lse ? lse + row : nullptr;
+        cudaError_t e = h2o::pool_attend(a, mem->p, s);
+        if (e != cudaSuccess) return cuda_fail(e, "pool attention launch");
+      }
+      return static_cast<int>(H2O_OK);
+    }
   });
 }
 

@@ -61,7 +61,7 @@ struct List {
 // Fills the list: skipped and refused entries have seq -1 and no tiles. An entry
 // is refused for an index outside the pool, the prefix's, or one named before;
 // repeats are looked for one by one only where a hashed bit says that there may
-// be some. Every CTA begins with this, so it takes few barriers. Blockwide;
+// be some, or where the list is a later part of the caller's. Every CTA begins with this, so it takes few barriers. Blockwide;
 // `bits`: 4 KB; `report`: this block sets the error word.
 __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int* wsum,
                            bool report) {
@@ -85,11 +85,11 @@ __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int*
     const int s = list.seq[b];
     if (s >= 0) seen |= (atomicOr(&bits[(s >> 5) & 1023], 1u << (s & 31)) >> (s & 31)) & 1u;
   }
-  if (__syncthreads_or(seen)) {
+  if (__syncthreads_or(seen || a.before)) {
     for (int b = b0; b < b1; ++b) {
       const int s = a.seqs[b];
       if (s < 0) continue;
-      for (int j = 0; j < b; ++j)
+      for (int j = -a.before; j < b; ++j)
         if (a.seqs[j] == s) {
           if (report) atomicOr(v.err, kErrBadList);
           list.len[b] = -1;

@@ -532,7 +532,9 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  * q_heads is a multiple of H, at most H2O_POOL_MAX_GROUP times. `prefix` in `seqs`
  * is a bad entry. With accumulate the call's scratch holds 4 bytes per query row
  * and slot of a longest sequence, 4 n q_heads C (twice that for a prefix with at
- * most 32 rows a head).
+ * most 32 rows a head). Where the allocator does not have that much the batch is
+ * served in 2, 4, ... parts, each of which reads the prefix, and adds to its scores,
+ * in its turn; H2O_ENOMEM when there is no memory for one entry.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
 int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int prefix,

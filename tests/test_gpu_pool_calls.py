@@ -86,3 +86,50 @@ print("second", out.eq(1).all().item())
                        env={**os.environ, "LD_PRELOAD": str(lib)})
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split("\n")[:2] == ["first refused -4", "second True"], r.stdout
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("failures,batch,heads,group,accumulate", [
+    (1, 7, 2, 3, True),    # parts of 4 and 3 entries, prefixes of few rows
+    (2, 70, 1, 2, True),   # of 18, 18, 18 and 16: many rows, then few
+    (1, 70, 2, 2, False),
+    (4, 9, 3, 1, True),    # one by one
+])
+def test_attention_with_less_memory_than_the_batch_wants(failures, batch, heads, group, accumulate, kv):
+    """The first allocations fail: the batch is served in parts, with the results of the whole."""
+    import h2o_heavy_hitter_gb300 as h2o
+    b = Both(pages=3 * batch + 30, page=16, heads=heads, d=64, sequences=batch + 1, max_pages=16, kv=kv, seed=batch)
+    b.write(range(batch + 1), 200, [(11 * i) % 40 for i in range(batch)] + [200])
+    seqs = list(range(batch))
+    seqs[batch // 3] = -1
+    h2o.h2o_test_fail_allocations(failures)
+    try:
+        b.attend(seqs, heads * group, prefix=batch, accumulate=accumulate)
+    finally:
+        h2o.h2o_test_fail_allocations(0)
+    b.check()
+    seqs[-1] = seqs[0]  # named in another part
+    h2o.h2o_test_fail_allocations(failures)
+    try:
+        b.attend(seqs, heads * group, prefix=batch, accumulate=accumulate)
+    finally:
+        h2o.h2o_test_fail_allocations(0)
+    b.check(errors=16)
+    b.close()
+
+
+def test_attention_without_memory_for_one_entry_is_refused_and_changes_nothing():
+    import h2o_heavy_hitter_gb300 as h2o
+    b = Both(pages=12, page=16, heads=2, d=64, sequences=4, max_pages=4)
+    b.write([0, 1, 2], 30)
+    _, q = bf16(b.queries(3, 4))
+    out = torch.full_like(q, 7.0)
+    h2o.h2o_test_fail_allocations(3)  # 3, 2 and 1 entries
+    try:
+        with pytest.raises(h2o.H2OError) as e:
+            h2o.h2o_pool_attend(b.pool, 0, ints([0, 1, 2]), q, out=out)
+    finally:
+        h2o.h2o_test_fail_allocations(0)
+    assert e.value.code == h2o.H2O_ENOMEM and bool((out == 7).all())
+    b.check()
+    b.close()
