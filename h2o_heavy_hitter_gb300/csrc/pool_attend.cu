@@ -223,6 +223,7 @@ struct Bars {
   uint64_t pv_done[2][2];
   uint64_t o_last[2], o_free[2];   // one phase per unit of the warpgroup
   uint64_t xbar[2];                // the warpgroup's exchange, a phase per use
+  uint64_t drained;
   uint32_t tmem;
   int wsum[33];
   float xmax[2][2][4][kFewRows];   // [warpgroup][use & 1][quadrant][row]
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->o_free[t], 4);
       mbar_init(&bars->xbar[t], 4);
     }
+    mbar_init(&bars->drained, 1);
     fence_barrier_init();
   }
   if (warp == kWarpMMA) {
@@ -453,7 +455,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                                               TileCursor(w), threadIdx.x - 32 * kWarpCodes);
   } else if (warp == kWarpQ) {
     if (lane == 0) {
-      for (int e = 0; w.next(); ++e) {
+      uint32_t e = 0;
+      for (; w.next(); ++e) {
         const int qb = e & 1;
         if (e >= 2 && !pool_wait(&bars->q_empty[qb], ((e >> 1) - 1) & 1, v.err)) break;
         mbar_arrive_expect_tx(&bars->q_full[qb], w.rows() * D * 2);
@@ -464,6 +467,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                       c == 1 && F8 ? (w.prefix ? &tq2 : &t2) : (w.prefix ? &tq : &t1), F8 ? 0 : c * 64, 0,
                       w.h, w.prefix ? 0 : w.b, &bars->q_full[qb]);
       }
+      drain_copies(bars->q_full, e, v.err);
     }
   } else if (warp == kWarpMMA) {
     // ---------------------------------------------------------------- MMA issuer
@@ -563,6 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         ++e;
       }
       if (ok && pv.live) issue_pv();
+      drain_products(&bars->drained, v.err);
     }
   } else if (warp >= kWarpRows && warp < kWarpCodes) {
     // ---------------------------------------------------------------- softmax

@@ -48,6 +48,7 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_ready[2], pv_done[2];  // by S buffer
   uint64_t o_last[2], o_free[2];               // one phase per unit
+  uint64_t drained;
   uint32_t tmem;
 };
 
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       mbar_init(&bars->codes.full[i], 1);
       mbar_init(&bars->codes.empty[i], kCodeThreads / 32);
     }
+    mbar_init(&bars->drained, 1);
     fence_barrier_init();
   }
   if (warp == kWarpMMA) {
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                         F8 ? 0 : c * 64, 0, w.h, (2 * w.b + t) * p.s.per_tile, &bars->q_full[qb]);
         }
       }
+      drain_copies(bars->q_full, qn, v.err);
     }
   } else if (warp == kWarpMMA) {
     // ---------------------------------------------------------------- MMA issuer
@@ -310,6 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
         ++e;
       }
       if (ok && pv.live) issue_pv();
+      drain_products(&bars->drained, v.err);
     }
   } else if (warp >= kWarpSoftmax && warp < kWarpCodes) {
     // ---------------------------------------------------------------- softmax
@@ -510,6 +514,7 @@ struct ScoreBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[4], s_free[4];  // S buffers 2 t + (0, 1) of half t
   uint64_t joined;                // a phase per head of the share
+  uint64_t drained;
   uint32_t tmem;
   // -lse [0] and the scale of the codes [1] of rows, which all lanes read at once: of a head's
   // rows, by heads & 1 (score_joins), or of the 32 rows that a warp has at hand
@@ -618,6 +623,7 @@ __global__ void __launch_bounds__(kScoreBound, 1)
       mbar_init(&bars->q_empty[i], 1);
     }
     mbar_init(&bars->joined, 8);
+    mbar_init(&bars->drained, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_free[i], 4);
@@ -667,6 +673,7 @@ __global__ void __launch_bounds__(kScoreBound, 1)
                         F8 ? 0 : c * 64, 0, k.h, qt * p.s.per_tile, &bars->q_full[qb]);
         }
       }
+      drain_copies(bars->q_full, f, v.err);
     }
   } else if (warp == kWarpMMA) {
     {
@@ -719,6 +726,7 @@ __global__ void __launch_bounds__(kScoreBound, 1)
           ++cnt[t];
         }
       }
+      drain_products(&bars->drained, v.err);
     }
   } else if (warp >= kWarpSoftmax && warp < kWarpCodes) {
     const int t = (warp - kWarpSoftmax) >> 2, quad = warp & 3, r = quad * 32 + lane;

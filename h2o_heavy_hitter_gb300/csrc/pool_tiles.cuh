@@ -83,6 +83,27 @@ static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int3
 __device__ __forceinline__ bool pool_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
   return mbar_try_wait(bar, parity) || wait_on(bar, parity, err);
 }
+// A role that filled slots of a ring of R `count` times in all, in order, waits for its copies
+// in flight before it leaves, whoever gave up: the CTA's shared memory may be another's then.
+// When nobody did, they are what the consumers wait for. One thread, or a whole warp. (Both out
+// of line: in line they cost the E4M3 kernels 3 us.)
+static __device__ __noinline__ void drain_ring(uint64_t* full, uint32_t ring, uint32_t count, int32_t* err) {
+  for (uint32_t i = count > ring ? count - ring : 0; i < count; ++i)
+    mbar_wait(&full[i % ring], (i / ring) & 1, err);
+}
+template <int R>
+__device__ __forceinline__ void drain_copies(uint64_t (&full)[R], uint32_t count, int32_t* err) {
+  drain_ring(full, R, count, err);
+}
+// The warp that issued products waits until none is left, before the CTA frees their TMEM.
+// `bar`: one phase of one arrival.
+static __device__ __noinline__ void drain_products(uint64_t* bar, int32_t* err) {
+  __syncwarp();
+  if (elect_one()) umma_commit(bar);
+  __syncwarp();
+  mbar_wait(bar, 0, err);
+  __syncwarp();
+}
 // The result is made warp-uniform (see warp_wait).
 __device__ __forceinline__ bool pool_warp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
   return __all_sync(0xffffffffu, pool_wait(bar, parity, err));
@@ -163,13 +184,14 @@ template <int D, bool ONCE, int R, typename Cursor>
 __device__ void produce_tma(const PoolView& v, const CUtensorMap* map, uint8_t* ring,
                             RingBars<R>& bars, Cursor c) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  for (uint32_t n = 0; c.step(); ++n) {
+  uint32_t n = 0;
+  for (; c.step(); ++n) {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
     const uint32_t st = n % R;
-    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
+    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) break;
     if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * D * 2);
     __syncwarp();
     if (lane < boxes) {
@@ -179,6 +201,7 @@ __device__ void produce_tma(const PoolView& v, const CUtensorMap* map, uint8_t* 
                        b * 64, row, &bars.full[st]);
     }
   }
+  drain_copies(bars.full, n, v.err);
 }
 
 // Four E4M3 codes to bf16, exactly (three significant bits more than a code has).
@@ -200,13 +223,14 @@ template <int D, bool ONCE, int R, typename Cursor>
 __device__ void produce_codes(const PoolView& v, const CUtensorMap* map, const float* scale,
                               uint8_t* ring, float* scales, RingBars<R>& bars, Cursor c) {
   const int lane = threadIdx.x & 31, per = TILE_KEYS >> v.shift;
-  for (uint32_t n = 0; c.step(); ++n) {
+  uint32_t n = 0;
+  for (; c.step(); ++n) {
     const int left = c.len - c.kt * TILE_KEYS, boxes = min(per, (left + v.page - 1) >> v.shift);
     const int row = lane < boxes
                         ? (checked_page(v, c.seq, c.kt * per + lane) * v.heads + c.h) << v.shift
                         : 0;
     const uint32_t st = n % R;
-    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) return;
+    if (n >= R && !pool_warp_wait(&bars.empty[st], ((n / R) - 1) & 1, v.err)) break;
     if (lane == 0) mbar_arrive_expect_tx(&bars.full[st], boxes * v.page * (D + 4));
     __syncwarp();
     if (lane < boxes) {
@@ -214,6 +238,7 @@ __device__ void produce_codes(const PoolView& v, const CUtensorMap* map, const f
       bulk_copy_g2s(scales + st * TILE_KEYS + (lane << v.shift), scale + row, v.page * 4, &bars.full[st]);
     }
   }
+  drain_copies(bars.full, n, v.err);
 }
 
 // E4M3 pool, NT threads: tiles of value codes (linear, S slots) to bf16 operands,

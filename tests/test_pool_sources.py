@@ -1,5 +1,5 @@
-"""Chained launches of the paged attention: what the sources have to hold, since a missing
-acquire shows in no result."""
+"""Launches and waits of the paged attention: what the sources have to hold, since a missing acquire,
+or a copy left in flight by a wait that gave up, shows in no result."""
 import re
 from pathlib import Path
 
@@ -62,3 +62,20 @@ def test_the_joining_kernel_reads_what_others_wrote_from_l2():
         at = tiles.index(name)
         assert form in tiles[at:tiles.index("}", at)], name
     assert "row_lse<32, L2>" in body and "record_ml(" not in body and "finish_block<D, beside>" in text
+
+
+def test_roles_wait_for_their_copies_and_products_before_they_leave():
+    """A wait that gives up anywhere in a CTA leaves no copy into its shared memory and no product
+    into its Tensor Memory in flight: nobody returns early, and every role that issues drains."""
+    tiles = (CSRC / "pool_tiles.cuh").read_text()
+    for name in ("produce_tma(", "produce_codes("):
+        body = tiles[tiles.index("__device__ void " + name):]
+        body = body[:body.index("\n}\n")]
+        assert "return" not in body and body.rstrip().endswith("drain_copies(bars.full, n, v.err);"), name
+    for source, names in (("pool_attend.cu", ["pool_rows_kernel"]),
+                          ("pool_prefix.cu", ["pool_prefix_kernel", "pool_prefix_score_kernel"])):
+        for name in names:
+            body = kernels(source)[name]
+            assert body.index("tma_load_4d(") < body.index("drain_copies(bars->q_full,"), name
+            assert body.rindex("umma_ss(") < body.index("drain_products(&bars->drained,") < body.index("tmem_dealloc("), name
+            assert "mbar_init(&bars->drained, 1)" in body, name
