@@ -142,18 +142,21 @@ struct Spread {
 };
 
 // ------------------------------------------------------------------ fork, copy
-// plan of an entry: {served, length, -, -}
-__global__ void __launch_bounds__(kPlanThreads)
+constexpr int kSlab = 1024;  // slots of a sequence that the copy takes in one go, at least
+
+// plan of an entry: {served, length, slabs (of kSlab) of the longest served entry, -}
+__global__ void __launch_bounds__(kPlanThreads, 1)
     fork_plan_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
                      const int32_t* __restrict__ dst, bool share, int32_t* fresh_all,
                      int fresh_stride, int32_t* plan_all) {
   __shared__ int s_list[kPlanThreads], s_src[kPlanThreads], s_len[kPlanThreads],
       s_first[kPlanThreads];
-  __shared__ int wsum[33];
+  __shared__ int wsum[33], longest;
   const PoolView v = at_layer(v0, blockIdx.x);
   int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.x) * fresh_stride;
   int32_t* plan = plan_all + static_cast<size_t>(blockIdx.x) * n * kPlanInts;
   const int i = threadIdx.x;
+  if (i == 0) longest = 0;
   grid_dependency_wait();
   grid_launch_dependents();
   int to = list_entry(v, dst, n, s_list);
@@ -182,10 +185,12 @@ __global__ void __launch_bounds__(kPlanThreads)
   s_src[i] = from;
   s_len[i] = len;
   s_first[i] = first;
+  if (to >= 0) atomicMax(&longest, len);
   __syncthreads();  // every length has been read
   if (i < n) {
     plan[i * kPlanInts] = to >= 0;
     plan[i * kPlanInts + 1] = len;
+    plan[i * kPlanInts + 2] = (longest + kSlab - 1) / kSlab;
   }
   if (to >= 0) {
     v.meta[2 * to] = len;
@@ -248,35 +253,55 @@ __device__ __forceinline__ void copy_slots(const PoolView& v, int to, int from, 
   }
 }
 
-// LANES threads per (entry, head, slab of kSlab slots): the slab's scores, and the
-// tokens of its pages that were not shared. A head's slots of a page are
-// contiguous, so a partial page is one run of bytes per head. Bound by the writes: 56
-// forks of 8 prompts of 200 tokens, 48 layers of 56 heads, 1.1 GB in 207 us, each
-// source read from HBM once. (Stores that leave L2 first made that 250 us.)
-constexpr int kSlab = 1024;
-
+// LANES threads copy the slots [lo, hi) of an entry's head: their scores, and the tokens
+// of their pages that were not shared. A head's slots of a page are contiguous, so a
+// partial page is one run of bytes per head.
 template <int LANES>
-__global__ void __launch_bounds__(256)
-    fork_copy_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
-                     const int32_t* __restrict__ dst, bool share,
-                     const int32_t* plan_all) {
-  const PoolView v = at_layer(v0, blockIdx.z);
-  const int32_t* plan = plan_all + static_cast<size_t>(blockIdx.z) * n * kPlanInts;
-  const int lane = threadIdx.x % LANES;
-  const int task = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-  const int e = task / v.heads, head = task % v.heads;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (e >= n || !plan[e * kPlanInts]) return;
-  const int len = plan[e * kPlanInts + 1], lo = blockIdx.y * kSlab, hi = min(len, lo + kSlab);
-  if (lo >= hi) return;
-  const int from = src[e], to = dst[e];
+__device__ __forceinline__ void copy_slab(const PoolView& v, int from, int to, int head, int len, int lo,
+                                          int hi, bool share, int lane) {
   copy_values<LANES>(v.score + (static_cast<size_t>(to) * v.heads + head) * v.cap + lo,
                      v.score + (static_cast<size_t>(from) * v.heads + head) * v.cap + lo, hi - lo, lane);
   const int first = share ? max(lo >> v.shift, len >> v.shift) : lo >> v.shift;
   for (int j = first; j << v.shift < hi; ++j) {
     const int a = held_page(v, from, j), b = held_page(v, to, j);
     if (a >= 0 && b >= 0) copy_slots<LANES>(v, b, a, head, min(v.page, len - (j << v.shift)), lane);
+  }
+}
+
+// A warp per slab where the slabs that there are fill the GPU, else a block: 32 heads x 4
+// entries of some 50 tokens take 7.6 us by blocks, 19.4 us by warps; 128 heads x 32768
+// tokens (4096 slabs of kSlab) 33 us by blocks of 256 slots, 16 us by warps. The lengths
+// decide, not what the sequences could hold.
+constexpr int kManySlabs = 4096;
+
+// LANES threads per unit (entry, head) and slab of `slab` slots: 32 where the units alone
+// are many, else 256, one block or eight warps to the slab. Bound by HBM's writes and by a
+// warp's loads behind one another: 56 forks of 8 prompts of 200 tokens, 48 layers of
+// 56 heads, 1.1 GB in 207 us, each source read from HBM once. (Stores that leave L2 first
+// made that 250 us; a loop over slabs of one size, with its registers, 225 us.)
+template <int LANES>
+__global__ void __launch_bounds__(256)
+    fork_copy_kernel(PoolView v0, int n, const int32_t* __restrict__ src,
+                     const int32_t* __restrict__ dst, bool share, int slab,
+                     const int32_t* plan_all) {
+  const PoolView v = at_layer(v0, blockIdx.z);
+  const int32_t* plan = plan_all + static_cast<size_t>(blockIdx.z) * n * kPlanInts;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit = LANES == 32 ? blockIdx.x * 8 + warp : blockIdx.x;
+  const int e = unit / v.heads, head = unit % v.heads;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (e >= n || !plan[e * kPlanInts]) return;
+  const int len = plan[e * kPlanInts + 1], lo = blockIdx.y * slab;
+  if (lo >= len) return;
+  const int from = src[e], to = dst[e];
+  if (LANES == 32) {
+    copy_slab<32>(v, from, to, head, len, lo, min(len, lo + slab), share, lane);
+  } else if (static_cast<int64_t>(gridDim.x) * gridDim.z * plan[2] >= kManySlabs) {
+    const int part = lo + warp * (slab / 8);  // whole pages
+    if (part < len) copy_slab<32>(v, from, to, head, len, part, min(len, part + slab / 8), share, lane);
+  } else {
+    copy_slab<256>(v, from, to, head, len, lo, min(len, lo + slab), share, threadIdx.x);
   }
 }
 
@@ -704,15 +729,17 @@ cudaError_t pool_fork(const PoolView& v, int layers, int n, const int32_t* src, 
   cudaError_t e = launch_after(fork_plan_kernel, dim3(layers), kPlanThreads, 0, stream, v, n, src, dst,
                                share, fresh, share ? n : n * v.width, plan);
   if (e != cudaSuccess) return e;
-  // a warp per task where the tasks fill the GPU, else a block: 32 heads x 4
-  // entries of some 50 tokens take 7.6 us by blocks, 19.4 us by warps; scores of
-  // 128 heads x 32768 tokens (4096 tasks) 33 us by blocks of 256 slots, 18 us by warps
-  const int tasks = n * v.heads, slabs = (v.cap + kSlab - 1) / kSlab;
-  const bool many = static_cast<long>(tasks) * slabs * layers >= 4096;
-  const int per_block = many ? 8 : 1;
-  const dim3 grid((tasks + per_block - 1) / per_block, slabs, layers);
-  return launch_after(many ? fork_copy_kernel<32> : fork_copy_kernel<256>, grid, 256, 0, stream, v, n,
-                      src, dst, share, static_cast<const int32_t*>(plan));
+  // slabs of kSlab slots, or longer ones where those of full sequences would be more than some 4
+  // blocks an SM (32 where each has pages to copy): most of what the sequences could hold may be
+  // empty, and a pool 40 times as wide as its contents then took 271 us for 202. (4 against 12
+  // and 24: 4 beams in a pool of 32768 tokens a sequence 9.9, 10.0, 11.5 us, 4 full ones 15.6, 16.1, 16.9)
+  const int units = n * v.heads, most = (share ? 4 : 32) * num_sms();
+  const bool many = static_cast<int64_t>(units) * layers >= kManySlabs;
+  const int x = many ? (units + 7) / 8 : units, slabs = (v.cap + kSlab - 1) / kSlab;
+  const int y = static_cast<int>(std::min<int64_t>(slabs, 1 + most / (static_cast<int64_t>(x) * layers)));
+  const int slab = (slabs + y - 1) / y * kSlab;
+  return launch_after(many ? fork_copy_kernel<32> : fork_copy_kernel<256>, dim3(x, y, layers), 256, 0,
+                      stream, v, n, src, dst, share, slab, static_cast<const int32_t*>(plan));
 }
 
 cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
