@@ -148,8 +148,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---- packed fp32 pairs (sm_100+ f32x2 instructions) ---------------------------
-// Two fp32 values in one 64-bit register, element 0 in the low half. fma and
-// add round each element exactly as the scalar instructions do.
+// Two fp32 values in one 64-bit register, element 0 in the low half. fma, add
+// and mul round each element exactly as the scalar instructions do.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
@@ -166,6 +166,11 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 // max(a, b, c) in one instruction (sm_100+).

@@ -328,10 +328,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       const int rows = w.rows(t), step = w.two ? 2 : 1;
       const bool active = quad * 32 < rows;  // warp-uniform
       const int chunks = w.two ? 2 : 1, col0 = w.two ? 0 : 64 * t;
-      float m = -INFINITY, l = 0.f, qscale = p.qscale;
-      if (F8 && r < rows) {  // the row's codes have a scale
+      // bf16: of all logits, in the exponent's product; E4M3: of the row's codes, in the key's scale
+      // (their product stays in range where a key's times the sum of codes need not)
+      float m = -INFINITY, l = 0.f, rscale = p.qscale;
+      const float qscale = F8 ? 1.f : p.qscale;
+      if (F8 && r < rows) {
         const int entry = (2 * w.b + (w.two ? t : 0)) * p.s.per_tile + r / p.s.group;
-        qscale *= p.w.qfac[(static_cast<size_t>(entry) * p.s.heads + w.h) * p.s.group + r % p.s.group];
+        rscale *= p.w.qfac[(static_cast<size_t>(entry) * p.s.heads + w.h) * p.s.group + r % p.s.group];
       }
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++g) {
         const uint32_t jj = j0 + (kt - w.kt0) * step, j = w.two ? jj + t : jj;
@@ -350,9 +353,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        const float4* ks = reinterpret_cast<const float4*>(kscales + g % RK * TILE_KEYS);
+        const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(kscales + g % RK * TILE_KEYS);
+        const uint64_t rs = f2_pack(rscale, rscale);
         const float4* vs = reinterpret_cast<const float4*>(vscales + g % kScaleTiles * TILE_KEYS);
-        // 64 logits from column `first`, unscaled by 1 / sqrt(d); those behind the end -inf
+        // 64 logits from column `first`, (bf16) unscaled by 1 / sqrt(d); those behind the end -inf
         auto load = [&](uint32_t (&s)[64], int first) {
           tmem_ld32(s_tm + first, s);
           tmem_ld32(s_tm + first + 32, s + 32);
@@ -360,11 +364,17 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           if (F8) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-              const float4 k4 = ks[first / 4 + x];
-              s[4 * x] = __float_as_uint(__uint_as_float(s[4 * x]) * k4.x);
-              s[4 * x + 1] = __float_as_uint(__uint_as_float(s[4 * x + 1]) * k4.y);
-              s[4 * x + 2] = __float_as_uint(__uint_as_float(s[4 * x + 2]) * k4.z);
-              s[4 * x + 3] = __float_as_uint(__uint_as_float(s[4 * x + 3]) * k4.w);
+              const ulonglong2 k4 = ks[first / 4 + x];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int i = 4 * x + 2 * y;
+                float a, b;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                 f2_mul(y ? k4.y : k4.x, rs)),
+                          a, b);
+                s[i] = __float_as_uint(a);
+                s[i + 1] = __float_as_uint(b);
+              }
             }
           }
           if (first + 64 > valid) {

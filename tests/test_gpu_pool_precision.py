@@ -152,3 +152,19 @@ def test_what_lies_behind_the_last_token_reaches_neither_outputs_nor_scores(batc
     q64, q = bf16(rng.standard_normal((batch, heads * group, d)))
     attend_and_compare(b, batch, heads, group, batch, q64, q)
     b.close()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("exponent", [-118, -100, 100])
+@pytest.mark.parametrize("batch,heads,group,prefix,own", [PATHS[1], PATHS[4], PATHS[6], PATHS[8], PATHS[10]])
+def test_queries_and_keys_of_opposite_magnitudes(batch, heads, group, prefix, own, exponent, kv):
+    """Queries of 2^exponent and keys of 2^-exponent have ordinary logits, whichever product of
+    theirs with a scale comes first."""
+    d = 64
+    rng = np.random.default_rng(group)
+    K = lambda n, T: rng.standard_normal((n, heads, T, d)) * 2.0 ** -exponent
+    V = lambda n, T: rng.standard_normal((n, heads, T, d))
+    b = filled(batch, heads, prefix, own, d, kv, K, V)
+    q64 = rng.standard_normal((batch, heads * group, d)) * 2.0 ** exponent
+    attend_and_compare(b, batch, heads, group, batch if prefix else -1, *bf16(q64))
+    b.close()
