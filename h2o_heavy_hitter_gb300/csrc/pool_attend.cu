@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 // scaled by a power of two to a magnitude in [128, 256); the first code has the
 // upper four of a bf16 value's eight significant bits, the second what is left,
 // down to steps of 2^-9: no more than 2^-17 of the row's largest value is lost in
-// any value. A row with an infinity or a NaN gets a NaN for its factor. A warp
+// any value (2^-136 where the largest is below 2^-119: the power of two ends at 2^126,
+// whose reciprocal fp32 still holds in full). A row with an infinity or a NaN gets a NaN for its factor. A warp
 // per row.
 template <int D>
 __global__ void __launch_bounds__(256)

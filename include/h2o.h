@@ -406,7 +406,8 @@ int h2o_sync_check(h2o_ctx* ctx);
  * (C = W * page tokens) and H key/value heads, a pool holds
  *   K, V   bf16  [N][H][page][d]  stored keys / values (E4M3 codes, uint8, in
  *                                 an H2O_KV_FP8 pool, quantised as h2o_create_ex
- *                                 describes, with fp32 [N][H][page] scales each)
+ *                                 describes but for the two cases below, with
+ *                                 fp32 [N][H][page] scales each)
  *   pos    int32 [N][H][page]     position of the token a slot holds
  *   score  fp32  [S][H][C]        accumulated score of each slot of a sequence
  *   table  int32 [S][W]           pages of a sequence in order, -1 behind the last
@@ -417,6 +418,9 @@ int h2o_sync_check(h2o_ctx* ctx);
  * Scores belong to the sequence, keys, values and positions to the page. Whole
  * pages may be shared and are never written again; the partial last page of a
  * sequence is its own. Slots behind a sequence's last token hold no result.
+ * An H2O_KV_FP8 pool stores a vector of magnitude up to 2^-119, whose 448 / amax
+ * fp32 does not hold, as a zero vector, and one with a NaN or an infinity as zero
+ * codes with a NaN for their scale: it reads as NaN in every channel.
  *
  * Lists. `seqs`, `src` and `dst` are device int32 [n], read on the device, n <=
  * H2O_POOL_MAX_LIST; entries of -1 are skipped (a padded batch). An index
@@ -519,7 +523,10 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  * sqrt(d)) over both token lists, out = sum_j p_j v_j (bf16, rounded once from
  * an fp32 sum; p_j, in an H2O_KV_FP8 pool times v_j's scale, enters it with 16
  * significant bits, as two bf16 terms), lse = the natural log of the softmax's
- * normaliser (fp32; may be NULL).
+ * normaliser (fp32; may be NULL). An H2O_KV_FP8 pool takes a query's values as two
+ * E4M3 codes each: what is lost of a value is at most 2^-17 of the largest value of
+ * its row, or 2^-136. Sums of p_j v_j are kept in units of the largest p_j so far,
+ * up to 2^8: values beyond 2^120 divided by the number of tokens can leave fp32.
  * With accumulate, every probability is added to its slot's accumulated score:
  * to the sequence's for its own tokens (summed over the head's query group), to
  * the prefix's, summed over group and batch, for the prefix: the statistic by
