@@ -129,15 +129,15 @@ class Pool:
 
     def fork(self, src, dst, share=True):
         dst = self._list(dst)
-        lens, todo = self.meta[:, 0].copy(), []
+        meta, todo = self.meta.copy(), []
         for a, b in zip(src, dst):
             a = int(a)
             if b < 0 or a == -1:
                 continue
-            if not 0 <= a < len(lens) or lens[b] != 0:
+            if not 0 <= a < len(meta) or meta[b, 0] != 0:
                 self.errors |= BAD_LIST
                 continue
-            n = int(lens[a])
+            n = int(meta[a, 0])
             todo.append((a, b, n, int(n % self.page > 0) if share else self._need(n)))
         for a, b, n, need in todo[:self._serve([x[3] for x in todo])]:
             whole = n // self.page if share else 0
@@ -147,7 +147,7 @@ class Pool:
             for j in range(whole * self.page, n):
                 self._move(self.table[b, j // self.page], j % self.page,
                            self.table[a, j // self.page], j % self.page)
-            self.meta[b] = self.meta[a]
+            self.meta[b] = meta[a]
             self.score[b, :, :n] = self.score[a, :, :n]
 
     def free(self, seqs):

@@ -212,3 +212,13 @@ def test_a_fork_costs_what_its_sequences_hold_not_what_they_could():
         h2o.h2o_pool_sync_check(pool)
         pool.close()
     assert min(times[1]) <= 1.15 * min(times[0]), times
+
+
+@pytest.mark.parametrize("share", [True, False])
+def test_a_source_that_the_same_call_fills_is_empty(share):
+    b = Both(pages=12, page=16, heads=2, d=64, sequences=5, max_pages=4)
+    b.write([0], 40)
+    b.fork([0, 1, 2, 0], [1, 2, 3, 4], share)
+    assert b.view["meta"][:, 0].tolist() == [40, 40, 0, 0, 40]
+    b.check()
+    b.close()
