@@ -12,8 +12,9 @@
 //   tile runs under the softmax of this one. P is two bf16 terms (pool_attend.cu), side
 //   by side in the columns that S held. Bound by HBM up to some 128 rows,
 //   beyond by the exponentials and the products of 256 rows a tile: 512 rows a
-//   head, 8 heads, 32768 keys take 94 us with the joining (730 TFLOP/s). At 1024
-//   keys a CTA has two tiles, and 17 us are its start and the read-out.
+//   head, 8 heads, 32768 keys take 97 us with the joining (706 TFLOP/s, the products
+//   with the second terms not counted). At 1024 keys a CTA has two tiles, and 17 us are
+//   its start and the read-out.
 // pool_prefix_score_kernel: the prefix's scores once the pieces are there: S^T = K
 //   Q^T again, a thread per key, p = 2^(s - lse) summed over all rows in order. It
 //   reads K once more (2 d bytes a key and head); keeping the logits of more than
@@ -599,8 +600,8 @@ __device__ __noinline__ float joined_row(const AttendParams& p, int qt, int r, i
 }
 
 // Fewer registers than THREADS threads could have (112 at most), so that three blocks of
-// the finish kernel fit beside a CTA: grouped E4M3 heads 75.9 us a call, with 162 registers
-// 84.4, with 80 and spills 77.9.
+// the finish kernel fit beside a CTA: grouped E4M3 heads 75.9 us a call (when P was one
+// term), with 162 registers 84.4, with 80 and spills 77.9.
 constexpr int kScoreBound = 576;
 
 // The row tiles of a head stay in shared memory when there are at most two; more

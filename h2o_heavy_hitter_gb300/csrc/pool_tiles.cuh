@@ -21,9 +21,10 @@ constexpr int kFewRows = 32;  // query rows of a head that the few-rows kernel t
 struct Shape {
   int n, heads, group, d;
   // The prefix has at most kFewRows query rows per head. Narrow against wide rows, us a
-  // call: 16 rows x 32 heads over 32768 keys 128 against 166, 24 rows 145 against 168; 32
-  // rows 183 against 170 there, 60 against 63 as 8 heads of groups of 4, 39 against 52
-  // as 8 heads of groups of 8 over 8192 keys and 1000 own tokens each.
+  // call (E4M3): 16 rows x 32 heads over 32768 keys 129 against 169 (151 against 187), 24
+  // rows 164 against 173 (198, 192), 32 rows 211 against 173 (250, 196) there; but 43 against
+  // 50 (52, 55) as 8 heads of groups of 4 and 43 against 54 (50, 62) as 8 heads of groups of
+  // 8 over 8192 keys and 1000 own tokens each. The lengths, which would decide, are on the device.
   bool few;
   int per_tile;  // sequences whose query groups share a tile of rows of the prefix
   int nq;        // row tiles per head
