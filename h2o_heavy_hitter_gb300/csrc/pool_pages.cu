@@ -496,8 +496,8 @@ constexpr int kDigit = 11;              // bits of a radix step: 3 steps
 // the block's barriers between them, not by the row's 4 bytes a token.
 constexpr int kHists = 4;
 
-// Blocks (head, entry, layer) select; the block with head == heads of entry 0
-// plans its layer: plan of an entry = {first fresh page or -1, -, -, -}. The
+// Blocks (head, entry, layer) select; the block behind the last head of entry 0
+// plans its layer (alone in the grid where no sequence can be longer than h + r): plan of an entry = {first fresh page or -1, -, -, -}. The
 // selection reads lengths and scores only and the plan writes neither, so the
 // two run side by side. where[]: slot (page * page size + offset) of each kept
 // token, ascending; kept[]: its score. The h-th largest key is found by an
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   __shared__ int wsum[33];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x == static_cast<unsigned>(v.heads)) {
+  if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y) return;
     __shared__ int s_list[kPlanThreads];
     int32_t* fresh = fresh_all + static_cast<size_t>(blockIdx.z) * fresh_stride;
@@ -774,14 +774,15 @@ cudaError_t pool_compact(const PoolView& v, int layers, int n, const int32_t* se
   if (n == 0) return cudaSuccess;
   const int stride = n * ((k + v.page - 1) >> v.shift);
   // the keys of a row in shared memory, where rows can be that long
-  const int held = std::min(v.cap, kSelectKeys);
+  const bool any = k < v.cap;  // else no sequence can be longer than h + r, and the list is checked alone
+  const int held = any ? std::min(v.cap, kSelectKeys) : 0;
   static int opted_in[kMaxDevices] = {};
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(compact_select_kernel),
                                    kSelectKeys * sizeof(unsigned), opted_in);
   if (e != cudaSuccess) return e;
-  e = launch_after(compact_select_kernel, dim3(v.heads + 1, n, layers), kSelectThreads,
+  e = launch_after(compact_select_kernel, any ? dim3(v.heads + 1, n, layers) : dim3(1, 1, layers), kSelectThreads,
                    held * sizeof(unsigned), stream, v, n, seqs, h, r, fresh, stride, plan, where, kept, held);
-  if (e != cudaSuccess || k >= v.cap) return e;  // (no sequence can be longer than h + r)
+  if (e != cudaSuccess || !any) return e;
   const int slots = 8 * gather_slots(v.row_bytes);  // per block
   const dim3 grid(n * v.heads, (k + slots - 1) / slots, layers);
   auto kern = v.row_bytes == 256 ? compact_gather_kernel<256>
