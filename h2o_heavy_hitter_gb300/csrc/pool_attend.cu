@@ -36,15 +36,14 @@
 // their own, and their scales go into P. Bound by the work on a tile, not by its
 // bytes: 64 sequences of up to 1000 tokens, 8 heads, 4 query heads each: 74 MB in 39 us.
 //
-// The second product takes P as two bf16 terms, p rounded and what is left of it
-// rounded: 16 significant bits, with an exponent that reaches as far as fp32's (a
-// value's scale is in it). Logits, sums and accumulators are fp32. (One term, 8
-// bits, was the largest error of an output before its own rounding. The second costs
-// the rows kernel next to nothing up to 16 rows and 15 % at 32, a prefix of 512
-// rows over 32768 keys 73 -> 92 us, the E4M3 case below 76 -> 81 us in all.)
-// What lies behind a sequence's end in its last page is
-// not trusted: its probabilities are set to zero, and its values in shared
-// memory too, since 0 times a NaN is not 0.
+// The second product takes P as two bf16 terms (split_bits): 16 significant bits,
+// with an exponent that reaches as far as fp32's (a value's scale is in it). Logits,
+// sums and accumulators are fp32. (One term, 8 bits, was the largest error of an
+// output before its own rounding. The second costs the rows kernel next to nothing
+// up to 16 rows and 15 % at 32, a prefix of 512 rows over 32768 keys 73 -> 92 us, the
+// grouped E4M3 case above 76 -> 82 us in all.) What lies behind a sequence's
+// end in its last page is not trusted: its probabilities are set to zero, and its
+// values in shared memory too, since 0 times a NaN is not 0.
 #include <algorithm>
 
 #include "device_state.h"
@@ -63,8 +62,9 @@ struct List {
 // Fills the list: skipped and refused entries have seq -1 and no tiles. An entry
 // is refused for an index outside the pool, the prefix's, or one named before;
 // repeats are looked for one by one only where a hashed bit says that there may
-// be some, or where the list is a later part of the caller's. Every CTA begins with this, so it takes few barriers. Blockwide;
-// `bits`: 4 KB; `report`: this block sets the error word.
+// be some, or where the list is a later part of the caller's. Every CTA begins with
+// this, so it takes few barriers. Blockwide; `bits`: 4 KB; `report`: this block sets
+// the error word.
 __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int* wsum,
                            bool report) {
   const PoolView& v = a.v;
@@ -348,10 +348,9 @@ __device__ __forceinline__ bool tile_softmax(const TileRows& a, float& m, float&
       // K-major, 128-byte swizzle: 16-byte chunk (key / 8) of a row at chunk ^ (row & 7)
       const int row = r0 + i;
       uint8_t* at = a.p + row * 128 + ((a.chunk ^ (row & 7)) << 4);
-      const float x = a.live ? pr[i] * a.vs : 0.f;
-      const __nv_bfloat16 first = __float2bfloat16(x);
-      *reinterpret_cast<__nv_bfloat16*>(at) = first;
-      *reinterpret_cast<__nv_bfloat16*>(at + a.second) = __float2bfloat16(x - __bfloat162float(first));
+      const uint32_t x = a.live ? split_bits<F8>(pr[i] * a.vs) : 0u;
+      *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(x >> 16);
+      *reinterpret_cast<__nv_bfloat16*>(at + a.second) = __float2bfloat16(__uint_as_float(x) - split_first(x));
     }
     const float x = __shfl_sync(0xffffffffu, warp_sums<CH>(pr, lane), (lane - r0) & 31);
     if (lane >= r0 && lane < r0 + CH) sum = x;
@@ -744,8 +743,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
 // upper four of a bf16 value's eight significant bits, the second what is left,
 // down to steps of 2^-9: no more than 2^-17 of the row's largest value is lost in
 // any value (2^-136 where the largest is below 2^-119: the power of two ends at 2^126,
-// whose reciprocal fp32 still holds in full). A row with an infinity or a NaN gets a NaN for its factor. A warp
-// per row.
+// whose reciprocal fp32 still holds in full). A row with an infinity or a NaN gets a
+// NaN for its factor. A warp per row.
 template <int D>
 __global__ void __launch_bounds__(256)
     pool_split_queries_kernel(const __nv_bfloat16* __restrict__ q, int rows, uint8_t* q8, float* qfac) {
@@ -849,8 +848,8 @@ __device__ void prefix_scores(const AttendParams& p, int block, float* s_lse) {
     const int i = i0 + (threadIdx.x >> 3), b = min(i, rows - 1) / p.s.group;
     const int cum[3] = {p.w.cum[b], p.w.cum[b + 1], p.w.cum[p.s.n]};
     float first;
-    const float x = row_lse<8, false>(p, records_of<8>(p, b, h, plen, cum, lane), min(i, rows - 1) - b * p.s.group,
-                               lane, first);
+    const float x = row_lse<8, false>(p, records_of<8>(p, b, h, plen, cum, lane),
+                                      min(i, rows - 1) - b * p.s.group, lane, first);
     // +inf: not counted, whatever its logits are
     if (lane == 0 && i < rows) s_lse[i] = p.w.seq[b] < 0 ? INFINITY : x;
   }

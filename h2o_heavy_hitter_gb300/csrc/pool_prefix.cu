@@ -429,9 +429,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
                   p0 *= v2.x;
                   p1 *= v2.y;
                 }
-                pk[x] = pack_bf16x2(p0, p1);
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(pk[x] << 16), __uint_as_float(pk[x] & 0xffff0000u)),
-                                 minus, f2_pack(p0, p1)),
+                const uint32_t b0 = split_bits<F8>(p0), b1 = split_bits<F8>(p1);
+                pk[x] = __byte_perm(b0, b1, 0x7632);
+                f2_unpack(f2_fma(f2_pack(split_first(b0), split_first(b1)), minus,
+                                 f2_pack(__uint_as_float(b0), __uint_as_float(b1))),
                           p0, p1);
                 pk2[x] = pack_bf16x2(p0, p1);
               }

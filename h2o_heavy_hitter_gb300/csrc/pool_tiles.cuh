@@ -242,6 +242,16 @@ __device__ void produce_codes(const PoolView& v, const CUtensorMap* map, const f
   drain_copies(bars.full, n, v.err);
 }
 
+// The two bf16 terms of a probability: its upper 16 bits as they are, and what is left, rounded
+// (the terms' sum is off by 2^-16 of p at most). For bf16 values the lowest bit is set first, so
+// that the second term of a p that has a first one is above zero: an infinite value stays one in
+// both products, where 0 would make a NaN of it. (Codes have no infinity.)
+template <bool F8>
+__device__ __forceinline__ uint32_t split_bits(float p) {
+  return __float_as_uint(p) | (F8 ? 0u : 1u);
+}
+__device__ __forceinline__ float split_first(uint32_t bits) { return __uint_as_float(bits & 0xffff0000u); }
+
 // E4M3 pool, NT threads: tiles of value codes (linear, S slots) to bf16 operands,
 // and their scales to out_scales [kScaleTiles][128] by tile; rows behind the last
 // token become zero. Each warp arrives once on a slot's barriers. (Codes loaded

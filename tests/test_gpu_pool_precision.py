@@ -168,3 +168,29 @@ def test_queries_and_keys_of_opposite_magnitudes(batch, heads, group, prefix, ow
     q64 = rng.standard_normal((batch, heads * group, d)) * 2.0 ** exponent
     attend_and_compare(b, batch, heads, group, batch if prefix else -1, *bf16(q64))
     b.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch,heads,group,prefix,own", PATHS)
+def test_an_infinite_value_gives_an_infinite_output(batch, heads, group, prefix, own, d):
+    """An infinity in a value that is attended to is one in its channel, of its sign, and nowhere
+    else: no term of a probability makes a NaN of it."""
+    rng = np.random.default_rng(group)
+    K = lambda n, T: rng.standard_normal((n, heads, T, d)) * 0.3
+
+    def V(n, T):
+        v = rng.standard_normal((n, heads, T, d))
+        if T == own:
+            v[:, :, T // 2, 3] = np.inf
+        if T == (prefix or own):
+            v[:, :, T - 1, 5] = -np.inf
+        return v
+
+    b = filled(batch, heads, prefix, own, d, "bf16", K, V)
+    _, q = bf16(rng.standard_normal((batch, heads * group, d)))
+    out, lse = b.h2o.h2o_pool_attend(b.pool, 0, ints(range(batch)), q, prefix=batch if prefix else -1)
+    b.h2o.h2o_pool_sync_check(b.pool)
+    assert out[..., 3].eq(float("inf")).all() and out[..., 5].eq(float("-inf")).all()
+    out[..., [3, 5]] = 0
+    assert out.isfinite().all() and lse.isfinite().all()
+    b.close()
