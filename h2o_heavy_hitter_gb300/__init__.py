@@ -568,6 +568,11 @@ def _ptr(pool: H2OPool, t, dtype: torch.dtype, shape: tuple, name: str) -> int:
     return _dev_ptr(t, dtype, shape, name)
 
 
+def _laid_out(t):
+    """t, or a contiguous copy of it, made on the current stream."""
+    return t.contiguous() if isinstance(t, torch.Tensor) and not t.is_contiguous() else t
+
+
 def _list_ptr(pool: H2OPool, seqs, name: str = "seqs") -> tuple[int, int]:
     """Address and length of a sequence list."""
     if not isinstance(seqs, torch.Tensor):
@@ -705,14 +710,16 @@ def h2o_pool_attend(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, out=No
 def h2o_pool_attend_tree(pool: H2OPool, layer: int, seqs, q, prefix: int = -1, lens=None, parent=None, out=None,
                          lse=None):
     """Attention of the last lens[i] (CUDA int32 [n]; default T) tokens of each sequence, a tree of
-    drafts: q bf16 [n, T, q_heads, d], T <= 64, over sequence ``prefix`` (-1: none), the sequence's
-    tokens before the drafts, the nodes that a node hangs below (``parent``: CUDA int32 [n, T], -1:
-    none; default: the one before it) and itself. Returns (out bf16 like q, lse fp32
-    [n, T, q_heads]); rows behind lens[i] and those of -1 entries are not written."""
+    drafts: q bf16 [n, T, q_heads, d], T <= 64 (copied where it is not contiguous), over sequence
+    ``prefix`` (-1: none), the sequence's tokens before the drafts, the nodes that a node hangs below
+    (``parent``: CUDA int32 [n, T], -1: none; default: the one before it) and itself. Returns (out
+    bf16 like q, contiguous, and lse fp32 [n, T, q_heads]); rows behind lens[i] and those of -1
+    entries are not written."""
     ps, n = _list_ptr(pool, seqs)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a tensor [n, T, q_heads, head_dim]")
     shape = (n, q.shape[1], q.shape[2], pool.head_dim)
+    q = _laid_out(q)
     pq = _ptr(pool, q, torch.bfloat16, shape, "q")
     pn = None if lens is None else _ptr(pool, lens, torch.int32, shape[:1], "lens")
     pp = None if parent is None else _ptr(pool, parent, torch.int32, shape[:2], "parent")
@@ -736,8 +743,8 @@ def h2o_pool_accept(pool: H2OPool, layer: int, seqs, nodes: int, path=None, lens
     """Keeps the drafts that ``path`` names (CUDA int32 [n, P]: ascending nodes, -1 behind the last;
     default: none) of the last lens[i] (CUDA int32 [n]; default ``nodes``) tokens of each sequence,
     and drops the others (layer -1, without q: in every layer). With ``q`` [n, nodes, q_heads, d] and
-    ``lse`` [n, nodes, q_heads] of h2o_pool_attend_tree (and its ``prefix``), the probabilities of
-    the kept rows are added to the accumulated scores."""
+    ``lse`` [n, nodes, q_heads] of h2o_pool_attend_tree (and its ``prefix``; each copied where it is
+    not contiguous), the probabilities of the kept rows are added to the accumulated scores."""
     ps, n = _list_ptr(pool, seqs)
     pn = None if lens is None else _ptr(pool, lens, torch.int32, (n,), "lens")
     P, pp = 0, None
@@ -751,6 +758,7 @@ def h2o_pool_accept(pool: H2OPool, layer: int, seqs, nodes: int, path=None, lens
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("q must be a tensor [n, nodes, q_heads, head_dim], with lse")
         heads = q.shape[2]
+        q, lse = _laid_out(q), _laid_out(lse)
         pq = _ptr(pool, q, torch.bfloat16, (n, nodes, heads, pool.head_dim), "q") or None
         pl = _ptr(pool, lse, torch.float32, (n, nodes, heads), "lse") or None
     _check(load_library().h2o_pool_accept(pool.handle, layer, n, ps, nodes, pn, pp, P, pq, heads, pl, prefix))
