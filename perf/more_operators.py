@@ -267,8 +267,7 @@ def prepare(case, seed):
     state["pool"] = arrays
     if op == "accept":
         _stage(state)
-        lse = torch.where(node < state["lens"][:, None], 0, math.nan)[:, :, None] + _log_sums(state)
-        state["lse"] = lse.contiguous()
+        state["lse"] = torch.where(node < state["lens"][:, None], 0, math.nan)[:, :, None] + _log_sums(state)
         _free(arrays, state["dst"])
     if own:
         import h2o_heavy_hitter_gb300 as h2o
