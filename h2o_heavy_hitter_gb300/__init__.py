@@ -629,8 +629,8 @@ def h2o_pool_append(pool: H2OPool, layer: int, seqs, q, k, v, rotary=None, lens=
     """Appends a projection's keys and values bf16 k, v [n, T, heads, d] (any strides, contiguous
     channels) to sequences, normed and rotated at the positions that they take; returns the queries
     q [n, T, q_heads, d] (or None), normed and rotated too, bf16 and contiguous. lens: CUDA int32
-    [n], the first lens[i] tokens of entry i (default T); rows of the result behind them are not
-    written. ``parent`` (CUDA int32 [n, T], T <= 64): the tokens are drafts, each below an earlier
+    [n], the first lens[i] tokens of entry i (default T); rows of the result behind them, and those
+    of entries that get no pages, which the calls behind this one pass over, are not written. ``parent`` (CUDA int32 [n, T], T <= 64): the tokens are drafts, each below an earlier
     one or (-1) below the sequence's last, for h2o_pool_attend_tree and h2o_pool_accept."""
     ps, n = _list_ptr(pool, seqs)
     x, n2, T, hq, hk, d = _qkv(q, k, v, q_norm, k_norm, eps, pool.device)

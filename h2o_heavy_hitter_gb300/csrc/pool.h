@@ -21,12 +21,17 @@ struct PoolView {
   int32_t* table;   // [layers][seqs][width] pages of a sequence, -1 behind the last
   int32_t* meta;    // [layers][seqs][2] {length, next position}
   int32_t* ref;     // [layers][pages] sequences that hold a page
+  int32_t* refused; // [layers][seqs] kRefused bits of a sequence's last write or append
   int32_t* err;     // device error word
   int pages, seqs, width, heads, d;
   int page, shift;  // tokens per page = 1 << shift
   int cap;          // width * page, the longest sequence
   int row_bytes;    // bytes of one stored key or value vector
 };
+
+// A sequence's tokens of its last write or append were refused: its last tokens are no drafts, and
+// (kRefusedQueries) there are no queries either. Only a call that is served, or ends the round, takes these away.
+constexpr int kRefused = 1, kRefusedQueries = 2;
 
 constexpr int kPoolMaxList = 1024;  // longest list of sequences of one call: one thread each
 // 448 / amax overflows below 448 / FLT_MAX (just above 2^-120): such vectors are stored as zero.
@@ -52,9 +57,9 @@ cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void
                        int32_t* plan, cudaStream_t stream);
 
 // The plan of a write alone: pages, lengths and (unless the tokens are drafts) next positions; plan of an
-// entry = {tokens to write (0: none), first slot, next position before, -}.
+// entry = {tokens to write (0: none), first slot, next position before, -}. mark: kRefused bits of what is refused.
 cudaError_t pool_write_plan(const PoolView& v, int n, const int32_t* seqs, int T, const int32_t* lens,
-                            bool drafts, int32_t* fresh, int32_t* plan, cudaStream_t stream);
+                            bool drafts, int mark, int32_t* fresh, int32_t* plan, cudaStream_t stream);
 
 // Keeps the r last tokens and the h others of largest (score, slot) of every
 // head of each sequence longer than h + r. fresh: n * ceil(k / page) per layer;

@@ -46,6 +46,7 @@ h2o::PoolView layer_view(const h2o_pool* p, int layer) {
   v.table += l * v.seqs * v.width;
   v.meta += l * v.seqs * 2;
   v.ref += l * v.pages;
+  v.refused += l * v.seqs;
   return v;
 }
 
@@ -142,7 +143,8 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
   const size_t table = align_up(L * sequences * max_pages * 4, 256);
   const size_t meta = align_up(L * sequences * 8, 256);
   const size_t ref = align_up(L * pages * 4, 256);
-  const size_t total = 2 * kv + per_slot + 2 * scale + score + table + meta + ref + 256;
+  const size_t refused = align_up(L * sequences * 4, 256);
+  const size_t total = 2 * kv + per_slot + 2 * scale + score + table + meta + ref + refused + 256;
   cudaStream_t s = nullptr;
   try {
     s = current_stream();
@@ -166,6 +168,7 @@ int h2o_pool_create(int layers, int pages, int page_size, int heads, int head_di
   v.score = reinterpret_cast<float*>(take(score));
   v.meta = reinterpret_cast<int32_t*>(take(meta));
   v.ref = reinterpret_cast<int32_t*>(take(ref));
+  v.refused = reinterpret_cast<int32_t*>(take(refused));
   v.err = reinterpret_cast<int32_t*>(take(256));
   // everything above starts at zero, the two below at -1
   const size_t zeros = static_cast<size_t>(at - static_cast<uint8_t*>(p->base));

@@ -77,7 +77,9 @@ __device__ void build_list(const AttendArgs& a, List& list, uint32_t* bits, int*
       if (report) atomicOr(v.err, kErrBadList);
       s = -1;
     }
+    const int refused = s >= 0 ? __ldcg(v.refused + s) : 0;
     list.len[b] = s >= 0 ? checked_length(v, s, report) : -1;
+    if (refused & kRefusedQueries) list.len[b] = -1;  // its row of the queries was not written
     list.seq[b] = s;
   }
   for (int i = tid; i < 1024; i += nt) bits[i] = 0;

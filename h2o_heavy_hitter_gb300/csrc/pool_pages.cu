@@ -41,6 +41,7 @@ __device__ __forceinline__ PoolView at_layer(PoolView v, int layer) {
   v.table += static_cast<size_t>(v.seqs) * v.width * layer;
   v.meta += static_cast<size_t>(v.seqs) * 2 * layer;
   v.ref += static_cast<size_t>(v.pages) * layer;
+  v.refused += static_cast<size_t>(v.seqs) * layer;
   return v;
 }
 
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (to >= 0) {
     v.meta[2 * to] = len;
     v.meta[2 * to + 1] = next;
+    v.refused[to] = 0;
   }
   const Spread w(n);
   for (int e = w.first; e < n; e += w.step) {
@@ -318,7 +320,10 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();  // every thread has compared the list
   s_list[threadIdx.x] = seq;
   s_len[threadIdx.x] = len;
-  if (seq >= 0) *reinterpret_cast<int2*>(v.meta + 2 * seq) = make_int2(0, 0);
+  if (seq >= 0) {
+    *reinterpret_cast<int2*>(v.meta + 2 * seq) = make_int2(0, 0);
+    v.refused[seq] = 0;
+  }
   __syncthreads();
   const Spread w(n);
   for (int e = w.first; e < n; e += w.step) {
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // plan of an entry: {tokens to write (0: none), first slot, first position, -}
 __global__ void __launch_bounds__(kPlanThreads)
     write_plan_kernel(PoolView v, int n, const int32_t* __restrict__ seqs, int T,
-                      const int32_t* __restrict__ lens, bool drafts, int32_t* fresh, int32_t* plan) {
+                      const int32_t* __restrict__ lens, bool drafts, int mark, int32_t* fresh,
+                      int32_t* plan) {
   __shared__ int s_list[kPlanThreads], s_len[kPlanThreads], s_new[kPlanThreads],
       s_first[kPlanThreads];
   __shared__ int wsum[33];
@@ -347,6 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   grid_launch_dependents();
   int seq = list_entry(v, seqs, n, s_list);
   __syncthreads();
+  const int named = seq;
   int len = 0, next = 0, t = 0;
   if (seq >= 0) {
     t = lens ? lens[i] : T;
@@ -388,6 +395,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     plan[i * kPlanInts + 1] = len;
     plan[i * kPlanInts + 2] = next;
   }
+  if (named >= 0) v.refused[named] = seq < 0 && t > 0 ? mark : 0;
   if (seq >= 0) {
     v.meta[2 * seq] = len + t;
     if (!drafts) v.meta[2 * seq + 1] = next + t;
@@ -500,15 +508,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   }
   int nodes = 0, len = 0, count = 0;
   if (seq >= 0) {
+    const int refused = v.refused[seq];
     nodes = lens ? lens[i] : T;
-    if (nodes < 0 || nodes > T) {
+    len = seq_length(v, seq);
+    if (refused) {  // there are no drafts: the round ends here for this entry
+      v.refused[seq] = 0;
+      seq = -1;
+    } else if (nodes < 0 || nodes > T) {
       atomicOr(v.err, kErrBadLength);
       nodes = nodes < 0 ? 0 : T;
     }
-    len = seq_length(v, seq);
     if (len < 0) {
       seq = -1;
-    } else if (nodes > len) {
+    } else if (seq >= 0 && nodes > len) {
       atomicOr(v.err, kErrBadLength);
       seq = -1;
     }
@@ -907,8 +919,8 @@ cudaError_t pool_free(const PoolView& v, int layers, int n, const int32_t* seqs,
 }
 
 cudaError_t pool_write_plan(const PoolView& v, int n, const int32_t* seqs, int T, const int32_t* lens,
-                            bool drafts, int32_t* fresh, int32_t* plan, cudaStream_t stream) {
-  return launch_after(write_plan_kernel, dim3(1), kPlanThreads, 0, stream, v, n, seqs, T, lens, drafts, fresh,
+                            bool drafts, int mark, int32_t* fresh, int32_t* plan, cudaStream_t stream) {
+  return launch_after(write_plan_kernel, dim3(1), kPlanThreads, 0, stream, v, n, seqs, T, lens, drafts, mark, fresh,
                       plan);
 }
 
@@ -916,7 +928,7 @@ cudaError_t pool_write(const PoolView& v, int n, const int32_t* seqs, const void
                        int T, const int32_t* lens, const float* score, int32_t* fresh,
                        int32_t* plan, cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
-  cudaError_t e = pool_write_plan(v, n, seqs, T, lens, false, fresh, plan, stream);
+  cudaError_t e = pool_write_plan(v, n, seqs, T, lens, false, kRefused, fresh, plan, stream);
   if (e != cudaSuccess || T == 0) return e;
   int span = 0;
   while (1 << span < kWriteTokens && 1 << span < T) ++span;

@@ -41,13 +41,14 @@ __device__ __forceinline__ TreeEntry tree_entry(const AttendParams& p, int b, in
     e.seq = -1;
     return e;
   }
+  const int refused = __ldcg(v.refused + e.seq);  // (its last tokens are no drafts)
   int nodes = p.t.lens ? p.t.lens[b] : p.t.T;
+  e.len = checked_length(v, e.seq, report);
+  if (e.len < 0 || refused) return e;
   if (nodes < 0 || nodes > p.t.T) {
     if (report) atomicOr(v.err, kErrBadLength);
     nodes = nodes < 0 ? 0 : p.t.T;
   }
-  e.len = checked_length(v, e.seq, report);
-  if (e.len < 0) return e;
   if (nodes > e.len) {  // more drafts than tokens
     if (report) atomicOr(v.err, kErrBadLength);
     return e;

@@ -307,7 +307,9 @@ cudaError_t rotate_qkv(const RotateArgs& a, cudaStream_t stream) { return rotate
 cudaError_t pool_append(const PoolView& v, const RotateArgs& a, const int32_t* seqs, const int32_t* lens,
                         const int32_t* parent, int32_t* fresh, int32_t* plan, cudaStream_t stream) {
   if (a.n == 0) return cudaSuccess;
-  cudaError_t e = pool_write_plan(v, a.n, seqs, a.T, lens, parent != nullptr, fresh, plan, stream);
+  // (rows of queries that belong to no written token stay as they were)
+  const int mark = kRefused | (a.heads[0] ? kRefusedQueries : 0);
+  cudaError_t e = pool_write_plan(v, a.n, seqs, a.T, lens, parent != nullptr, mark, fresh, plan, stream);
   if (e != cudaSuccess || a.T == 0) return e;
   const Pages p{v, seqs, plan, parent};
   return v.kscale ? rotate<kPagesF8>(a, p, stream) : rotate<kPagesBf16>(a, p, stream);

@@ -575,6 +575,13 @@ int h2o_pool_write(h2o_pool* pool, int layer, int n, const int32_t* seqs, const 
  * than the next position, which stays until h2o_pool_accept. With parent NULL the tokens
  * follow each other and the next position moves on. Drafts are to be accepted or dropped
  * before the sequence is written, forked, copied, compacted or attended to otherwise.
+ *
+ * A round goes on without a look at the error word: while the last tokens that were to
+ * be written to a sequence, by this call or by h2o_pool_write, were refused,
+ * h2o_pool_attend_tree and h2o_pool_accept pass over its entries as over -1 (what it
+ * holds is no drafts), and, where this call had queries, so does h2o_pool_attend (their
+ * rows were not written). It ends, layer by layer, with a write or append that is
+ * served, a fork or copy into the sequence, h2o_pool_free or h2o_pool_accept.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
 int h2o_pool_append(h2o_pool* pool, int layer, int n, const int32_t* seqs, const h2o_qkv* x,
@@ -631,7 +638,8 @@ int h2o_pool_compact(h2o_pool* pool, int layer, int n, const int32_t* seqs, int 
  * the prefix's, summed over group and batch, for the prefix: the statistic by
  * which h2o_pool_compact can compact the prefix for all. Sums run in a fixed
  * order: equal calls give equal bits. Without any token out is 0 and lse is
- * -infinity. Rows of skipped entries keep what they held.
+ * -infinity. Rows of skipped entries keep what they held, as do those of entries whose
+ * queries h2o_pool_append did not write.
  *
  * q: device bf16 [n][q_heads][d]; out: device bf16 [n][q_heads][d]; lse: device
  * fp32 [n][q_heads]; q and out 16-byte aligned; the three must not overlap.
@@ -658,8 +666,9 @@ int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int p
  * before it, the next tokens of a prompt for instance. q, out: device bf16
  * [n][T][q_heads][d], 16-byte aligned; lse: device fp32 [n][T][q_heads], may be NULL; the
  * three must not overlap. Rows t >= lens[i] and those of skipped entries keep what they
- * held. A length outside [0, T] is clamped, and one beyond the sequence's skips the
- * entry; both set bit 4. 0 <= T <= H2O_POOL_MAX_NODES, n * T * q_heads < 2^31.
+ * held; so do those of entries whose tokens were refused (h2o_pool_append). A length
+ * outside [0, T] is clamped, and one beyond the sequence's skips the entry; both set bit 4.
+ * 0 <= T <= H2O_POOL_MAX_NODES, n * T * q_heads < 2^31.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
 int h2o_pool_attend_tree(h2o_pool* pool, int layer, int n, const int32_t* seqs, int prefix,
@@ -677,7 +686,8 @@ int h2o_pool_attend_tree(h2o_pool* pool, int layer, int n, const int32_t* seqs, 
  * sequence's alone (they are, unless it was forked while it held drafts): else the entry
  * is refused, unchanged, with bit 2. A path that does not ascend or names no draft, and a
  * sequence that is `prefix`, set bit 16, and the entry is refused, unchanged; lengths as for
- * h2o_pool_attend_tree.
+ * h2o_pool_attend_tree. An entry whose tokens were refused (h2o_pool_append) is passed over,
+ * once.
  *
  * With q, device bf16 [n][T][q_heads][d], 16-byte aligned, and lse, device fp32
  * [n][T][q_heads], as h2o_pool_attend_tree took and gave them, the probabilities of the

@@ -12,6 +12,44 @@ from .kv_pool import BAD_LENGTH, BAD_LIST, BAD_STATE, NO_PAGE, Pool, quantise
 
 
 class DraftPool(Pool):
+    """refused: by sequence, REFUSED where its last write or append was not served, QUERIES too where
+    that was an append with queries."""
+
+    REFUSED, QUERIES = 1, 2
+
+    def __init__(self, pages, page, heads, d, sequences, max_pages, fp8=False):
+        super().__init__(pages, page, heads, d, sequences, max_pages, fp8)
+        self.refused = np.zeros(sequences, np.int32)
+
+    def _mark(self, seqs, T, lens, before, mark):
+        """Entries whose tokens did not come have `mark`, the others none."""
+        errors = self.errors
+        for i, s in enumerate(self._list(seqs)):
+            if s >= 0:
+                t = self._lens(T, lens, i)
+                self.refused[s] = mark if t > 0 and self.meta[s, 0] == before[s] else 0
+        self.errors = errors
+
+    def write(self, seqs, K, V, lens=None, score=None):
+        before = self.meta[:, 0].copy()
+        super().write(seqs, K, V, lens, score)
+        self._mark(seqs, K.shape[2], lens, before, self.REFUSED)
+
+    def fork(self, src, dst, share=True):
+        before = self.meta[:, 0].copy()
+        super().fork(src, dst, share)
+        for a, b in zip(src, dst):
+            if 0 <= b < len(before) and 0 <= a < len(before) and before[b] == 0 and self.meta[b, 0] == before[a]:
+                self.refused[b] = 0
+
+    def free(self, seqs):
+        super().free(seqs)
+        self.refused[[s for s in seqs if 0 <= s < len(self.refused)]] = 0
+
+    def attend(self, seqs, q, prefix=-1, accumulate=True):
+        seqs = [-1 if s >= 0 and self.refused[s] & self.QUERIES else s for s in self._list(seqs)]
+        return super().attend(seqs, q, prefix, accumulate)
+
     def _lens(self, T, lens, i):
         t = T if lens is None else int(lens[i])
         if not 0 <= t <= T:
@@ -19,10 +57,10 @@ class DraftPool(Pool):
             t = min(max(t, 0), T)
         return t
 
-    def append(self, seqs, T, lens, parent, make):
+    def append(self, seqs, T, lens, parent, make, queries=True):
         """make(i, positions) gives keys and values float64 [heads, tokens, d] of entry i before they are
         stored. Returns {entry: positions}."""
-        todo, got = [], {}
+        todo, got, before = [], {}, self.meta[:, 0].copy()
         for i, s in enumerate(self._list(seqs)):
             if s < 0:
                 continue
@@ -53,6 +91,7 @@ class DraftPool(Pool):
             self.pos[p, :, o] = got[i][:, None]
             self.score[s, :, have:have + t] = 0
             self.meta[s] += (t, 0 if parent is not None else t)
+        self._mark(seqs, T, lens, before, self.REFUSED | (self.QUERIES if queries else 0))
         return got
 
     def _at(self, seq, slots):
@@ -74,6 +113,8 @@ class DraftPool(Pool):
                 continue
             if s == prefix:
                 self.errors |= BAD_LIST
+                continue
+            if self.refused[s]:
                 continue
             nodes, length = self._lens(T, lens, i), int(self.meta[s, 0])
             if nodes > length:
@@ -104,6 +145,9 @@ class DraftPool(Pool):
                 continue
             if s == prefix and q is not None:
                 self.errors |= BAD_LIST
+                continue
+            if self.refused[s]:
+                self.refused[s] = 0
                 continue
             nodes, length = self._lens(T, lens, i), int(self.meta[s, 0])
             if nodes > length:
