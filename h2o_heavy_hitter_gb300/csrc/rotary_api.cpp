@@ -20,6 +20,38 @@ constexpr double kPi = 3.14159265358979323846;
 
 bool rotated_channels(int dim) { return dim >= 0 && dim % 16 == 0 && dim <= 2 * H2O_ROTARY_MAX_PAIRS; }
 
+// f / (2 pi) without whole turns, in units of 2^-64 of a turn, rounded once; |f| <= 2^53. A long division in
+// binary: f = m 2^e is brought down bit by bit, what is left of it by 2 pi kept in units of 2^-120. Those are
+// 2^-121 radians off for every whole turn taken, less than 2^-9 of a unit in all at 2^53; what of f lies
+// below them is dropped.
+constexpr double kMostRadians = 0x1p53;
+uint64_t fraction_of_a_turn(double f) {
+  using u128 = unsigned __int128;
+  constexpr u128 kTwoPi = (static_cast<u128>(0x06487ed5110b4611ull) << 64) | 0xa62633145c06e0e7ull;  // 2 pi 2^120
+  constexpr u128 kOne = static_cast<u128>(1) << 120;
+  int e;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(std::fabs(f), &e), 53));
+  e -= 53;  // |f| = m 2^e
+  u128 r = 0;
+  for (int x = e + 52; x >= 0; --x) {  // the whole radians, from the top: r = 2 r + bit, by 2 pi
+    r = 2 * r + (x >= e && (m >> (x - e) & 1) ? kOne : 0);
+    while (r >= kTwoPi) r -= kTwoPi;
+  }
+  if (e < 0) {  // and what is left below one
+    const uint64_t rest = e > -64 ? m & ((uint64_t{1} << -e) - 1) : m;
+    r += 120 + e >= 0 ? static_cast<u128>(rest) << (120 + e) : -(120 + e) < 64 ? static_cast<u128>(rest >> -(120 + e)) : 0;
+    if (r >= kTwoPi) r -= kTwoPi;
+  }
+  uint64_t turns = 0;
+  for (int i = 0; i < 64; ++i) {
+    r *= 2;
+    turns = 2 * turns + (r >= kTwoPi);
+    if (r >= kTwoPi) r -= kTwoPi;
+  }
+  turns += 2 * r >= kTwoPi;  // (up to a whole turn, which is none)
+  return f < 0 ? 0 - turns : turns;
+}
+
 // Bytes from the first to behind the last channel of a view.
 size_t extent(const RotateArgs& a, int i) {
   if (!a.heads[i] || !a.n || !a.T) return 0;
@@ -135,16 +167,13 @@ int h2o_rotary_init(h2o_rotary* out, int dim, int layout, const double* frequenc
   if (dim && !frequencies) return fail(H2O_EINVAL, "null frequencies");
   if (!std::isfinite(static_cast<float>(factor))) return fail(H2O_EINVAL, "factor must be finite");
   for (int i = 0; i < dim / 2; ++i)
-    if (!std::isfinite(frequencies[i])) return fail(H2O_EINVAL, "frequencies must be finite");
+    if (!(std::fabs(frequencies[i]) <= kMostRadians))
+      return fail(H2O_EINVAL, "frequencies must be finite and at most 2^53 radians a position");
   *out = h2o_rotary{};
   out->dim = dim;
   out->layout = layout;
   out->factor = static_cast<float>(factor);
-  for (int i = 0; i < dim / 2; ++i) {
-    // whole turns are left out; what rounds up to one (a tiny negative frequency) is none
-    const double t = frequencies[i] / (2 * kPi), part = std::ldexp(t - std::floor(t), 64);
-    out->turns[i] = part < 0x1p64 ? static_cast<uint64_t>(part) : 0;
-  }
+  for (int i = 0; i < dim / 2; ++i) out->turns[i] = fraction_of_a_turn(frequencies[i]);
   return H2O_OK;
 }
 

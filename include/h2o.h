@@ -406,8 +406,8 @@ int h2o_sync_check(h2o_ctx* ctx);
  * The first `dim` channels of a head are dim / 2 pairs: channels (i, i + dim / 2)
  * with H2O_ROTARY_HALF, (2 i, 2 i + 1) with H2O_ROTARY_INTERLEAVED. At position p
  * pair i becomes factor * (x cos a - y sin a, x sin a + y cos a) with a = p f_i; other
- * channels stay. Angles are exact for every 32-bit p up to the rounding of f_i to
- * 2^-64 of a turn and of a to fp32 (2 pi 2^-26).
+ * channels stay. Angles are exact for every 32-bit p and the f_i that are given, as fp64,
+ * up to the rounding of f_i to 2^-64 of a turn and of a to fp32 (2 pi 2^-26).
  */
 #define H2O_ROTARY_HALF 0
 #define H2O_ROTARY_INTERLEAVED 1
@@ -434,9 +434,10 @@ typedef struct h2o_rotary {
 
 /*
  * h2o_rotary_frequencies - dim / 2 frequencies in radians a position, host memory.
- * dim a multiple of 16 in [16, 128]; what a scaling does not name is ignored.
- * h2o_rotary_init - the rotation by given frequencies (host memory; any finite
- * values; NULL with dim = 0, which rotates nothing). No GPU work. Errors: H2O_EINVAL.
+ * dim a multiple of 16 in [16, 128]; what a scaling does not name is ignored. (Powers
+ * and products in fp64: relative errors of some 2^-49, which times p are the angle's.)
+ * h2o_rotary_init - the rotation by given frequencies (host memory; any values of
+ * magnitude up to 2^53; NULL with dim = 0, which rotates nothing). No GPU work. Errors: H2O_EINVAL.
  */
 int h2o_rotary_frequencies(int dim, double base, int scaling, double factor, double original,
                            double low, double high, double* frequencies);
