@@ -16,6 +16,7 @@ namespace h2o {
 namespace host {
 namespace {
 
+constexpr int64_t kMostElements = int64_t{1} << 60;
 constexpr double kPi = 3.14159265358979323846;
 
 bool rotated_channels(int dim) { return dim >= 0 && dim % 16 == 0 && dim <= 2 * H2O_ROTARY_MAX_PAIRS; }
@@ -90,9 +91,11 @@ int rotate_args(const h2o_qkv* x, const h2o_rotary* r, int n, int T, void* const
     const int sizes[3] = {n, T, heads};
     int64_t* const mine[3] = {&a.batch[i], &a.token[i], &a.head[i]};
     for (int k = 0; k < 3; ++k) {
-      // (2^31 entries of 2^24 channels, the most that can be asked for, stay inside 64 bits)
       if (sizes[k] > 1 && (strides[k] < 0 || strides[k] % 8 || strides[k] > (int64_t{1} << 30) * x->head_dim))
         return fail(H2O_EINVAL, "strides of " + name + " must be multiples of 8 in [0, 2^30 head_dim]");
+      // (the bytes of three dimensions then stay inside 63 bits)
+      if (sizes[k] > 1 && strides[k] > kMostElements / (sizes[k] - 1))
+        return fail(H2O_EINVAL, "strides of " + name + " reach beyond 2^60 elements");
       *mine[k] = sizes[k] > 1 ? strides[k] : 0;
     }
   }

@@ -443,8 +443,8 @@ int h2o_rotary_frequencies(int dim, double base, int scaling, double factor, dou
                            double low, double high, double* frequencies);
 int h2o_rotary_init(h2o_rotary* out, int dim, int layout, const double* frequencies, double factor);
 
-/* bf16 [batch][T][heads][d], 16-byte aligned: strides in elements, >= 0 and multiples of 8 (of sizes above
- * 1); channels are contiguous. data NULL: not there. */
+/* bf16 [batch][T][heads][d], 16-byte aligned: strides in elements, multiples of 8 in [0, 2^30 d] that
+ * reach no further than 2^60 elements (of sizes above 1); channels are contiguous. data NULL: not there. */
 typedef struct h2o_heads {
   const void* data;
   int64_t batch, token, head;
