@@ -662,6 +662,7 @@ int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int p
  * sequence's tokens before the nodes, to the nodes that node t hangs below and to itself;
  * else as h2o_pool_attend, without scores (h2o_pool_accept adds those of the rows that
  * were kept). Keys and values of other nodes, whatever they are, do not reach a row.
+ * The prefix is read for every sequence: it costs as much as tokens of their own would.
  *
  * parent: device int32 [n][T] as for h2o_pool_append; NULL: each node hangs below the one
  * before it, the next tokens of a prompt for instance. q, out: device bf16
@@ -669,7 +670,8 @@ int h2o_pool_attend(h2o_pool* pool, int layer, int n, const int32_t* seqs, int p
  * three must not overlap. Rows t >= lens[i] and those of skipped entries keep what they
  * held; so do those of entries whose tokens were refused (h2o_pool_append). A length
  * outside [0, T] is clamped, and one beyond the sequence's skips the entry; both set bit 4.
- * 0 <= T <= H2O_POOL_MAX_NODES, n * T * q_heads < 2^31.
+ * 0 <= T <= H2O_POOL_MAX_NODES, n * T * q_heads < 2^31. Scratch: some 2^11 (d + 2) bytes an
+ * SM (40 MB on 152 with d = 128), and 2 d + 4 more a row of q in an H2O_KV_FP8 pool.
  * Errors: H2O_EINVAL, H2O_ENOMEM, H2O_ECUDA.
  */
 int h2o_pool_attend_tree(h2o_pool* pool, int layer, int n, const int32_t* seqs, int prefix,
