@@ -17,7 +17,7 @@
 //
 // Measured in a graph, with the fork, the drafts' write and the other kernels of accept: four
 // documents of 32768 tokens, 32 heads of bf16 (1.07 GB) 211 us; 64 sequences of up to 2000
-// tokens, 8 heads of E4M3 (85 MB) 63 us (calls back to back 73), under a prefix of 8197 168 (rows
+// tokens, 8 heads of E4M3 (85 MB) 65 us (calls back to back 73), under a prefix of 8197 168 (rows
 // staged when they are needed: 64.5 and 270). Before: one chain of products for a row's sum, and the mask
 // tested at every logit 66.5; keys loaded straight into registers, four blocks an SM, 216
 // and 72; 32 keys a warp 248; a lane's own 64-byte pieces of rows through the ring 217 and
@@ -49,6 +49,24 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes times 2^-11 to bf16, exactly (the smallest code is then 2^-20, and halves go down to
+// 2^-24). A sum of d codes up to 448 times a query beyond 2^112 would leave fp32 although the logit, with
+// the key's scale, does not; so the sum stays inside up to 2^123, where a key of 2^-119, the least that is
+// stored, has logits of some 128. The key's scale is multiplied by 2^11 instead, at the softmax's factor: by 2^8.6
+// at most, which the largest, 2^119.2, bears. (The batch of E4M3 below
+// 63.6 -> 64.7 us; codes moved into bf16's places by bits, and one product, 67.)
+constexpr float kCodeScale = 0x1p11f;
+__device__ __forceinline__ uint2 small_codes(uint32_t w) {
+  uint2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+    const float2 f = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&hr), __float2half2_rn(1.f / kCodeScale)));
+    (i ? r.y : r.x) = pack_bf16x2(f.x, f.y);
+  }
+  return r;
 }
 
 // Last i in [0, n) with cum[i] <= x.
@@ -197,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       for (int u = 0; u < 2; ++u) {
         const int r = 8 * u + g, at = i % kStages * kWarpKeys + 16 * m + r;
         sum[m][u] = 0.f;
-        ks[m][u] = F8 ? s_ks[at] * qscale : qscale;
+        ks[m][u] = F8 ? s_ks[at] * (kCodeScale * qscale) : qscale;
 #pragma unroll
         for (int y = 0; y < LD; ++y) {
           const uint4 raw = s_k[at * CK + ((4 * y + c) ^ (CK < 8 ? 0 : (r & 1) * 4))];
@@ -205,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             if constexpr (F8) {
-              const uint2 pair = e4m3x4_to_bf16(w[z]);
+              const uint2 pair = small_codes(w[z]);
               k[m][u][8 * y + 2 * z] = pair.x;
               k[m][u][8 * y + 2 * z + 1] = pair.y;
             } else {
