@@ -36,18 +36,22 @@ class DraftPool(Pool):
         self._mark(seqs, K.shape[2], lens, before, self.REFUSED)
 
     def fork(self, src, dst, share=True):
-        before = self.meta[:, 0].copy()
-        super().fork(src, dst, share)
-        for a, b in zip(src, dst):
-            if 0 <= b < len(before) and 0 <= a < len(before) and before[b] == 0 and self.meta[b, 0] == before[a]:
+        before, free, errors = self.meta[:, 0].copy(), int(np.sum(self.ref == 0)), self.errors
+        for a, b in zip(src, self._list(dst)):
+            if b >= 0 and 0 <= a < len(before) and before[b] == 0:
+                free -= int(before[a] % self.page > 0) if share else self._need(before[a])
+                if free < 0:
+                    break
                 self.refused[b] = 0
+        self.errors = errors
+        super().fork(src, dst, share)
 
     def free(self, seqs):
         super().free(seqs)
         self.refused[[s for s in seqs if 0 <= s < len(self.refused)]] = 0
 
     def attend(self, seqs, q, prefix=-1, accumulate=True):
-        seqs = [-1 if s >= 0 and self.refused[s] & self.QUERIES else s for s in self._list(seqs)]
+        seqs = [-1 if s >= 0 and s != prefix and self.refused[s] & self.QUERIES else s for s in self._list(seqs)]
         return super().attend(seqs, q, prefix, accumulate)
 
     def _lens(self, T, lens, i):
