@@ -32,25 +32,28 @@ struct TreeList {
   TreeEntry e[2];
 };
 
-__device__ __forceinline__ TreeEntry tree_entry(const AttendParams& p, int b, int ptiles, bool report) {
+// bad: what there is to report.
+__device__ __forceinline__ TreeEntry tree_entry(const AttendParams& p, int b, int ptiles, int* bad) {
   const PoolView& v = p.a.v;
   TreeEntry e{};
+  *bad = 0;
   e.seq = p.a.seqs[b];
   if (e.seq < 0 || e.seq >= v.seqs || e.seq == p.a.prefix) {
-    if (report && e.seq != -1) atomicOr(v.err, kErrBadList);
+    if (e.seq != -1) *bad = kErrBadList;
     e.seq = -1;
     return e;
   }
   const int refused = __ldcg(v.refused + e.seq);  // (its last tokens are no drafts)
   int nodes = p.t.lens ? p.t.lens[b] : p.t.T;
-  e.len = checked_length(v, e.seq, report);
+  e.len = checked_length(v, e.seq, false);
+  if (e.len < 0) *bad = kErrBadState;
   if (e.len < 0 || refused) return e;
   if (nodes < 0 || nodes > p.t.T) {
-    if (report) atomicOr(v.err, kErrBadLength);
+    *bad = kErrBadLength;
     nodes = nodes < 0 ? 0 : p.t.T;
   }
   if (nodes > e.len) {  // more drafts than tokens
-    if (report) atomicOr(v.err, kErrBadLength);
+    *bad = kErrBadLength;
     return e;
   }
   e.nodes = nodes;
@@ -81,9 +84,10 @@ __device__ __forceinline__ void tree_list(const AttendParams& p, int workers, in
   const int tid = threadIdx.x, nt = blockDim.x, n = p.t.n, lane = tid & 31, warp = tid >> 5;
   const int per = (n + nt - 1) / nt, b0 = tid * per;
   TreeEntry e[kTreePer];
+  int bad[kTreePer] = {};
 #pragma unroll
   for (int i = 0; i < kTreePer; ++i)
-    if (i < per && b0 + i < n) e[i] = tree_entry(p, b0 + i, ptiles, report);
+    if (i < per && b0 + i < n) e[i] = tree_entry(p, b0 + i, ptiles, &bad[i]);
   // entries named before: looked for one by one only where a hashed bit says that there may be some
   bool seen = false;
   if (n > 1) {
@@ -118,6 +122,7 @@ __device__ __forceinline__ void tree_list(const AttendParams& p, int workers, in
     const bool in = i < per && b < n && !((list.skip[b >> 5] >> (b & 31)) & 1u);
     weight[i] = in ? e[i].tiles * e[i].blocks : 0;
     mine += weight[i];
+    if (report && in && bad[i]) atomicOr(v.err, bad[i]);  // (not of one that was named before)
   }
   int at = mine;  // inclusive over the warp, then over the block
 #pragma unroll
@@ -188,7 +193,8 @@ static __device__ __noinline__ TreeEntry tree_next_entry(const AttendParams& p, 
                                                          int* found) {
   TreeEntry e;
   for (;; ++b) {
-    e = tree_entry(p, b, ptiles, false);
+    int reported;
+    e = tree_entry(p, b, ptiles, &reported);
     if (e.tiles && !((list.skip[b >> 5] >> (b & 31)) & 1u)) break;
   }
   *found = b;

@@ -224,3 +224,16 @@ def test_captured_rounds_pass_over_what_runs_out(kv):
     h2o.h2o_pool_sync_check(pools[1])
     for p in (*pools, spare):
         p.close()
+
+
+def test_an_entry_named_before_is_a_bad_list_alone():
+    """Whatever its number of drafts: longer than the sequence, or out of range."""
+    b = pool_of([20, 9], 9, 8, 16, "bf16")
+    q64, q = torch.zeros(3, 12, H * GROUP, D).double().numpy(), torch.zeros(3, 12, H * GROUP, D, dtype=torch.bfloat16, device="cuda")
+    b.tree([1, 0, 1], q64, q, lens=[4, 3, 12])
+    b.check(errors=16)
+    b.tree([1, 1, 7], q64, q, lens=[4, 13, -1])
+    b.check(errors=16)
+    b.accept([1, 1, 7], 12, [[0]] * 3, lens=[4, 13, -1])
+    b.check(errors=16)
+    b.close()
