@@ -54,9 +54,9 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
 // Four E4M3 codes times 2^-11 to bf16, exactly (the smallest code is then 2^-20, and halves go down to
 // 2^-24). A sum of d codes up to 448 times a query beyond 2^112 would leave fp32 although the logit, with
 // the key's scale, does not; so the sum stays inside up to 2^123, where a key of 2^-119, the least that is
-// stored, has logits of some 128. The key's scale is multiplied by 2^11 instead, at the softmax's factor: by 2^8.6
-// at most, which the largest, 2^119.2, bears. (The batch of E4M3 below
-// 63.6 -> 64.7 us; codes moved into bf16's places by bits, and one product, 67.)
+// stored, has logits of some 128. The key's scale is multiplied by 2^11 instead, with the softmax's factor by
+// 2^8.6 at most, which the largest, 2^119.2, bears. (The batch of E4M3 above 63.6 -> 64.7 us; codes moved
+// into bf16's places by bits, and one product, 67.)
 constexpr float kCodeScale = 0x1p11f;
 __device__ __forceinline__ uint2 small_codes(uint32_t w) {
   uint2 r;

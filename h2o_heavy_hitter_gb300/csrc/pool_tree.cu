@@ -7,8 +7,9 @@
 // E4M3), against 4 d flops a row, of which a head has nodes x group: HBM up to some 250 rows,
 // tensor cores beyond. A prefix is read, and multiplied with whole row tiles, for every sequence:
 // 64 sequences of 4 drafts, 8 heads of 128, over 32768 tokens take 985 us, where single tokens of
-// the same sequences, whose rows share the tiles, take 66. Units are 256 rows (two row tiles share a tile of keys and
-// values) or 128, where the CTA's two halves of softmax warps are workers of their own.
+// the same sequences, whose rows share the tiles, take 66. Units are 256 rows (two row tiles
+// share a tile of keys and values) or 128, where the CTA's two halves of softmax warps are
+// workers of their own.
 // A worker has an equal share of the tiles of all units; a unit that it has alone is
 // written out from its accumulators, the at most two others of a worker become pieces,
 // which the join kernel adds up by the records that the workers leave.

@@ -6,8 +6,8 @@
 // of the first `dim` channels becomes factor (x cos a - y sin a, x sin a + y cos a).
 // The angle of pair i at position p is 2 pi frac(p turns_i / 2^64): the product
 // wraps at whole turns, so it is exact for every p and the turns that there are (an fp32
-// product p f is off by 0.06 rad at p = 2^20). Everything between the loads and the stores is fp32, each
-// result rounded once.
+// product p f is off by 0.06 rad at p = 2^20). Everything between the loads and the
+// stores is fp32, each result rounded once.
 //
 // Bound by HBM, 4 bytes a channel: 32768 tokens of 3 x 32 heads of 128, 1.61 GB in 247
 // us (6.5 TB/s); 8168 tokens of 48 heads with norms, 0.20 GB in 37.5 us; 8 prompts of up
